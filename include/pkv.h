@@ -225,6 +225,94 @@ PKV_API int kv_absmax(const void* d_x, pkv_dtype dtype, int64_t n, float* d_amax
  * take as k_scale / v_scale.  PKV_EINVAL for a NULL pointer or n < 1. */
 PKV_API int kv_fp8_scale(const float* d_amax, int n, float* d_scale, cudaStream_t stream);
 
+/* ---------------------------------------------------------------- rotary positions */
+
+/* Rotary positions ([UNLOCK], RoPE extrapolation: position interpolation, NTK-aware
+ * scaling and YaRN): the pairs i < rotary_dim / 2 of a head's row at position p turn by the
+ * angle p * f_i,
+ *   (a, b) -> attn_scale * (a cos - b sin, a sin + b cos),
+ * with (a, b) = (x[i], x[i + rotary_dim / 2]) in the half layout and
+ * (x[2i], x[2i + 1]) in the interleaved one; elements from rotary_dim on are
+ * unchanged.  A frequency is held as the fraction of a full turn per position,
+ * in units of 2^-64 turns (uint64): p times it, modulo 2^64, is the angle reduced
+ * to one turn without rounding, so positions far out (up to 2^31 - 1) turn as
+ * exactly as the first ones. */
+typedef enum {
+  PKV_ROPE_NONE = 0,   /* f_i = base^(-2 i / r), r = rotary_dim */
+  PKV_ROPE_LINEAR = 1, /* position interpolation: f_i / factor */
+  PKV_ROPE_NTK = 2,    /* NTK-aware: base * factor^(r / (r - 2)) in base's place (r = 2: as NONE) */
+  PKV_ROPE_YARN = 3    /* with t_i = original_positions * f_i / (2 pi) turns over the training
+                          length and g_i = (t_i - beta_slow) / (beta_fast - beta_slow) limited
+                          to [0, 1]: f_i (g_i + (1 - g_i) / factor); attn_scale =
+                          0.1 ln(factor) + 1 */
+} pkv_rope_scaling;
+typedef struct {
+  int32_t rotary_dim; /* even, >= 2 */
+  int32_t scaling;    /* a pkv_rope_scaling */
+  double base;        /* > 0 */
+  double factor;      /* >= 1; unused by NONE */
+  double original_positions, beta_fast, beta_slow; /* YaRN: > 0, and beta_fast > beta_slow */
+} pkv_rope_config;
+/* The table of rotary_dim / 2 frequencies and the attention scale (1 except for
+ * YaRN) of a configuration, on the host; the caller uploads the table. */
+PKV_API int pkv_rope_freqs(const pkv_rope_config* config, uint64_t* h_freqs, float* h_attn_scale);
+/* The table of n frequencies given in radians per position (any finite values:
+ * scalings other than the ones above). */
+PKV_API int pkv_rope_freqs_from(const double* h_radians, int n, uint64_t* h_freqs);
+
+/* A rotation: the table on the device (rotary_dim / 2 values, 8-byte aligned), the
+ * layout (0 half, 1 interleaved) and the factor on rotated pairs (finite). */
+typedef struct {
+  const uint64_t* d_freqs;
+  int32_t rotary_dim, interleaved;
+  float attn_scale;
+} pkv_rope;
+/* Rows of a tensor [tokens, heads, head_dim] with unit stride along head_dim and
+ * any token and head strides (in elements), such as the q, k and v parts of one
+ * projection's output.  Output rows must not overlap one another. */
+typedef struct {
+  void* data;
+  int64_t token_stride, head_stride;
+} pkv_rows;
+
+/* Rotate num_tokens tokens' queries and keys: token t sits at d_positions[t].
+ * q [num_tokens, num_q_heads, head_dim] -> q_out, and k likewise with num_k_heads
+ * (0: no k).  q_out may be q (in place: same data and strides); another overlap of
+ * an input with an output gives undefined values.  A token with a negative
+ * position is padding: its output rows are left as they were.  backward = 1 turns
+ * by the opposite angle (attn_scale stays a factor): the gradient with respect to
+ * q and k of a loss whose gradients with respect to q_out and k_out are given as q
+ * and k.  dtype f32, f16 or bf16; angles, products and sums are fp32 with one
+ * rounding to dtype at the end.  head_dim <= 512, rotary_dim <= head_dim.
+ * Asynchronous on `stream`; PKV_EINVAL for NULL or misaligned pointers (to the
+ * element size), negative counts or strides, overlapping output rows or a bad
+ * rotation. */
+PKV_API int rope_apply(const pkv_rows* q_out, const pkv_rows* q, int num_q_heads,
+                       const pkv_rows* k_out, const pkv_rows* k, int num_k_heads, pkv_dtype dtype,
+                       int head_dim, const int32_t* d_positions, int64_t num_tokens,
+                       const pkv_rope* rope, int backward, cudaStream_t stream);
+
+/* rope_apply of q and k fused with kv_append_tokens: the rotated q goes to q_out
+ * (q and q_out NULL: keys and values only), the rotated k and the unchanged v into
+ * the pool slot of (d_seq_ids[t], or t when d_seq_ids is NULL, at d_positions[t]),
+ * in one launch and without a rotated k in memory.  in_dtype as in
+ * kv_append_tokens; k is rotated in fp32 and rounded once, to the pool's dtype, or
+ * for an E4M3 pool straight from fp32 as e4m3(rot(k) / k_scale) (the attached block
+ * scales in k_scale's place when there are any).  An E4M3 scale is chosen for the
+ * rotated keys: an element of a rotated pair can be sqrt(2) * attn_scale times as
+ * large as the pair's larger element.  A token with a negative position is
+ * skipped: its slot and its row of q_out are left as they were.  A sequence id, a
+ * position past the table or a block id out of range records PKV_EBOUNDS and skips
+ * the store; the token's q is still rotated.  Heads, head_dim and block size are
+ * the pool's; other arguments and errors as in kv_append_tokens and rope_apply,
+ * except that k and v have strides and need only their elements' alignment. */
+PKV_API int kv_append_rope(pkv_pool* pool, int layer, const pkv_rows* q_out, const pkv_rows* q,
+                           const pkv_rows* k, const pkv_rows* v, pkv_dtype in_dtype,
+                           const pkv_rope* rope, const int32_t* d_block_tables,
+                           int max_blocks_per_seq, int batch, const int32_t* d_seq_ids,
+                           const int32_t* d_positions, int64_t num_tokens, float k_scale,
+                           float v_scale, cudaStream_t stream);
+
 /* ---------------------------------------------------------------- decode attention */
 
 /* Workspace bytes paged_decode_attention needs on the current device for this
@@ -470,6 +558,51 @@ PKV_API int paged_decode_attention_static(void* d_out, pkv_dtype out_dtype, cons
                                           const int32_t* d_seq_lens, int batch, int max_seq_len,
                                           float scale, float k_scale, float v_scale,
                                           int num_splits, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- draft verification */
+
+/* Probabilities [batch, rows, vocab] with unit stride along vocab. */
+typedef struct {
+  const void* data;
+  int64_t seq_stride, row_stride; /* elements, >= 0 */
+} pkv_probs;
+
+/* Speculative verification of drafted tokens ([UNLOCK], speculative decoding): after
+ * paged_decode_attention_mq has given the target's probabilities p of the token
+ * after each of a sequence's last num_drafts + 1 tokens, keep the drafts the
+ * target agrees with and draw one more token, so that the kept tokens are
+ * distributed as the target's own.  Sequence s has n = d_num_drafts[s] drafts (NULL:
+ * max_drafts), x_j = d_drafts[s][j], drawn from the probabilities q_j (draft row j);
+ * target row j is p_j.  Draft j is accepted while u_j q_j(x_j) < p_j(x_j),
+ * u_j = d_u_accept[s][j]; with a the number accepted, the next token is the lowest i
+ * with w_0 + ... + w_i > u * (w_0 + ... + w_last), u = d_u_sample[s], where
+ *   w = p_n            if a = n (all accepted),
+ *   w = max(p_a - q_a, 0)  if a < n (draft a was refused).
+ * draft->data NULL: the drafts were not drawn (a lookup), q_j is 1 at x_j and 0
+ * elsewhere.  The products u q are exact and the sums are 64-bit fixed point
+ * (2^-56), so the result does not depend on the order of summation or on the
+ * launch.  A residual without mass (w all 0) falls back to w = p_a.
+ *   d_tokens       int32 [batch, max_drafts + 1]: the accepted drafts, the next
+ *                  token, then -1
+ *   d_num_accepted int32 [batch]: a
+ *   target         [batch, max_drafts + 1, vocab], draft [batch, max_drafts, vocab],
+ *                  both in dtype (f32, f16 or bf16); rows past n are never read
+ *   d_drafts       int32 [batch, max_drafts]; d_u_accept f32 of that shape and
+ *                  d_u_sample f32 [batch], uniform in [0, 1)
+ * NaN and negative probabilities count as 0, ones above 1 as 1, and a row's sum
+ * saturates at 64; a draft of p = 0 is refused; a NaN u refuses
+ * (u_accept) or counts as 0 (u_sample), a u_sample of 1 or more as the largest
+ * value below 1.  d_status: device int32 (zero: no error) that takes the first error,
+ * as a pool's status word does, or NULL.  A refused-by-range draft (an id outside
+ * [0, vocab)) counts as refused and records PKV_EBOUNDS, as does a d_num_drafts
+ * outside [0, max_drafts], which is limited to it; a row without any mass gives the
+ * next token -1 and records PKV_EINVAL.  Asynchronous on `stream`, no workspace;
+ * PKV_EINVAL for NULL pointers, negative sizes or strides, vocab < 1 or dtype. */
+PKV_API int verify_drafts(int32_t* d_tokens, int32_t* d_num_accepted, const pkv_probs* target,
+                          const pkv_probs* draft, pkv_dtype dtype, const int32_t* d_drafts,
+                          const int32_t* d_num_drafts, const float* d_u_accept,
+                          const float* d_u_sample, int batch, int max_drafts, int vocab,
+                          int32_t* d_status, cudaStream_t stream);
 
 /* ---------------------------------------------------------------- status */
 

@@ -118,6 +118,47 @@ cudaError_t launch_absmax(const void* x, int dtype, int64_t n, float* amax, cuda
 // scale = max(amax[0..n)) / 448 (1 when that is 0), one thread block.
 cudaError_t launch_fp8_scale(const float* amax, int n, float* scale, cudaStream_t stream);
 
+// Rotary positions, alone (pool == nullptr: k goes to ko) or with the store of k
+// and v into the pool.  Strides in elements.
+struct RopeArgs {
+  const void *q, *k, *v;
+  void *qo, *ko;
+  void* pool;
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, qo_ts, qo_hs, ko_ts, ko_hs;
+  const uint64_t* freqs;     // [rd / 2], 2^-64 turns per position
+  float m;                   // attention scale on cos and sin
+  float sign;                // -1: backward
+  int interleaved;
+  int copy_tail;             // 0: in place, elements from rd on need no copy
+  const int32_t* positions;
+  const int32_t* seq_ids;    // nullptr: token i belongs to sequence i
+  const int32_t* tables;
+  int32_t* status;
+  int64_t T;
+  int Hq, Hk, D, rd;         // Hq = 0: no q; Hk = 0: no k
+  int B, BS, L, layer, max_blocks, num_blocks;
+  int in_dtype, kv_dtype;    // kv_dtype: the pool's
+  float k_scale, v_scale;
+  const float* block_scales;
+  int groups_q, groups_k;    // set by the launcher: grid rows of q and of k (then of v)
+};
+cudaError_t launch_rope(RopeArgs a, int sms, cudaStream_t stream);
+
+struct VerifyArgs {
+  int32_t* tokens;
+  int32_t* num_accepted;
+  const void* target;
+  const void* draft;         // nullptr: drafts without probabilities
+  int64_t t_seq, t_row, d_seq, d_row;
+  const int32_t* drafts;
+  const int32_t* num_drafts;
+  const float* u_accept;
+  const float* u_sample;
+  int32_t* status;
+  int B, K, V, dtype;
+};
+cudaError_t launch_verify(const VerifyArgs& a, int sms, cudaStream_t stream);
+
 // Launch counter shared by every launcher.
 void count_launch();
 

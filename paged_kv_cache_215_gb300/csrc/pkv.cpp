@@ -1126,6 +1126,193 @@ int merge_partials(void* d_out, pkv_dtype out_dtype, const float* d_part_o,
              : PKV_ECUDA;
 }
 
+// ---------------------------------------------------------------- rotary positions
+
+static bool rope_ok(const pkv_rope* r, int head_dim) {
+  return r && r->d_freqs && (reinterpret_cast<uintptr_t>(r->d_freqs) & 7u) == 0 &&
+         r->rotary_dim >= 2 && r->rotary_dim % 2 == 0 && r->rotary_dim <= head_dim &&
+         (r->interleaved == 0 || r->interleaved == 1) && std::isfinite(r->attn_scale);
+}
+
+// Rows an op reads: any strides >= 0, data aligned to the element.
+static bool rows_ok(const pkv_rows* r, int dtype) {
+  return r && r->data && r->token_stride >= 0 && r->head_stride >= 0 &&
+         reinterpret_cast<uintptr_t>(r->data) % elem_bytes(dtype) == 0;
+}
+
+// Rows an op writes: no two of them overlap (tokens outermost or heads outermost).
+static bool out_rows_ok(const pkv_rows* r, int dtype, int64_t tokens, int heads, int head_dim) {
+  if (!rows_ok(r, dtype)) return false;
+  const int64_t ts = r->token_stride, hs = r->head_stride;
+  if ((heads > 1 && hs < head_dim) || (tokens > 1 && ts < head_dim)) return false;
+  if (heads == 1 || tokens == 1) return true;
+  return ts / hs >= heads || (ts % hs >= head_dim && ts / hs == heads - 1) ||
+         hs / ts >= tokens || (hs % ts >= head_dim && hs / ts == tokens - 1);
+}
+
+// Output rows that start where the input's do are the input's own rows.
+static bool same_or_apart(const pkv_rows* out, const pkv_rows* in, int64_t tokens, int heads) {
+  return out->data != in->data ||
+         ((tokens == 1 || out->token_stride == in->token_stride) &&
+          (heads == 1 || out->head_stride == in->head_stride));
+}
+
+// One token or one head: its stride is never used; 0 keeps it out of the
+// alignment rule.
+static void set_rows(const pkv_rows* r, int64_t tokens, int heads, int64_t* ts, int64_t* hs) {
+  *ts = tokens == 1 ? 0 : r->token_stride;
+  *hs = heads == 1 ? 0 : r->head_stride;
+}
+
+static int finish_rope(RopeArgs& a, const pkv_rope* rope, int backward, cudaStream_t stream) {
+  DeviceInfo dev;
+  if (!device_info(&dev)) return PKV_ECUDA;
+  a.freqs = rope->d_freqs;
+  a.m = rope->attn_scale;
+  a.sign = backward ? -1.f : 1.f;
+  a.interleaved = rope->interleaved;
+  a.rd = rope->rotary_dim;
+  return launch_rope(a, dev.sms, stream) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+int rope_apply(const pkv_rows* q_out, const pkv_rows* q, int num_q_heads, const pkv_rows* k_out,
+               const pkv_rows* k, int num_k_heads, pkv_dtype dtype, int head_dim,
+               const int32_t* d_positions, int64_t num_tokens, const pkv_rope* rope, int backward,
+               cudaStream_t stream) {
+  if (num_tokens < 0 || num_q_heads < 1 || num_k_heads < 0 || num_q_heads > 65535 ||
+      num_k_heads > 65535 || head_dim < 2 || head_dim > 512 || !act_dtype(dtype) || backward < 0 ||
+      backward > 1 || !rope_ok(rope, head_dim))
+    return PKV_EINVAL;
+  if (num_tokens == 0) return PKV_OK;
+  if (num_tokens > 0x7fffffffLL || !d_positions) return PKV_EINVAL;
+  if (!rows_ok(q, dtype) || !out_rows_ok(q_out, dtype, num_tokens, num_q_heads, head_dim) ||
+      !same_or_apart(q_out, q, num_tokens, num_q_heads))
+    return PKV_EINVAL;
+  RopeArgs a{};
+  a.q = q->data;
+  a.qo = q_out->data;
+  set_rows(q, num_tokens, num_q_heads, &a.q_ts, &a.q_hs);
+  set_rows(q_out, num_tokens, num_q_heads, &a.qo_ts, &a.qo_hs);
+  bool in_place = q_out->data == q->data;
+  if (num_k_heads > 0) {
+    if (!rows_ok(k, dtype) || !out_rows_ok(k_out, dtype, num_tokens, num_k_heads, head_dim) ||
+        !same_or_apart(k_out, k, num_tokens, num_k_heads))
+      return PKV_EINVAL;
+    a.k = k->data;
+    a.ko = k_out->data;
+    set_rows(k, num_tokens, num_k_heads, &a.k_ts, &a.k_hs);
+    set_rows(k_out, num_tokens, num_k_heads, &a.ko_ts, &a.ko_hs);
+    in_place = in_place && k_out->data == k->data;
+  }
+  a.copy_tail = !in_place;
+  a.positions = d_positions;
+  a.T = num_tokens;
+  a.Hq = num_q_heads;
+  a.Hk = num_k_heads;
+  a.D = head_dim;
+  a.in_dtype = dtype;
+  a.kv_dtype = dtype;
+  return finish_rope(a, rope, backward, stream);
+}
+
+int kv_append_rope(pkv_pool* p, int layer, const pkv_rows* q_out, const pkv_rows* q,
+                   const pkv_rows* k, const pkv_rows* v, pkv_dtype in_dtype, const pkv_rope* rope,
+                   const int32_t* d_block_tables, int max_blocks_per_seq, int batch,
+                   const int32_t* d_seq_ids, const int32_t* d_positions, int64_t num_tokens,
+                   float k_scale, float v_scale, cudaStream_t stream) {
+  if (!p || layer < 0 || layer >= p->g.num_layers || batch < 0 || num_tokens < 0)
+    return PKV_EINVAL;
+  const pkv_geometry& g = p->g;
+  if (!rope_ok(rope, g.head_dim) || !q != !q_out || g.num_q_heads > 65535) return PKV_EINVAL;
+  const bool fp8 = g.kv_dtype == PKV_FP8_E4M3;
+  if (fp8 ? !act_dtype(in_dtype) : (int)in_dtype != g.kv_dtype) return PKV_EINVAL;
+  if (fp8 && !p->d_block_scales &&
+      (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale)))
+    return PKV_EINVAL;
+  if (num_tokens == 0) return PKV_OK;
+  if (num_tokens > 0x7fffffffLL || !d_positions || !d_block_tables || max_blocks_per_seq < 1 ||
+      batch < 1 || !rows_ok(k, in_dtype) || !rows_ok(v, in_dtype))
+    return PKV_EINVAL;
+  RopeArgs a{};
+  if (q) {
+    if (!rows_ok(q, in_dtype) ||
+        !out_rows_ok(q_out, in_dtype, num_tokens, g.num_q_heads, g.head_dim) ||
+        !same_or_apart(q_out, q, num_tokens, g.num_q_heads))
+      return PKV_EINVAL;
+    a.q = q->data;
+    a.qo = q_out->data;
+    set_rows(q, num_tokens, g.num_q_heads, &a.q_ts, &a.q_hs);
+    set_rows(q_out, num_tokens, g.num_q_heads, &a.qo_ts, &a.qo_hs);
+    a.Hq = g.num_q_heads;
+  }
+  a.k = k->data;
+  a.v = v->data;
+  set_rows(k, num_tokens, g.num_kv_heads, &a.k_ts, &a.k_hs);
+  set_rows(v, num_tokens, g.num_kv_heads, &a.v_ts, &a.v_hs);
+  a.pool = p->d_pool;
+  a.copy_tail = 1;
+  a.positions = d_positions;
+  a.seq_ids = d_seq_ids;
+  a.tables = d_block_tables;
+  a.status = p->d_status;
+  a.T = num_tokens;
+  a.Hk = g.num_kv_heads;
+  a.D = g.head_dim;
+  a.B = batch;
+  a.BS = g.block_size;
+  a.L = g.num_layers;
+  a.layer = layer;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = g.num_blocks;
+  a.in_dtype = in_dtype;
+  a.kv_dtype = g.kv_dtype;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_scales = fp8 ? p->d_block_scales : nullptr;
+  return finish_rope(a, rope, 0, stream);
+}
+
+// ---------------------------------------------------------------- draft verification
+
+int verify_drafts(int32_t* d_tokens, int32_t* d_num_accepted, const pkv_probs* target,
+                  const pkv_probs* draft, pkv_dtype dtype, const int32_t* d_drafts,
+                  const int32_t* d_num_drafts, const float* d_u_accept, const float* d_u_sample,
+                  int batch, int max_drafts, int vocab, int32_t* d_status, cudaStream_t stream) {
+  if (batch < 0 || max_drafts < 0 || vocab < 1 || !act_dtype(dtype)) return PKV_EINVAL;
+  if (batch == 0) return PKV_OK;
+  const int eb = elem_bytes(dtype);
+  if (!d_tokens || !d_num_accepted || !target || !target->data || target->seq_stride < 0 ||
+      target->row_stride < 0 || reinterpret_cast<uintptr_t>(target->data) % eb || !d_u_sample)
+    return PKV_EINVAL;
+  if (max_drafts > 0 && (!d_drafts || !d_u_accept)) return PKV_EINVAL;
+  VerifyArgs a{};
+  if (draft && draft->data && max_drafts > 0) {
+    if (draft->seq_stride < 0 || draft->row_stride < 0 ||
+        reinterpret_cast<uintptr_t>(draft->data) % eb)
+      return PKV_EINVAL;
+    a.draft = draft->data;
+    a.d_seq = draft->seq_stride;
+    a.d_row = draft->row_stride;
+  }
+  a.tokens = d_tokens;
+  a.num_accepted = d_num_accepted;
+  a.target = target->data;
+  a.t_seq = target->seq_stride;
+  a.t_row = target->row_stride;
+  a.drafts = d_drafts;
+  a.num_drafts = d_num_drafts;
+  a.u_accept = d_u_accept;
+  a.u_sample = d_u_sample;
+  a.status = d_status;
+  a.B = batch;
+  a.K = max_drafts;
+  a.V = vocab;
+  a.dtype = dtype;
+  DeviceInfo dev;
+  if (!device_info(&dev)) return PKV_ECUDA;
+  return launch_verify(a, dev.sms, stream) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
 int pkv_check_status(const pkv_pool* p, cudaStream_t stream) {
   if (!p) return PKV_EINVAL;
   if (cudaStreamSynchronize(stream) != cudaSuccess) return PKV_ECUDA;

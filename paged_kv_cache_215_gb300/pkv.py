@@ -46,6 +46,28 @@ class LaunchOpts(ctypes.Structure):
                 ("reserved", ctypes.c_int32 * 2)]
 
 
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_positions", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double)]
+
+
+class RopeRef(ctypes.Structure):
+    _fields_ = [("d_freqs", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("attn_scale", ctypes.c_float)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class Probs(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("seq_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64)]
+
+
 def _load() -> ctypes.CDLL:
     path = _build.SO
     if not os.path.exists(path):
@@ -55,6 +77,7 @@ def _load() -> ctypes.CDLL:
     P, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     I64 = ctypes.c_int64
     G = ctypes.POINTER(Geometry)
+    R = ctypes.POINTER(Rows)
     sig = {
         "kv_pool_bytes": (Z, [G]),
         "kv_pool_create": (I, [G, P, Z, P, ctypes.POINTER(P)]),
@@ -89,6 +112,13 @@ def _load() -> ctypes.CDLL:
         "paged_decode_attention_cascade": (I, [P, I, P, I, P, I, P, I, I, P, P, I, P, I, I, F, F,
                                                F, P, Z, ctypes.POINTER(LaunchOpts), P]),
         "paged_decode_workspace_bytes_cascade": (Z, [G, I, I, I, I]),
+        "pkv_rope_freqs": (I, [ctypes.POINTER(RopeConfig), P, ctypes.POINTER(F)]),
+        "pkv_rope_freqs_from": (I, [P, I, P]),
+        "rope_apply": (I, [R, R, I, R, R, I, I, I, P, I64, ctypes.POINTER(RopeRef), I, P]),
+        "kv_append_rope": (I, [P, I, R, R, R, R, I, ctypes.POINTER(RopeRef), P, I, I, P, P, I64,
+                               F, F, P]),
+        "verify_drafts": (I, [P, P, ctypes.POINTER(Probs), ctypes.POINTER(Probs), I, P, P, P, P,
+                              I, I, I, P, P]),
         "pkv_check_status": (I, [P, P]),
         "pkv_wait_selftest": (I, [P, P]),
         "pkv_strerror": (ctypes.c_char_p, [I]),
@@ -113,6 +143,8 @@ EXPORTS = ("kv_pool_bytes", "kv_pool_create", "kv_pool_destroy", "kv_pool_geomet
            "paged_decode_attention_static", "paged_decode_step",
            "paged_decode_attention_mq", "paged_decode_workspace_bytes_mq",
            "paged_decode_attention_cascade", "paged_decode_workspace_bytes_cascade",
+           "pkv_rope_freqs", "pkv_rope_freqs_from", "rope_apply", "kv_append_rope",
+           "verify_drafts",
            "pkv_check_status", "pkv_wait_selftest", "pkv_strerror", "pkv_launch_count")
 
 
@@ -166,6 +198,145 @@ def launch_opts(kernel=0, ctas_per_sm=0, kv_heads_per_cta=0, stages=0, phase=0,
     o.kernel, o.ctas_per_sm, o.kv_heads_per_cta, o.stages, o.phase, o.pdl = \
         kernel, ctas_per_sm, kv_heads_per_cta, stages, phase, pdl
     return o
+
+
+# ---- checks of the rotary and verification calls' tensors
+def _one_device(tensors) -> torch.device:
+    dev = tensors[0].device
+    for t in tensors:
+        if t.device != dev or dev.type != "cuda":
+            raise ValueError(f"tensors on {t.device} and {dev}: one CUDA device is needed")
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("this call records no gradient: detach its tensors "
+                             "(rope_apply(..., backward=True) is the gradient of rope_apply)")
+    return dev
+
+
+def _on(dev: torch.device):
+    """The device current for a call on tensors of `dev`."""
+    return torch.cuda.device(dev)
+
+
+def _act_code(t: torch.Tensor) -> int:
+    code = TORCH_CODE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"dtype {t.dtype}: float32, float16 or bfloat16 is needed")
+    return code
+
+
+def _rows(t: Optional[torch.Tensor], shape, dtype, name: str):
+    if t is None:
+        return None
+    if tuple(t.shape) != shape or t.dtype != dtype or (t.numel() and t.stride(2) != 1):
+        raise ValueError(f"{name}: {shape} of {dtype} with unit stride along the last dimension "
+                         f"is needed, got {tuple(t.shape)} of {t.dtype}, strides {t.stride()}")
+    return ctypes.byref(Rows(t.data_ptr(), t.stride(0), t.stride(1)))
+
+
+def _int32(t: Optional[torch.Tensor], shape, name: str):
+    if t is None:
+        return None
+    if tuple(t.shape) != shape or t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous int32 {shape} is needed, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    return t.data_ptr()
+
+
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+class Rope:
+    """Rotary positions: the frequency table of rotary_dim / 2 pairs on the device,
+    the layout and the attention scale.
+
+    scaling: "none", "linear" (position interpolation), "ntk" or "yarn", with
+    ``factor`` the ratio of the served to the trained length and, for "yarn",
+    ``original_positions`` the trained length.  ``frequencies`` (radians per
+    position, rotary_dim / 2 numbers) gives the table of any other scaling;
+    ``attn_scale`` replaces the factor on the rotated pairs."""
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0, original_positions: float = 0.0,
+                 beta_fast: float = 32.0, beta_slow: float = 1.0, frequencies=None,
+                 attn_scale: Optional[float] = None, device="cuda"):
+        if rotary_dim < 2 or rotary_dim % 2:
+            raise ValueError(f"rotary_dim {rotary_dim}: an even number is needed")
+        n = rotary_dim // 2
+        table = (ctypes.c_uint64 * n)()
+        scale = ctypes.c_float(1.0)
+        if frequencies is not None:
+            values = [float(x) for x in frequencies]
+            if len(values) != n:
+                raise ValueError(f"{len(values)} frequencies for {n} pairs")
+            _check(_lib.pkv_rope_freqs_from((ctypes.c_double * n)(*values), n, table),
+                   "pkv_rope_freqs_from")
+        else:
+            if scaling not in ROPE_SCALING:
+                raise ValueError(f"scaling {scaling!r}: one of {sorted(ROPE_SCALING)}")
+            cfg = RopeConfig(rotary_dim, ROPE_SCALING[scaling], base, factor, original_positions,
+                             beta_fast, beta_slow)
+            _check(_lib.pkv_rope_freqs(ctypes.byref(cfg), table, ctypes.byref(scale)),
+                   "pkv_rope_freqs")
+        self.rotary_dim, self.interleaved = rotary_dim, bool(interleaved)
+        self.attn_scale = scale.value if attn_scale is None else float(attn_scale)
+        self.freqs = torch.frombuffer(bytearray(table), dtype=torch.int64).to(device)
+        self.ref = RopeRef(self.freqs.data_ptr(), rotary_dim, int(interleaved), self.attn_scale)
+
+
+def rope_apply(q_out, q, positions, rope: Rope, k_out=None, k=None, backward=False, stream=None):
+    """Rotate q [tokens, heads, head_dim] (and k, with its own heads) to q_out (k_out),
+    token t at positions[t] (int32; negative: padding, its rows are left alone).
+    Any strides with a unit one along head_dim; q_out may be q.  backward: the
+    gradients of q_out and k_out come in as q and k, those of q and k go out."""
+    if (k is None) != (k_out is None):
+        raise ValueError("rope_apply takes k and k_out together")
+    T, H, D = q.shape
+    dev = _one_device((q, q_out, positions, rope.freqs) + ((k, k_out) if k is not None else ()))
+    ks = (T, k.shape[1], D) if k is not None else None
+    with _on(dev):
+        _check(_lib.rope_apply(
+            _rows(q_out, (T, H, D), q.dtype, "q_out"), _rows(q, (T, H, D), q.dtype, "q"), H,
+            _rows(k_out, ks, q.dtype, "k_out"), _rows(k, ks, q.dtype, "k"), ks[1] if ks else 0,
+            _act_code(q), D, _int32(positions, (T,), "positions"), T, rope.ref, int(backward),
+            _stream(stream)), "rope_apply")
+    return q_out if k is None else (q_out, k_out)
+
+
+def verify_drafts(tokens, num_accepted, target, draft, drafts, u_accept, u_sample,
+                  num_drafts=None, status=None, stream=None):
+    """Speculative verification: target [B, K + 1, V] and draft [B, K, V] probabilities
+    (draft None: drafts looked up rather than drawn), drafts [B, K] int32, u_accept
+    [B, K] and u_sample [B] float32 in [0, 1); num_drafts [B] int32 (None: K each).
+    tokens [B, K + 1] int32 receives the accepted drafts, the next token, then -1;
+    num_accepted [B] int32.  status: an int32 tensor taking the first device error."""
+    B, K = drafts.shape
+    V = target.shape[2]
+    dev = _one_device(tuple(t for t in (tokens, num_accepted, target, draft, drafts, u_accept,
+                                        u_sample, num_drafts, status) if t is not None))
+
+    def probs(t, rows, name):
+        if t is None:
+            return None
+        if tuple(t.shape) != (B, rows, V) or t.dtype != target.dtype or \
+                (t.numel() and t.stride(2) != 1):
+            raise ValueError(f"{name}: {(B, rows, V)} of {target.dtype} with unit stride along "
+                             f"the last dimension is needed, got {tuple(t.shape)} of {t.dtype}, "
+                             f"strides {t.stride()}")
+        return ctypes.byref(Probs(t.data_ptr(), t.stride(0), t.stride(1)))
+
+    for t, shape, name in ((u_accept, (B, K), "u_accept"), (u_sample, (B,), "u_sample")):
+        if tuple(t.shape) != shape or t.dtype != torch.float32 or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous float32 {shape} is needed")
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status: an int32 tensor is needed")
+    with _on(dev):
+        _check(_lib.verify_drafts(
+            _int32(tokens, (B, K + 1), "tokens"), _int32(num_accepted, (B,), "num_accepted"),
+            probs(target, K + 1, "target"), probs(draft, K, "draft"), _act_code(target),
+            _int32(drafts, (B, K), "drafts"), _int32(num_drafts, (B,), "num_drafts"),
+            u_accept.data_ptr(), u_sample.data_ptr(), B, K, V,
+            None if status is None else status.data_ptr(), _stream(stream)), "verify_drafts")
+    return tokens, num_accepted
 
 
 class KVPool:
@@ -264,6 +435,33 @@ class KVPool:
                                      _ptr(tables), tables.shape[1], tables.shape[0],
                                      _ptr(seq_ids), _ptr(positions), seq_ids.shape[0], k_scale,
                                      v_scale, _stream(stream)), "kv_append_tokens")
+
+    def append_rope(self, layer, q_out, q, k, v, rope, tables, positions, seq_ids=None,
+                    k_scale=1.0, v_scale=1.0, stream=None):
+        """append_tokens of rotated keys (and v) with the rotated queries written to
+        q_out, in one launch.  q, k, v and q_out are [tokens, heads, head_dim] with
+        unit stride along head_dim (views of a joint projection are fine; q_out may
+        be q); q_out = q = None stores keys and values only."""
+        g = self.geom
+        T = k.shape[0]
+        qh, kh = (T, g.num_q_heads, g.head_dim), (T, g.num_kv_heads, g.head_dim)
+        dev = _one_device((k, v, tables, positions, self.storage, rope.freqs) +
+                          ((q, q_out) if q is not None else ()) +
+                          ((seq_ids,) if seq_ids is not None else ()))
+        if (q is None) != (q_out is None):
+            raise ValueError("append_rope takes q and q_out together")
+        ids = _int32(seq_ids, (T,), "seq_ids")
+        pos = _int32(positions, (T,), "positions")
+        if tables.dim() != 2 or (seq_ids is None and tables.shape[0] < T):
+            raise ValueError("tables: one row [max_blocks] per sequence")
+        with _on(dev):
+            _check(_lib.kv_append_rope(
+                self.handle, layer, _rows(q_out, qh, k.dtype, "q_out"),
+                _rows(q, qh, k.dtype, "q"), _rows(k, kh, k.dtype, "k"),
+                _rows(v, kh, k.dtype, "v"), _act_code(k), rope.ref,
+                _int32(tables, tuple(tables.shape), "tables"), tables.shape[1], tables.shape[0],
+                ids, pos, T, k_scale, v_scale, _stream(stream)), "kv_append_rope")
+        return q_out
 
     def set_block_scales(self, scales: Optional[torch.Tensor]):
         """Attach a [NB, 2, L, Hkv] float32 device tensor of per-tile E4M3 scales."""

@@ -3,14 +3,19 @@
 Each .cu file is compiled by nvcc for sm_103a in parallel, the host C++ file by
 g++, and the objects are linked into one shared library against the CUDA
 runtime.  No CMake, no setuptools: one nvcc invocation per translation unit.
+The module that checks torch tensors for the short calls (csrc/binding) is built
+beside it against the installed torch, and again when that changes.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 SO = os.path.join(BUILD, "libpkv.so")
+BINDING = os.path.join(BUILD, "pkv_tensors.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -36,11 +42,45 @@ def _sources():
     return cus, cpps, deps
 
 
-def _stale(deps) -> bool:
-    if not os.path.exists(SO):
+def _stale(deps, target=SO) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(SO)
+    t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps + [__file__])
+
+
+def _torch():
+    """The installed torch's folder and version (without importing it)."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin), importlib.metadata.version("torch")
+
+
+def _binding_job():
+    """(command that compiles the binding, its object), or None if it is up to date."""
+    src = os.path.join(CSRC, "binding", "pkv_tensors.cpp")
+    where, version = _torch()
+    stamp = BINDING + ".torch"
+    built = open(stamp).read() if os.path.exists(stamp) else ""
+    if built == version and not _stale([src, os.path.join(INCLUDE, "pkv.h")], BINDING):
+        return None
+    obj = os.path.join(BUILD, "pkv_tensors.cpp.o")
+    inc = [INCLUDE, os.path.join(_cuda_home(), "include"), os.path.join(where, "include"),
+           os.path.join(where, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+            *[x for i in inc for x in ("-isystem" if i != INCLUDE else "-I", i)],
+            "-c", src, "-o", obj], obj
+
+
+def _link_binding(obj):
+    where, version = _torch()
+    lib = os.path.join(where, "lib")
+    _run(["g++", "-shared", "-o", BINDING + ".tmp", obj, "-L", BUILD, "-l:libpkv.so", "-L", lib,
+          "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda",
+          "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib])
+    os.replace(BINDING + ".tmp", BINDING)
+    with open(BINDING + ".torch", "w") as f:
+        f.write(version)
 
 
 def _run(cmd):
@@ -52,9 +92,13 @@ def _run(cmd):
 
 def build(force: bool = False, verbose: bool = False) -> str:
     cus, cpps, deps = _sources()
-    if not force and not _stale(deps):
-        return SO
     os.makedirs(BUILD, exist_ok=True)
+    binding = _binding_job()
+    if not force and not _stale(deps):
+        if binding:
+            _run(binding[0])
+            _link_binding(binding[1])
+        return SO
     cuda = _cuda_home()
     nvcc = os.path.join(cuda, "bin", "nvcc")
     inc = ["-I", INCLUDE, "-I", CSRC, "-I", os.path.join(cuda, "include")]
@@ -71,6 +115,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *inc, "-c", src,
                "-o", obj]
         jobs.append((cmd, obj))
+    if binding:
+        jobs.insert(0, binding)
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
         logs = list(ex.map(lambda j: _run(j[0]), jobs))
     if verbose:
@@ -78,10 +124,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if l.strip():
                 print(l)
     tmp = SO + ".tmp"
-    _run([nvcc, *ARCH, "-shared", "-o", tmp, *[o for _, o in jobs],
+    _run([nvcc, *ARCH, "-shared", "-o", tmp, *[j[1] for j in jobs if j is not binding],
           "-L", os.path.join(cuda, "lib64"), "-lcudart",
           "-Xlinker", "-rpath=" + os.path.join(cuda, "lib64")])
     os.replace(tmp, SO)
+    if binding:
+        _link_binding(binding[1])
     return SO
 
 

@@ -8,6 +8,7 @@ without it raises -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -131,7 +132,19 @@ def _load() -> ctypes.CDLL:
     return lib
 
 
+def _load_tensors():
+    """The compiled module that checks and passes tensors of the short calls."""
+    path = _build.BINDING
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is not built; run paged_kv_cache_215_gb300.build.build()")
+    spec = importlib.util.spec_from_file_location("pkv_tensors", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
 _lib = _load()
+_tensors = _load_tensors()
 EXPORTS = ("kv_pool_bytes", "kv_pool_create", "kv_pool_destroy", "kv_pool_geometry",
            "kv_pool_alloc", "kv_pool_reserve", "kv_pool_free", "kv_pool_share",
            "kv_pool_refcount", "kv_pool_num_free", "kv_pool_cow", "kv_pool_prepare_append",
@@ -200,48 +213,6 @@ def launch_opts(kernel=0, ctas_per_sm=0, kv_heads_per_cta=0, stages=0, phase=0,
     return o
 
 
-# ---- checks of the rotary and verification calls' tensors
-def _one_device(tensors) -> torch.device:
-    dev = tensors[0].device
-    for t in tensors:
-        if t.device != dev or dev.type != "cuda":
-            raise ValueError(f"tensors on {t.device} and {dev}: one CUDA device is needed")
-        if t.requires_grad and torch.is_grad_enabled():
-            raise ValueError("this call records no gradient: detach its tensors "
-                             "(rope_apply(..., backward=True) is the gradient of rope_apply)")
-    return dev
-
-
-def _on(dev: torch.device):
-    """The device current for a call on tensors of `dev`."""
-    return torch.cuda.device(dev)
-
-
-def _act_code(t: torch.Tensor) -> int:
-    code = TORCH_CODE.get(t.dtype)
-    if code is None:
-        raise ValueError(f"dtype {t.dtype}: float32, float16 or bfloat16 is needed")
-    return code
-
-
-def _rows(t: Optional[torch.Tensor], shape, dtype, name: str):
-    if t is None:
-        return None
-    if tuple(t.shape) != shape or t.dtype != dtype or (t.numel() and t.stride(2) != 1):
-        raise ValueError(f"{name}: {shape} of {dtype} with unit stride along the last dimension "
-                         f"is needed, got {tuple(t.shape)} of {t.dtype}, strides {t.stride()}")
-    return ctypes.byref(Rows(t.data_ptr(), t.stride(0), t.stride(1)))
-
-
-def _int32(t: Optional[torch.Tensor], shape, name: str):
-    if t is None:
-        return None
-    if tuple(t.shape) != shape or t.dtype != torch.int32 or not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous int32 {shape} is needed, got {t.dtype} "
-                         f"{tuple(t.shape)}")
-    return t.data_ptr()
-
-
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
@@ -281,6 +252,7 @@ class Rope:
         self.attn_scale = scale.value if attn_scale is None else float(attn_scale)
         self.freqs = torch.frombuffer(bytearray(table), dtype=torch.int64).to(device)
         self.ref = RopeRef(self.freqs.data_ptr(), rotary_dim, int(interleaved), self.attn_scale)
+        self.address = ctypes.addressof(self.ref)
 
 
 def rope_apply(q_out, q, positions, rope: Rope, k_out=None, k=None, backward=False, stream=None):
@@ -288,17 +260,10 @@ def rope_apply(q_out, q, positions, rope: Rope, k_out=None, k=None, backward=Fal
     token t at positions[t] (int32; negative: padding, its rows are left alone).
     Any strides with a unit one along head_dim; q_out may be q.  backward: the
     gradients of q_out and k_out come in as q and k, those of q and k go out."""
-    if (k is None) != (k_out is None):
-        raise ValueError("rope_apply takes k and k_out together")
-    T, H, D = q.shape
-    dev = _one_device((q, q_out, positions, rope.freqs) + ((k, k_out) if k is not None else ()))
-    ks = (T, k.shape[1], D) if k is not None else None
-    with _on(dev):
-        _check(_lib.rope_apply(
-            _rows(q_out, (T, H, D), q.dtype, "q_out"), _rows(q, (T, H, D), q.dtype, "q"), H,
-            _rows(k_out, ks, q.dtype, "k_out"), _rows(k, ks, q.dtype, "k"), ks[1] if ks else 0,
-            _act_code(q), D, _int32(positions, (T,), "positions"), T, rope.ref, int(backward),
-            _stream(stream)), "rope_apply")
+    rc = _tensors.rope_apply(q_out, q, positions, rope.freqs, rope.address, k_out, k, backward,
+                             stream)
+    if rc:
+        raise PkvError(rc, "rope_apply")
     return q_out if k is None else (q_out, k_out)
 
 
@@ -309,33 +274,10 @@ def verify_drafts(tokens, num_accepted, target, draft, drafts, u_accept, u_sampl
     [B, K] and u_sample [B] float32 in [0, 1); num_drafts [B] int32 (None: K each).
     tokens [B, K + 1] int32 receives the accepted drafts, the next token, then -1;
     num_accepted [B] int32.  status: an int32 tensor taking the first device error."""
-    B, K = drafts.shape
-    V = target.shape[2]
-    dev = _one_device(tuple(t for t in (tokens, num_accepted, target, draft, drafts, u_accept,
-                                        u_sample, num_drafts, status) if t is not None))
-
-    def probs(t, rows, name):
-        if t is None:
-            return None
-        if tuple(t.shape) != (B, rows, V) or t.dtype != target.dtype or \
-                (t.numel() and t.stride(2) != 1):
-            raise ValueError(f"{name}: {(B, rows, V)} of {target.dtype} with unit stride along "
-                             f"the last dimension is needed, got {tuple(t.shape)} of {t.dtype}, "
-                             f"strides {t.stride()}")
-        return ctypes.byref(Probs(t.data_ptr(), t.stride(0), t.stride(1)))
-
-    for t, shape, name in ((u_accept, (B, K), "u_accept"), (u_sample, (B,), "u_sample")):
-        if tuple(t.shape) != shape or t.dtype != torch.float32 or not t.is_contiguous():
-            raise ValueError(f"{name}: contiguous float32 {shape} is needed")
-    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
-        raise ValueError("status: an int32 tensor is needed")
-    with _on(dev):
-        _check(_lib.verify_drafts(
-            _int32(tokens, (B, K + 1), "tokens"), _int32(num_accepted, (B,), "num_accepted"),
-            probs(target, K + 1, "target"), probs(draft, K, "draft"), _act_code(target),
-            _int32(drafts, (B, K), "drafts"), _int32(num_drafts, (B,), "num_drafts"),
-            u_accept.data_ptr(), u_sample.data_ptr(), B, K, V,
-            None if status is None else status.data_ptr(), _stream(stream)), "verify_drafts")
+    rc = _tensors.verify_drafts(tokens, num_accepted, target, draft, drafts, u_accept, u_sample,
+                                num_drafts, status, stream)
+    if rc:
+        raise PkvError(rc, "verify_drafts")
     return tokens, num_accepted
 
 
@@ -442,25 +384,11 @@ class KVPool:
         q_out, in one launch.  q, k, v and q_out are [tokens, heads, head_dim] with
         unit stride along head_dim (views of a joint projection are fine; q_out may
         be q); q_out = q = None stores keys and values only."""
-        g = self.geom
-        T = k.shape[0]
-        qh, kh = (T, g.num_q_heads, g.head_dim), (T, g.num_kv_heads, g.head_dim)
-        dev = _one_device((k, v, tables, positions, self.storage, rope.freqs) +
-                          ((q, q_out) if q is not None else ()) +
-                          ((seq_ids,) if seq_ids is not None else ()))
-        if (q is None) != (q_out is None):
-            raise ValueError("append_rope takes q and q_out together")
-        ids = _int32(seq_ids, (T,), "seq_ids")
-        pos = _int32(positions, (T,), "positions")
-        if tables.dim() != 2 or (seq_ids is None and tables.shape[0] < T):
-            raise ValueError("tables: one row [max_blocks] per sequence")
-        with _on(dev):
-            _check(_lib.kv_append_rope(
-                self.handle, layer, _rows(q_out, qh, k.dtype, "q_out"),
-                _rows(q, qh, k.dtype, "q"), _rows(k, kh, k.dtype, "k"),
-                _rows(v, kh, k.dtype, "v"), _act_code(k), rope.ref,
-                _int32(tables, tuple(tables.shape), "tables"), tables.shape[1], tables.shape[0],
-                ids, pos, T, k_scale, v_scale, _stream(stream)), "kv_append_rope")
+        rc = _tensors.append_rope(self.handle.value if self.handle else 0, self.storage, layer, q_out, q, k, v,
+                                  rope.freqs, rope.address, tables, positions, seq_ids, k_scale,
+                                  v_scale, stream)
+        if rc:
+            raise PkvError(rc, "kv_append_rope")
         return q_out
 
     def set_block_scales(self, scales: Optional[torch.Tensor]):

@@ -8,9 +8,11 @@
 // turn, go to sincospi.  Products and sums are fp32, rounded once to the output's
 // type (for an E4M3 pool straight from fp32).
 //
-// A thread owns VEC pairs of one token's rows: VEC elements of each half of the
-// rotated part (half layout) or 2 VEC consecutive ones (interleaved).  Its sines
-// and cosines are computed once and used for every head it visits.
+// A thread owns one part of a token's rows: two vectors of VEC elements, at offset
+// e0 and half the rotated part further on, the same for both layouts (their pairs
+// lie across the two vectors or within each), so that neighbouring threads read
+// neighbouring 16 bytes.  Its sines and cosines are computed once and used for every
+// head it visits.
 #include <algorithm>
 
 #include "device.cuh"
@@ -46,31 +48,61 @@ struct Vec {
   __device__ __forceinline__ void store(void* base, int64_t i) const {
     *reinterpret_cast<R*>(static_cast<char*>(base) + i * elem_size(DT)) = r;
   }
-  __device__ __forceinline__ float get(int i) const {
-    if constexpr (DT == PKV_F32) return __uint_as_float(w[i]);
-    else if constexpr (DT == PKV_BF16) return __uint_as_float((uint32_t)h[i] << 16);
-    else return __half2float(__ushort_as_half(h[i]));
+  __device__ __forceinline__ void get(float (&x)[VEC]) const {
+    if constexpr (DT == PKV_F32) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) x[j] = __uint_as_float(w[j]);
+    } else if constexpr (VEC == 1) {
+      x[0] = DT == PKV_BF16 ? __uint_as_float((uint32_t)h[0] << 16)
+                            : __half2float(__ushort_as_half(h[0]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC / 2; ++j) {
+        const float2 f = unpack2<DT == PKV_BF16>(w[j]);
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+      }
+    }
   }
-  __device__ __forceinline__ void set(int i, float x) {
-    if constexpr (DT == PKV_F32) w[i] = __float_as_uint(x);
-    else if constexpr (DT == PKV_BF16) h[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-    else h[i] = __half_as_ushort(__float2half_rn(x));
+  // Rounded to DT; E4M3: x / scale, as kv_append encodes.
+  __device__ __forceinline__ void set(const float (&x)[VEC], float scale) {
+    if constexpr (DT == PKV_F32) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) w[j] = __float_as_uint(x[j]);
+    } else if constexpr (DT == PKV_FP8_E4M3) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) b[j] = encode_e4m3(x[j], scale);
+    } else if constexpr (VEC == 1) {
+      h[0] = DT == PKV_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x[0]))
+                            : __half_as_ushort(__float2half_rn(x[0]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC / 2; ++j) w[j] = pack2<DT == PKV_BF16>(x[2 * j], x[2 * j + 1]);
+    }
   }
 };
 
-// One row part (VEC or 2 x VEC elements) rotated (or copied) and stored as type KV.
-template <int KV, int VEC>
-__device__ __forceinline__ void put(void* out, int64_t i, const float (&x)[VEC], float scale) {
-  Vec<KV, VEC> y;
-  if constexpr (KV == PKV_FP8_E4M3) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) y.b[j] = encode_e4m3(x[j], scale);
+// Sine and cosine of `turns` (2^-32 of a full turn, signed) times m.  fp32 rows take
+// sincospi (1 ulp).  16-bit rows, and E4M3 pools filled from them, take the
+// special-function unit on the reduced angle, off by 2^-20.9 at most: a 2^-9 share
+// of bf16's half step, 2^-12 of f16's being the nearest.
+template <int IN>
+__device__ __forceinline__ void sine(int32_t turns, float m, float& s, float& c) {
+  if constexpr (IN == PKV_F32) {
+    sincospif((float)turns * 0x1p-31f, &s, &c);
   } else {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) y.set(j, x[j]);
+    __sincosf((float)turns * 1.46291807926715968e-9f, &s, &c);   // 2 pi 2^-32
   }
-  y.store(out, i);
+  s *= m;
+  c *= m;
 }
+
+// One part of a row.
+struct Part {
+  int e0, e1;       // offsets of its vectors in the head
+  bool second;      // the vector at e1 exists
+  bool turn;        // rotate, otherwise copy
+};
 
 struct Rows {
   const void* in;
@@ -79,50 +111,67 @@ struct Rows {
   int64_t i_hs, o_hs;   // head strides
 };
 
-// Heads [h0, h1) of one token.  turn: rotate the pair of parts at offsets e0 and e1;
-// otherwise copy them (pair: both, else the one at e0).
+// Loads in flight a thread: kBatch heads at a time, all loaded before the first is used.
+constexpr int kBatch = 4;
+
 template <int IN, int KV, int VEC, bool INTER>
-__device__ __forceinline__ void rows_of(const Rows& r, int h0, int h1, int e0, int e1, bool turn,
-                                        bool pair, const float (&cs)[VEC], const float (&sn)[VEC],
+__device__ __forceinline__ void rows_of(const Rows& r, int h0, int h1, const Part& p,
+                                        const float (&cs)[VEC], const float (&sn)[VEC],
                                         const float* scales, float scale) {
-  for (int h = h0; h < h1; ++h) {
-    const int64_t i = r.i0 + h * r.i_hs, o = r.o0 + h * r.o_hs;
-    Vec<IN, VEC> a, b;
-    a.load(r.in, i + e0);
-    if (pair) b.load(r.in, i + e1);
-    if constexpr (KV == IN) {
-      if (!turn) {
-        a.store(r.out, o + e0);
-        if (pair) b.store(r.out, o + e1);
-        continue;
+  for (int hb = h0; hb < h1; hb += kBatch) {
+    Vec<IN, VEC> a[kBatch], b[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (hb + i < h1) {
+        const int64_t at = r.i0 + (hb + i) * r.i_hs;
+        a[i].load(r.in, at + p.e0);
+        if (p.second) b[i].load(r.in, at + p.e1);
       }
     }
-    const float sc = scales ? scales[h] : scale;
-    float x[VEC], y[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      x[j] = a.get(j);
-      y[j] = pair ? b.get(j) : 0.f;
-    }
-    if (turn) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        if constexpr (INTER && VEC > 1) {
-          // pair j of the 2 VEC consecutive elements
-          float& p = 2 * j < VEC ? x[2 * j % VEC] : y[2 * j % VEC];
-          float& q = 2 * j < VEC ? x[2 * j % VEC + 1] : y[2 * j % VEC + 1];
-          const float u = p, v = q;
-          p = u * cs[j] - v * sn[j];
-          q = u * sn[j] + v * cs[j];
-        } else {
-          const float u = x[j], v = y[j];
-          x[j] = u * cs[j] - v * sn[j];
-          y[j] = u * sn[j] + v * cs[j];
+    for (int i = 0; i < kBatch; ++i) {
+      if (hb + i >= h1) break;
+      const int64_t to = r.o0 + (hb + i) * r.o_hs;
+      if constexpr (KV == IN) {
+        if (!p.turn) {
+          a[i].store(r.out, to + p.e0);
+          if (p.second) b[i].store(r.out, to + p.e1);
+          continue;
         }
       }
+      const float sc = scales ? scales[hb + i] : scale;
+      float x[VEC], y[VEC];
+      a[i].get(x);
+      if (p.second) b[i].get(y);
+      if (p.turn) {
+        if constexpr (INTER && VEC > 1) {
+          // pairs (0, 1), (2, 3) ... of each vector
+#pragma unroll
+          for (int j = 0; j < VEC; j += 2) {
+            const float u = x[j], v = x[j + 1], s = y[j], t = y[j + 1];
+            const int k = j / 2, l = VEC / 2 + j / 2;
+            x[j] = u * cs[k] - v * sn[k];
+            x[j + 1] = u * sn[k] + v * cs[k];
+            y[j] = s * cs[l] - t * sn[l];
+            y[j + 1] = s * sn[l] + t * cs[l];
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            const float u = x[j], v = y[j];
+            x[j] = u * cs[j] - v * sn[j];
+            y[j] = u * sn[j] + v * cs[j];
+          }
+        }
+      }
+      Vec<KV, VEC> o;
+      o.set(x, sc);
+      o.store(r.out, to + p.e0);
+      if (p.second) {
+        o.set(y, sc);
+        o.store(r.out, to + p.e1);
+      }
     }
-    put<KV, VEC>(r.out, o + e0, x, sc);
-    if (pair) put<KV, VEC>(r.out, o + e1, y, sc);
   }
 }
 
@@ -134,35 +183,47 @@ __global__ void __launch_bounds__(512) rope_kernel(const RopeArgs a, int hpt) {
   if (t >= a.T) return;
   const int pos = __ldg(a.positions + t);
   if (pos < 0) return;                       // padding: no token
-  const int c = threadIdx.x, turning = a.rd / (2 * VEC);
-  const bool pair = c < turning;
-  const int e0 = pair ? (INTER ? 2 * VEC * c : VEC * c) : a.rd + VEC * (c - turning);
-  const int e1 = INTER ? e0 + VEC : e0 + a.rd / 2;
   int g = blockIdx.y;
   const int kind = g < a.groups_q ? 0 : g < a.groups_q + a.groups_k ? 1 : 2;
+  const int c = threadIdx.x, turning = a.rd / (2 * VEC);
+  Part p;
+  if (c < turning) {
+    // one interleaved pair when VEC is 1; else the same two vectors in both layouts
+    p.e0 = INTER && VEC == 1 ? 2 * c : VEC * c;
+    p.e1 = INTER && VEC == 1 ? 2 * c + 1 : VEC * c + a.rd / 2;
+    p.second = true;
+    p.turn = kind < 2;
+  } else {
+    const int rest = (a.D - a.rd) / VEC, half = (rest + 1) / 2;
+    p.e0 = a.rd + VEC * (c - turning);
+    p.e1 = p.e0 + VEC * half;
+    p.second = c - turning + half < rest;
+    p.turn = false;
+  }
   float cs[VEC], sn[VEC];
-  if (pair && kind < 2) {
+  if (p.turn) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      const uint64_t turns = (uint64_t)(uint32_t)pos * __ldg(a.freqs + (VEC * c + j));
-      sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &sn[j], &cs[j]);
-      sn[j] *= a.m * a.sign;
-      cs[j] *= a.m;
+      // the pair's index: element e0 + j of the half layout; pairs of the two vectors
+      // one after the other in the interleaved one
+      const int i = INTER && VEC > 1 ? (j < VEC / 2 ? p.e0 / 2 + j : p.e1 / 2 + j - VEC / 2)
+                                     : VEC * c + j;
+      const uint64_t turns = (uint64_t)(uint32_t)pos * __ldg(a.freqs + i);
+      sine<IN>((int32_t)(turns >> 32), a.m, sn[j], cs[j]);
+      sn[j] *= a.sign;
     }
   }
   Rows r;
-  const bool turn = pair && kind < 2;
   if (kind == 0) {
     r = {a.q, a.qo, t * a.q_ts, t * a.qo_ts, a.q_hs, a.qo_hs};
-    rows_of<IN, IN, VEC, INTER>(r, g * hpt, min(a.Hq, (g + 1) * hpt), e0, e1, turn, pair, cs, sn,
-                                nullptr, 1.f);
+    rows_of<IN, IN, VEC, INTER>(r, g * hpt, min(a.Hq, (g + 1) * hpt), p, cs, sn, nullptr, 1.f);
     return;
   }
   g -= a.groups_q + (kind == 2 ? a.groups_k : 0);
   const int h0 = g * hpt, h1 = min(a.Hk, h0 + hpt);
   if (a.pool == nullptr) {
     r = {a.k, a.ko, t * a.k_ts, t * a.ko_ts, a.k_hs, a.ko_hs};
-    rows_of<IN, IN, VEC, INTER>(r, h0, h1, e0, e1, turn, pair, cs, sn, nullptr, 1.f);
+    rows_of<IN, IN, VEC, INTER>(r, h0, h1, p, cs, sn, nullptr, 1.f);
     return;
   }
   const int64_t s = a.seq_ids ? __ldg(a.seq_ids + t) : t;
@@ -182,7 +243,7 @@ __global__ void __launch_bounds__(512) rope_kernel(const RopeArgs a, int hpt) {
   r.out = a.pool;
   r.o_hs = (int64_t)a.BS * a.D;
   r.o0 = tile * r.o_hs + (int64_t)(pos % a.BS) * a.D;
-  rows_of<IN, KV, VEC, INTER>(r, h0, h1, e0, e1, turn, pair, cs, sn,
+  rows_of<IN, KV, VEC, INTER>(r, h0, h1, p, cs, sn,
                               KV == PKV_FP8_E4M3 && a.block_scales ? a.block_scales + tile
                                                                    : nullptr,
                               kind == 1 ? a.k_scale : a.v_scale);
@@ -214,7 +275,7 @@ cudaError_t run(const RopeArgs& a, dim3 grid, dim3 block, int hpt, cudaStream_t 
 template <int IN, int KV, int VEC>
 cudaError_t pick_layout(RopeArgs& a, int sms, cudaStream_t stream) {
   // parts of a row: the turning ones, then the copied rest (not copied in place)
-  const int parts = a.rd / (2 * VEC) + (a.copy_tail ? (a.D - a.rd) / VEC : 0);
+  const int parts = a.rd / (2 * VEC) + (a.copy_tail ? ((a.D - a.rd) / VEC + 1) / 2 : 0);
   const int rows = std::max(1, 256 / parts);
   // heads a thread visits: as many as leave every SM 1024 threads, so that a
   // sine is reused without idling SMs (a decode step visits one head a thread)

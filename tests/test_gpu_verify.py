@@ -106,6 +106,15 @@ def test_zeros_nan_and_values_above_one(pkv):
     _check(pkv, t, q, x, ua, us)
 
 
+@pytest.mark.parametrize("V", [200, 100000])
+def test_a_sum_above_64_saturates(pkv, V):
+    t, q, x, ua, us = _case(7, 2, V, seed=20)
+    t[:4] = 1.0
+    t[4:6, :, V // 2] = 1.0
+    _check(pkv, t, q, x, ua, us)
+    _check(pkv, t, None, x, ua, us)
+
+
 @pytest.mark.parametrize("V", [1000, 131072])
 def test_rows_without_mass_give_no_token_and_report_it(pkv, V):
     t, q, x, ua, us = _case(3, 2, V, seed=7)

@@ -580,7 +580,7 @@ typedef struct {
  *   w = max(p_a - q_a, 0)  if a < n (draft a was refused).
  * draft->data NULL: the drafts were not drawn (a lookup), q_j is 1 at x_j and 0
  * elsewhere.  The products u q are exact and the sums are 64-bit fixed point
- * (2^-56), so the result does not depend on the order of summation or on the
+ * (2^-54), so the result does not depend on the order of summation or on the
  * launch.  A residual without mass (w all 0) falls back to w = p_a.
  *   d_tokens       int32 [batch, max_drafts + 1]: the accepted drafts, the next
  *                  token, then -1

@@ -3,7 +3,7 @@
 //
 // Draft j is accepted while u_j q_j(x_j) < p_j(x_j).  With a accepted, the next
 // token is the lowest i with W_i > u W_last, W the running sum of w = max(p_a - q_a, 0)
-// (draft a refused) or p_a (none left).  The sums are fixed point in units of 2^-56:
+// (draft a refused) or p_a (none left).  The sums are fixed point in units of 2^-54:
 // integer addition is associative, so the token does not depend on how the row is
 // cut, and W_i > u W_last becomes W_i > floor(u W_last) exactly.
 //
@@ -12,6 +12,11 @@
 // another's shared memory; the CTA whose range holds the target finds the warp, and
 // all its threads read that warp's piece once more (it is in L2), each a few
 // consecutive elements, to find the token.
+//
+// Turning a float into 64-bit fixed point with shifts, and summing that, took 75
+// instructions an element and bound the kernel (9700 of 25000 cycles for one row of
+// 131072); two fp32 additions that truncate into the significand give the same
+// integers in 14, see Limbs.
 #include <algorithm>
 
 #include "device.cuh"
@@ -23,9 +28,9 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;             // CTAs of a cluster (the portable limit)
-constexpr int kStep = 8;                // elements a lane loads at a time, of each row
-constexpr int kWalk = 16;               // consecutive elements a thread walks in the search
-constexpr uint64_t kCap = 1ull << 62;   // 64.0: sums saturate here
+constexpr int kStep = 16;               // elements a lane loads at a time, of each row
+constexpr int kWalk = 4;                // consecutive elements a thread takes in the search
+constexpr uint64_t kCap = 1ull << 60;   // 64.0: sums saturate here
 
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -62,14 +67,45 @@ __device__ __forceinline__ void load4(const void* p, int64_t i, float* x) {
 // NaN and negative values are 0, values above 1 are 1.
 __device__ __forceinline__ float clean(float x) { return x > 0.f ? fminf(x, 1.f) : 0.f; }
 
-// clean(x) in units of 2^-56 (smaller parts are dropped): the 24-bit significand of
-// 2^(e - 127) shifted to its place.
+// floor(x 2^54) for x in [0, 1]: the 24-bit significand shifted to its place.
 __device__ __forceinline__ uint64_t fixed(float x) {
-  const uint32_t u = __float_as_uint(clean(x));
+  const uint32_t u = __float_as_uint(x);
   const uint32_t e = u >> 23;
-  const uint64_t sig = (uint64_t)((u & 0x7fffffu) | 0x800000u) << 33;
+  const uint64_t sig = (uint64_t)((u & 0x7fffffu) | 0x800000u) << 31;
   return sig >> min(127u - e, 63u);
 }
+
+// A sum of floor(x 2^54) in two limbs, 2^-31 and 2^-54, for x up to 2^-8: x 2^31 + 2^23
+// rounded toward zero has floor(x 2^31) in its significand, the rest (exact) times
+// 2^23 the lower limb.  Both significands are added with their exponent bits, which
+// `value` takes off again: `n` additions, at most 511.
+constexpr float kSmall = 0x1p-8f;
+struct Limbs {
+  uint32_t hi = 0, lo = 0;
+  __device__ __forceinline__ static void split(float x, uint32_t& h, uint32_t& l) {
+    const float y = x * 0x1p31f, t = __fadd_rz(y, 0x1p23f);
+    h = __float_as_uint(t);
+    l = __float_as_uint(__fmaf_rz(y - (t - 0x1p23f), 0x1p23f, 0x1p23f));
+  }
+  __device__ __forceinline__ void add(float x) {
+    uint32_t h, l;
+    split(x, h, l);
+    hi += h;
+    lo += l;
+  }
+  __device__ __forceinline__ void add_difference(float x, float y) {   // x >= y
+    uint32_t h, l, g, k;
+    split(x, h, l);
+    split(y, g, k);
+    hi += h - g;
+    lo += l - k;       // modulo 2^32; a negative sum of the limb is sign-extended
+  }
+  // n: the additions whose exponent bits did not cancel
+  __device__ __forceinline__ uint64_t value(int n) const {
+    const int32_t l = (int32_t)(lo - (uint32_t)n * 0x4b000000u);
+    return ((uint64_t)(hi - (uint32_t)n * 0x4b000000u) << 23) + (uint64_t)(int64_t)l;
+  }
+};
 
 __device__ __forceinline__ uint64_t add_sat(uint64_t a, uint64_t b) { return min(a + b, kCap); }
 
@@ -96,95 +132,154 @@ struct Row {
   int64_t zero;      // or -1
 };
 
-__device__ __forceinline__ uint64_t weight(float p, float q, bool zero) {
-  const uint64_t x = fixed(p), y = fixed(q);
-  return zero || x <= y ? 0 : x - y;
+__device__ __forceinline__ uint64_t weight(float p, float q) {
+  p = clean(p);
+  return fixed(p) - fixed(fminf(fmaxf(q, 0.f), p));
+}
+
+// The sum of a lane's weights, each max(p - q, 0) = p - min(p, q).
+template <bool Q>
+__device__ __forceinline__ uint64_t lane_sum(float (&p)[kStep], float (&q)[kStep]) {
+  float top = 0.f;
+#pragma unroll
+  for (int j = 0; j < kStep; ++j) {
+    p[j] = clean(p[j]);
+    if (Q) q[j] = fminf(fmaxf(q[j], 0.f), p[j]);
+    top = fmaxf(top, p[j]);
+  }
+  if (top > kSmall) {                // rare in a long row: at most 256 such probabilities
+    uint64_t s = 0;
+#pragma unroll 1
+    for (int j = 0; j < kStep; ++j) {
+      s += fixed(p[0]) - (Q ? fixed(q[0]) : 0);
+#pragma unroll
+      for (int i = 0; i + 1 < kStep; ++i) {      // shifted down: no indexed registers
+        p[i] = p[i + 1];
+        if (Q) q[i] = q[i + 1];
+      }
+    }
+    return s;
+  }
+  Limbs sum;
+#pragma unroll
+  for (int j = 0; j < kStep; ++j) {
+    if (Q) sum.add_difference(p[j], q[j]);
+    else sum.add(p[j]);
+  }
+  return sum.value(Q ? 0 : kStep);
 }
 
 // The sum of elements [lo, hi), by one warp: kStep elements a lane and step,
 // neighbouring lanes on neighbouring elements or (WIDE) groups of four.
-template <int DT, bool WIDE>
+template <int DT, bool WIDE, bool Q>
 __device__ __forceinline__ uint64_t piece_sum(const Row& r, int64_t lo, int64_t hi, int lane) {
   uint64_t s = 0;
   for (int64_t i0 = lo; i0 < hi; i0 += 32 * kStep) {
+    const int left = (int)min(hi - i0, (int64_t)32 * kStep);
     float p[kStep], q[kStep];
-    int64_t at[kStep];
 #pragma unroll
-    for (int j = 0; j < kStep; ++j) {
-      at[j] = WIDE ? i0 + (j / 4) * 128 + lane * 4 + j % 4 : i0 + j * 32 + lane;
-      p[j] = q[j] = 0.f;
-    }
+    for (int j = 0; j < kStep; ++j) p[j] = q[j] = 0.f;
     if constexpr (WIDE) {
 #pragma unroll
-      for (int j = 0; j < kStep; j += 4)
-        if (at[j] < hi) {              // lo and hi are multiples of 4
-          load4<DT>(r.p, at[j], p + j);
-          if (r.q) load4<DT>(r.q, at[j], q + j);
+      for (int j = 0; j < kStep; j += 4) {
+        const int at = j * 32 + lane * 4;
+        if (at < left) {             // lo and hi are multiples of 4
+          load4<DT>(r.p, i0 + at, p + j);
+          if (Q) load4<DT>(r.q, i0 + at, q + j);
         }
+      }
     } else {
 #pragma unroll
-      for (int j = 0; j < kStep; ++j)
-        if (at[j] < hi) {
-          p[j] = prob<DT>(r.p, at[j]);
-          if (r.q) q[j] = prob<DT>(r.q, at[j]);
+      for (int j = 0; j < kStep; ++j) {
+        const int at = j * 32 + lane;
+        if (at < left) {
+          p[j] = prob<DT>(r.p, i0 + at);
+          if (Q) q[j] = prob<DT>(r.q, i0 + at);
         }
+      }
     }
-    uint64_t t = 0;
+    if (!Q && r.zero >= i0 && r.zero < i0 + left) {
+      const int z = (int)(r.zero - i0);
 #pragma unroll
-    for (int j = 0; j < kStep; ++j) t += weight(p[j], q[j], at[j] == r.zero);
-    s = add_sat(s, t);
+      for (int j = 0; j < kStep; ++j)
+        if (z == (WIDE ? j / 4 * 128 + lane * 4 + j % 4 : j * 32 + lane)) p[j] = 0.f;
+    }
+    s = add_sat(s, lane_sum<Q>(p, q));
   }
   return warp_sum_sat(s);
 }
 
+template <int DT>
+__device__ __forceinline__ uint64_t piece_sum(const Row& r, int64_t lo, int64_t hi, int64_t V,
+                                              int lane) {
+  // rows of whole aligned groups of four are read four at a time
+  const uintptr_t at = reinterpret_cast<uintptr_t>(r.p) | reinterpret_cast<uintptr_t>(r.q);
+  if (at % (DT == PKV_F32 ? 16 : 8) == 0 && V % 4 == 0)
+    return r.q ? piece_sum<DT, true, true>(r, lo, hi, lane)
+               : piece_sum<DT, true, false>(r, lo, hi, lane);
+  return r.q ? piece_sum<DT, false, true>(r, lo, hi, lane)
+             : piece_sum<DT, false, false>(r, lo, hi, lane);
+}
+
+// The entry of x[0 .. n) (n <= 32) whose range of the running sum holds t, given that
+// one does; `before` (the sum ahead of x[0]) becomes the sum ahead of that entry.
+// Whole warps.
+__device__ __forceinline__ int entry_of(const uint64_t* x, int n, uint64_t t, uint64_t& before,
+                                        int lane) {
+  const uint64_t upto = add_sat(before, warp_scan_sat(lane < n ? x[lane] : 0, lane));
+  const uint32_t over = __ballot_sync(0xffffffffu, upto > t);
+  const int e = over ? __ffs(over) - 1 : n;
+  const uint64_t ahead = __shfl_sync(0xffffffffu, upto, e > 0 ? min(e, 32) - 1 : 0);
+  if (e > 0) before = ahead;
+  return e;
+}
+
 // Write the token that holds target t (`before` <= t: the sum ahead of the CTA's slice
 // at `base`): the warp's piece from the pieces' sums, then its elements, kWalk
-// consecutive ones a thread.  All threads of the CTA.
+// consecutive ones a thread and round.  All threads of the CTA.
 template <int DT>
 __device__ __forceinline__ void search(const Row& r, uint64_t t, uint64_t before,
                                        const uint64_t* sums, int64_t base, int64_t piece, int64_t V,
                                        int32_t* token) {
   __shared__ uint64_t found[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int w = 0;
-  for (; w < kWarps - 1; ++w) {
-    const uint64_t upto = add_sat(before, sums[w]);
-    if (t < upto) break;
-    before = upto;
-  }
+  const int w = entry_of(sums, kWarps, t, before, lane);
   const int64_t lo = base + w * piece, hi = min(V, lo + piece);
   for (int64_t i0 = lo; i0 < hi; i0 += kThreads * kWalk) {
     // a short piece is spread over all threads
-    const int64_t each = min((int64_t)kWalk, (hi - i0 + kThreads - 1) / kThreads);
+    const int each = (int)min((int64_t)kWalk, (hi - i0 + kThreads - 1) / kThreads);
     const int64_t i = i0 + tid * each;
-    uint64_t v[kWalk], s = 0;
+    float p[kWalk], q[kWalk];
 #pragma unroll
     for (int j = 0; j < kWalk; ++j) {
-      const bool in = j < each && i + j < hi;
-      const float p = in ? prob<DT>(r.p, i + j) : 0.f;
-      const float q = in && r.q ? prob<DT>(r.q, i + j) : 0.f;
-      v[j] = weight(p, q, i + j == r.zero);
-      s += v[j];
+      const bool in = j < each && i + j < hi && i + j != r.zero;
+      p[j] = in ? prob<DT>(r.p, i + j) : 0.f;
+      q[j] = in && r.q ? prob<DT>(r.q, i + j) : 0.f;
     }
+    uint64_t v[kWalk], s = 0;
+#pragma unroll
+    for (int j = 0; j < kWalk; ++j) s += v[j] = weight(p[j], q[j]);
     const uint64_t upto = warp_scan_sat(s, lane);
     if (lane == 31) found[warp] = upto;
     __syncthreads();
-    uint64_t ahead = before;                 // the sum before this thread's elements
-    for (int x = 0; x < warp; ++x) ahead = add_sat(ahead, found[x]);
-    const uint64_t end = add_sat(ahead, upto);
-    const uint64_t prev = __shfl_up_sync(0xffffffffu, upto, 1);
-    if (lane > 0) ahead = add_sat(ahead, prev);
-    if (ahead <= t && t < end) {
-      int at = 0;
+    const int hit = entry_of(found, kWarps, t, before, lane);
+    if (hit < kWarps) {
+      if (warp != hit) return;
+      const uint64_t end = add_sat(before, upto);
+      const uint32_t over = __ballot_sync(0xffffffffu, end > t);
+      const uint64_t prev = __shfl_up_sync(0xffffffffu, end, 1);
+      if (lane == __ffs(over) - 1) {
+        uint64_t ahead = lane > 0 ? prev : before;
+        int at = 0;
 #pragma unroll
-      for (int j = 0; j < kWalk; ++j) {
-        ahead = add_sat(ahead, v[j]);
-        if (ahead <= t) at = j + 1;
+        for (int j = 0; j < kWalk; ++j) {
+          ahead = add_sat(ahead, v[j]);
+          if (ahead <= t) at = j + 1;
+        }
+        *token = (int32_t)(i + at);
       }
-      *token = (int32_t)(i + at);
+      return;
     }
-    for (int x = 0; x < kWarps; ++x) before = add_sat(before, found[x]);
-    if (t < before) return;
     __syncthreads();                         // found is written again
   }
 }
@@ -200,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
 
   // accepted drafts: the first refused one, every CTA for itself
   int n = a.num_drafts ? __ldg(a.num_drafts + b) : a.K;
-  const double u = __ldg(a.u_sample + b);
+  const float u = __ldg(a.u_sample + b);
   if (n < 0 || n > a.K) {
     if (rank == 0 && tid == 0) record_error(a.status, PKV_EBOUNDS);
     n = min(max(n, 0), a.K);
@@ -217,15 +312,23 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     if (j >= n) break;
     bool ok = x >= 0 && x < a.V;
     if (ok) {
-      const float p = clean(prob<DT>(target, j * a.t_row + x));
-      const float q = draft ? clean(prob<DT>(draft, j * a.d_row + x)) : 1.f;
-      // a product of two 24-bit significands is exact in fp64
-      ok = p > 0.f && (double)ua * (double)q < (double)p;
+      const float p = clean(prob<DT>(target, j * a.t_row + x)) * 0x1p60f;
+      const float q = (draft ? clean(prob<DT>(draft, j * a.d_row + x)) : 1.f) * 0x1p60f;
+      // u q < p exactly: the rounded product decides unless it equals p, then its
+      // rounding error does (2^60 keeps that error a normal number)
+      const float h = ua * q, l = fmaf(ua, q, -h);
+      ok = p > 0.f && (h < p || (h == p && l < 0.f));
     } else {
       record_error(a.status, PKV_EBOUNDS);
     }
     if (!ok) atomicMin(&first, j);
   }
+  // u in units of 2^-64: NaN and negative 0, 1 and above the largest value below 1
+  const uint32_t ub = __float_as_uint(u);
+  const uint64_t u64 = !(u > 0.f) ? 0
+                       : u >= 1.f ? ~0ull
+                                  : (uint64_t)((ub & 0x7fffffu) | (ub >> 23 ? 0x800000u : 0u)) << 40
+                                        >> min(126u - (ub >> 23), 63u);
   __syncthreads();
   const int acc = first;
   const bool refused = acc < n;
@@ -234,58 +337,45 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
   row.q = refused && draft ? draft + (int64_t)acc * a.d_row * esize : nullptr;
   row.zero = refused && !draft ? __ldg(a.drafts + (int64_t)b * a.K + acc) : -1;
 
-  // every warp a contiguous piece of the CTA's slice, a multiple of 128 elements; a
-  // row of whole aligned groups of four is read four at a time
+  // every warp a contiguous piece of the CTA's slice, a multiple of 128 elements
   const int64_t unit = (int64_t)ctas * kWarps * 128;
   const int64_t piece = ((int64_t)a.V + unit - 1) / unit * 128;
   const int64_t lo = min((int64_t)a.V, ((int64_t)rank * kWarps + warp) * piece);
   const int64_t hi = min((int64_t)a.V, lo + piece);
 
   uint64_t all = 0, before = 0;
+  int owner = 0;
   for (int pass = 0;; ++pass) {
-    const uintptr_t off = reinterpret_cast<uintptr_t>(row.p) | reinterpret_cast<uintptr_t>(row.q);
-    const bool wide = off % (4 * esize) == 0 && a.V % 4 == 0;
-    const uint64_t s = wide ? piece_sum<DT, true>(row, lo, hi, lane)
-                            : piece_sum<DT, false>(row, lo, hi, lane);
+    const uint64_t s = piece_sum<DT>(row, lo, hi, a.V, lane);
     if (lane == 0) sums[warp] = s;
     __syncthreads();
-    if (ctas > 1) {
-      if (pass == 0) cluster_wait();         // all CTAs run
-      if (warp == 0) {
-        const uint64_t mine = warp_sum_sat(lane < kWarps ? sums[lane] : 0);
+    if (ctas > 1 && pass == 0) cluster_wait();   // all CTAs run
+    if (warp == 0) {
+      const uint64_t mine = warp_sum_sat(lane < kWarps ? sums[lane] : 0);
+      if (ctas > 1) {
         if (lane < ctas) store_to_cta(&totals[pass][rank], lane, mine);
+      } else if (lane == 0) {
+        totals[pass][0] = mine;
       }
+    }
+    if (ctas > 1) {
       cluster_arrive();
       cluster_wait();
     } else {
-      if (warp == 0) {
-        const uint64_t mine = warp_sum_sat(lane < kWarps ? sums[lane] : 0);
-        if (lane == 0) totals[pass][0] = mine;
-      }
       __syncthreads();
     }
-    all = before = 0;
-    uint64_t mine = 0;
-    for (int r = 0; r < ctas; ++r) {
-      const uint64_t x = totals[pass][r];
-      if (r < rank) before = add_sat(before, x);
-      if (r == rank) mine = x;
-      all = add_sat(all, x);
-    }
+    all = 0;
+#pragma unroll
+    for (int r = 0; r < kMaxCtas; ++r)
+      if (r < ctas) all = add_sat(all, totals[pass][r]);
     if (all > 0) {
-      if (rank == 0) {
-        for (int j = tid; j <= a.K; j += kThreads)
-          if (j != acc)
-            a.tokens[(int64_t)b * (a.K + 1) + j] =
-                j < acc ? __ldg(a.drafts + (int64_t)b * a.K + j) : -1;
-        if (tid == 0) a.num_accepted[b] = acc;
-      }
-      const uint64_t u64 = !(u > 0) ? 0 : u >= 1 ? ~0ull : (uint64_t)(u * 18446744073709551616.0);
       const uint64_t t = __umul64hi(u64, all);        // floor(u * all) < all
-      if (t < before || t >= add_sat(before, mine)) return;
-      search<DT>(row, t, before, sums, rank * kWarps * piece, piece, a.V,
-                 a.tokens + (int64_t)b * (a.K + 1) + acc);
-      return;
+      before = 0;
+      owner = entry_of(totals[pass], ctas, t, before, lane);
+      if (owner == rank)
+        search<DT>(row, t, before, sums, (int64_t)rank * kWarps * piece, piece, a.V,
+                   a.tokens + (int64_t)b * (a.K + 1) + acc);
+      break;
     }
     if (row.q == nullptr && row.zero < 0) break;
     row.q = nullptr;                         // a residual without mass: the target itself
@@ -293,11 +383,12 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
   }
   if (rank == 0) {
     for (int j = tid; j <= a.K; j += kThreads)
-      a.tokens[(int64_t)b * (a.K + 1) + j] =
-          j < acc ? __ldg(a.drafts + (int64_t)b * a.K + j) : -1;
+      if (j != acc || all == 0)
+        a.tokens[(int64_t)b * (a.K + 1) + j] =
+            j < acc ? __ldg(a.drafts + (int64_t)b * a.K + j) : -1;
     if (tid == 0) {
       a.num_accepted[b] = acc;
-      record_error(a.status, PKV_EINVAL);
+      if (all == 0) record_error(a.status, PKV_EINVAL);
     }
   }
 }

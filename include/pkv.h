@@ -590,7 +590,7 @@ typedef struct {
  *   d_drafts       int32 [batch, max_drafts]; d_u_accept f32 of that shape and
  *                  d_u_sample f32 [batch], uniform in [0, 1)
  * NaN and negative probabilities count as 0, ones above 1 as 1, and a row's sum
- * saturates at 64; a draft of p = 0 is refused; a NaN u refuses
+ * saturates at 16; a draft of p = 0 is refused; a NaN u refuses
  * (u_accept) or counts as 0 (u_sample), a u_sample of 1 or more as the largest
  * value below 1.  d_status: device int32 (zero: no error) that takes the first error,
  * as a pool's status word does, or NULL.  A refused-by-range draft (an id outside

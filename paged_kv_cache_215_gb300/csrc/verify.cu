@@ -27,10 +27,10 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCtas = 8;             // CTAs of a cluster (the portable limit)
+constexpr int kMaxCtas = 16;            // CTAs of a cluster
 constexpr int kStep = 16;               // elements a lane loads at a time, of each row
 constexpr int kWalk = 4;                // consecutive elements a thread takes in the search
-constexpr uint64_t kCap = 1ull << 60;   // 64.0: sums saturate here
+constexpr uint64_t kCap = 1ull << 58;   // 16.0: sums saturate here
 
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -75,17 +75,17 @@ __device__ __forceinline__ uint64_t fixed(float x) {
   return sig >> min(127u - e, 63u);
 }
 
-// A sum of floor(x 2^54) in two limbs, 2^-31 and 2^-54, for x up to 2^-8: x 2^31 + 2^23
-// rounded toward zero has floor(x 2^31) in its significand, the rest (exact) times
-// 2^23 the lower limb.  Both significands are added with their exponent bits, which
-// `value` takes off again: `n` additions, at most 511.
+// A sum of floor(x 2^54) in two limbs, 2^-31 and 2^-54, for x in [0, 2^-8]:
+// 2^-8 + x rounded toward zero has floor(x 2^31) in its significand, and 2^-31 plus
+// the rest of x (exact) the lower limb.  The words are added with their exponent
+// bits, which `value` takes off again: n additions, at most 511.
 constexpr float kSmall = 0x1p-8f;
 struct Limbs {
   uint32_t hi = 0, lo = 0;
   __device__ __forceinline__ static void split(float x, uint32_t& h, uint32_t& l) {
-    const float y = x * 0x1p31f, t = __fadd_rz(y, 0x1p23f);
+    const float t = __fadd_rz(x, 0x1p-8f);
     h = __float_as_uint(t);
-    l = __float_as_uint(__fmaf_rz(y - (t - 0x1p23f), 0x1p23f, 0x1p23f));
+    l = __float_as_uint(__fadd_rz(x - (t - 0x1p-8f), 0x1p-31f));
   }
   __device__ __forceinline__ void add(float x) {
     uint32_t h, l;
@@ -98,21 +98,23 @@ struct Limbs {
     split(x, h, l);
     split(y, g, k);
     hi += h - g;
-    lo += l - k;       // modulo 2^32; a negative sum of the limb is sign-extended
+    lo += l - k;       // modulo 2^32: a negative sum of the limb is sign-extended below
   }
   // n: the additions whose exponent bits did not cancel
   __device__ __forceinline__ uint64_t value(int n) const {
-    const int32_t l = (int32_t)(lo - (uint32_t)n * 0x4b000000u);
-    return ((uint64_t)(hi - (uint32_t)n * 0x4b000000u) << 23) + (uint64_t)(int64_t)l;
+    const int32_t l = (int32_t)(lo - (uint32_t)n * 0x30000000u);
+    return ((uint64_t)(hi - (uint32_t)n * 0x3b800000u) << 23) + (uint64_t)(int64_t)l;
   }
 };
 
+// Sums saturate at kCap.  Up to 32 of them are added without overflow, so a warp
+// limits its sum once, at the end.
 __device__ __forceinline__ uint64_t add_sat(uint64_t a, uint64_t b) { return min(a + b, kCap); }
 
 __device__ __forceinline__ uint64_t warp_sum_sat(uint64_t v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = add_sat(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return min(v, kCap);
 }
 
 // Inclusive running sum over the warp's lanes.
@@ -120,9 +122,9 @@ __device__ __forceinline__ uint64_t warp_scan_sat(uint64_t v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint64_t y = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v = add_sat(v, y);
+    if (lane >= o) v += y;
   }
-  return v;
+  return min(v, kCap);
 }
 
 // One sequence's row of weights: max(p - q, 0), or p without the token `zero`.
@@ -143,7 +145,7 @@ __device__ __forceinline__ uint64_t lane_sum(float (&p)[kStep], float (&q)[kStep
   float top = 0.f;
 #pragma unroll
   for (int j = 0; j < kStep; ++j) {
-    p[j] = clean(p[j]);
+    p[j] = fmaxf(p[j], 0.f);         // NaN: 0
     if (Q) q[j] = fminf(fmaxf(q[j], 0.f), p[j]);
     top = fmaxf(top, p[j]);
   }
@@ -151,7 +153,7 @@ __device__ __forceinline__ uint64_t lane_sum(float (&p)[kStep], float (&q)[kStep
     uint64_t s = 0;
 #pragma unroll 1
     for (int j = 0; j < kStep; ++j) {
-      s += fixed(p[0]) - (Q ? fixed(q[0]) : 0);
+      s += fixed(fminf(p[0], 1.f)) - (Q ? fixed(fminf(q[0], 1.f)) : 0);
 #pragma unroll
       for (int i = 0; i + 1 < kStep; ++i) {      // shifted down: no indexed registers
         p[i] = p[i + 1];
@@ -169,6 +171,24 @@ __device__ __forceinline__ uint64_t lane_sum(float (&p)[kStep], float (&q)[kStep
   return sum.value(Q ? 0 : kStep);
 }
 
+// A lane's share of elements [i0, i0 + left); FULL: left is 32 kStep.
+template <int DT, bool WIDE, bool Q, bool FULL>
+__device__ __forceinline__ void load_step(const Row& r, int64_t i0, int left, int lane,
+                                          float (&p)[kStep], float (&q)[kStep]) {
+#pragma unroll
+  for (int j = 0; j < kStep; j += WIDE ? 4 : 1) {
+    const int at = j * 32 + lane * (WIDE ? 4 : 1);
+    if (!FULL && at >= left) continue;       // WIDE: left is a multiple of 4
+    if constexpr (WIDE) {
+      load4<DT>(r.p, i0 + at, p + j);
+      if (Q) load4<DT>(r.q, i0 + at, q + j);
+    } else {
+      p[j] = prob<DT>(r.p, i0 + at);
+      if (Q) q[j] = prob<DT>(r.q, i0 + at);
+    }
+  }
+}
+
 // The sum of elements [lo, hi), by one warp: kStep elements a lane and step,
 // neighbouring lanes on neighbouring elements or (WIDE) groups of four.
 template <int DT, bool WIDE, bool Q>
@@ -177,26 +197,12 @@ __device__ __forceinline__ uint64_t piece_sum(const Row& r, int64_t lo, int64_t 
   for (int64_t i0 = lo; i0 < hi; i0 += 32 * kStep) {
     const int left = (int)min(hi - i0, (int64_t)32 * kStep);
     float p[kStep], q[kStep];
-#pragma unroll
-    for (int j = 0; j < kStep; ++j) p[j] = q[j] = 0.f;
-    if constexpr (WIDE) {
-#pragma unroll
-      for (int j = 0; j < kStep; j += 4) {
-        const int at = j * 32 + lane * 4;
-        if (at < left) {             // lo and hi are multiples of 4
-          load4<DT>(r.p, i0 + at, p + j);
-          if (Q) load4<DT>(r.q, i0 + at, q + j);
-        }
-      }
+    if (left == 32 * kStep) {
+      load_step<DT, WIDE, Q, true>(r, i0, left, lane, p, q);
     } else {
 #pragma unroll
-      for (int j = 0; j < kStep; ++j) {
-        const int at = j * 32 + lane;
-        if (at < left) {
-          p[j] = prob<DT>(r.p, i0 + at);
-          if (Q) q[j] = prob<DT>(r.q, i0 + at);
-        }
-      }
+      for (int j = 0; j < kStep; ++j) p[j] = q[j] = 0.f;
+      load_step<DT, WIDE, Q, false>(r, i0, left, lane, p, q);
     }
     if (!Q && r.zero >= i0 && r.zero < i0 + left) {
       const int z = (int)(r.zero - i0);
@@ -398,6 +404,11 @@ cudaError_t run(const VerifyArgs& a, int ctas, cudaStream_t stream) {
   if (ctas == 1) {
     verify_kernel<DT><<<(unsigned)a.B, kThreads, 0, stream>>>(a, 1);
     return cudaGetLastError();
+  }
+  if (ctas > 8) {                            // above the portable cluster size
+    const cudaError_t e = cudaFuncSetAttribute(
+        verify_kernel<DT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.B * ctas));

@@ -109,7 +109,7 @@ def verify(target, draft, drafts, u_accept, u_sample, num_drafts=None):
                 w = row
         u = float(us[s])
         u = 0.0 if not u > 0 else min(u, 1 - 2.0 ** -53)
-        total = np.minimum(np.cumsum(w), 64.0)
+        total = np.minimum(np.cumsum(w), 16.0)
         if total[-1] == 0:
             new = -1
         else:

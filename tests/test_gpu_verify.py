@@ -107,7 +107,7 @@ def test_zeros_nan_and_values_above_one(pkv):
 
 
 @pytest.mark.parametrize("V", [200, 100000])
-def test_a_sum_above_64_saturates(pkv, V):
+def test_a_sum_above_16_saturates(pkv, V):
     t, q, x, ua, us = _case(7, 2, V, seed=20)
     t[:4] = 1.0
     t[4:6, :, V // 2] = 1.0

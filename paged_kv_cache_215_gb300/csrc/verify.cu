@@ -349,8 +349,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
   const int64_t lo = min((int64_t)a.V, ((int64_t)rank * kWarps + warp) * piece);
   const int64_t hi = min((int64_t)a.V, lo + piece);
 
-  uint64_t all = 0, before = 0;
-  int owner = 0;
+  uint64_t all = 0;
   for (int pass = 0;; ++pass) {
     const uint64_t s = piece_sum<DT>(row, lo, hi, a.V, lane);
     if (lane == 0) sums[warp] = s;
@@ -370,14 +369,14 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     } else {
       __syncthreads();
     }
-    all = 0;
-#pragma unroll
-    for (int r = 0; r < kMaxCtas; ++r)
-      if (r < ctas) all = add_sat(all, totals[pass][r]);
+    // every warp for itself: the CTAs' running sums, one a lane
+    const uint64_t upto = warp_scan_sat(lane < ctas ? totals[pass][lane] : 0, lane);
+    all = __shfl_sync(0xffffffffu, upto, 31);
     if (all > 0) {
       const uint64_t t = __umul64hi(u64, all);        // floor(u * all) < all
-      before = 0;
-      owner = entry_of(totals[pass], ctas, t, before, lane);
+      const int owner = __ffs(__ballot_sync(0xffffffffu, upto > t)) - 1;
+      const uint64_t before =
+          owner > 0 ? __shfl_sync(0xffffffffu, upto, owner - 1) : 0;
       if (owner == rank)
         search<DT>(row, t, before, sums, (int64_t)rank * kWarps * piece, piece, a.V,
                    a.tokens + (int64_t)b * (a.K + 1) + acc);

@@ -32,6 +32,38 @@ __host__ __device__ constexpr int elem_size(int dtype) {
   return dtype == PKV_F32 ? 4 : dtype == PKV_FP8_E4M3 ? 1 : 2;
 }
 
+// E4M3 codes of x / scale (IEEE fp32 quotient, then rounded), mostly without the
+// division.  lo and hi are the reciprocal made 2^-21 smaller and larger, more than the
+// three roundings in between (2^-24 each) amount to, so the quotient lies between
+// x lo and x hi.  Rounding to codes is monotone: where both give one code, that is the
+// quotient's.  Otherwise (a boundary within 2^-20 of the value) the division is made.
+struct Quant {
+  float scale, lo, hi;
+  bool usable;       // the reciprocal is a normal number
+  __device__ __forceinline__ static Quant of(float s) {
+    const float r = __frcp_rn(s);
+    return {s, r * (1.f - 0x1p-21f), r * (1.f + 0x1p-21f), s > 0x1p-100f && s < 0x1p100f};
+  }
+  template <int N>
+  __device__ __forceinline__ void encode(const float (&x)[N], uint8_t (&out)[N]) const {
+    constexpr int M = (N + 1) / 2;
+    uint32_t c[M], differ = !usable;
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const float u = x[2 * j], v = N > 1 ? x[2 * j + 1] : 0.f;
+      c[j] = __nv_cvt_float2_to_fp8x2(make_float2(u * lo, v * lo), __NV_SATFINITE, __NV_E4M3);
+      differ |= c[j] ^ __nv_cvt_float2_to_fp8x2(make_float2(u * hi, v * hi), __NV_SATFINITE,
+                                                __NV_E4M3);
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) out[j] = (uint8_t)(c[j / 2] >> (j % 2 * 8));
+    if (differ) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) out[j] = encode_e4m3(x[j], scale);
+    }
+  }
+};
+
 // VEC elements of type DT, as loaded.
 template <int DT, int VEC>
 struct Vec {
@@ -43,7 +75,14 @@ struct Vec {
     uint8_t b[elem_size(DT) * VEC];
   };
   __device__ __forceinline__ void load(const void* base, int64_t i) {
-    r = *reinterpret_cast<const R*>(static_cast<const char*>(base) + i * elem_size(DT));
+    const void* p = static_cast<const char*>(base) + i * elem_size(DT);
+    if constexpr (DT == PKV_F32 && sizeof(R) == 16) {   // read once: not kept in L1 (8% faster)
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "l"(p));
+    } else {
+      r = *static_cast<const R*>(p);
+    }
   }
   __device__ __forceinline__ void store(void* base, int64_t i) const {
     *reinterpret_cast<R*>(static_cast<char*>(base) + i * elem_size(DT)) = r;
@@ -65,13 +104,12 @@ struct Vec {
     }
   }
   // Rounded to DT; E4M3: x / scale, as kv_append encodes.
-  __device__ __forceinline__ void set(const float (&x)[VEC], float scale) {
+  __device__ __forceinline__ void set(const float (&x)[VEC], const Quant& s) {
     if constexpr (DT == PKV_F32) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) w[j] = __float_as_uint(x[j]);
     } else if constexpr (DT == PKV_FP8_E4M3) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) b[j] = encode_e4m3(x[j], scale);
+      s.template encode<VEC>(x, b);
     } else if constexpr (VEC == 1) {
       h[0] = DT == PKV_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x[0]))
                             : __half_as_ushort(__float2half_rn(x[0]));
@@ -104,88 +142,91 @@ struct Part {
   bool turn;        // rotate, otherwise copy
 };
 
-struct Rows {
-  const void* in;
-  void* out;
-  int64_t i0, o0;       // element offsets of the token's first head
-  int64_t i_hs, o_hs;   // head strides
+// Two shapes of the kernel.  Few: a thread takes one head, with few registers and
+// little code, so that a decode step is one wave of short blocks.  Many: a thread
+// takes kManyHeads heads, all loaded before the first is used, and its sines serve
+// them all.  Blocks of 128 threads drain and refill the SMs evenly (256 threads at
+// the same occupancy: 29 instead of 27 us on the 8K-token prompt); the blocks per SM
+// are the fastest of 4 to 10 for each type.
+constexpr int kThreads = 128, kFewBlocks = 10, kManyHeads = 4;
+__host__ __device__ constexpr int blocks_of(int in, int kv, bool many) {
+  return !many ? kFewBlocks : kv == PKV_FP8_E4M3 ? 5 : in == PKV_F32 ? 7 : 6;
+}
+
+template <int IN, int VEC, int N>
+struct Loaded {
+  Vec<IN, VEC> a[N], b[N];
+  // heads h .. h + N of the token whose first head is at `in`, up to h1
+  __device__ __forceinline__ void load(const void* in, int64_t i0, int64_t hs, int h, int h1,
+                                       const Part& p) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (N == 1 || h + i < h1) {
+        const int64_t at = i0 + (h + i) * hs;
+        a[i].load(in, at + p.e0);
+        if (p.second) b[i].load(in, at + p.e1);
+      }
+  }
 };
 
-// Loads in flight a thread: kBatch heads at a time, all loaded before the first is used.
-constexpr int kBatch = 4;
-
+// One head's part, rotated or copied, and stored as type KV.
 template <int IN, int KV, int VEC, bool INTER>
-__device__ __forceinline__ void rows_of(const Rows& r, int h0, int h1, const Part& p,
-                                        const float (&cs)[VEC], const float (&sn)[VEC],
-                                        const float* scales, float scale) {
-  for (int hb = h0; hb < h1; hb += kBatch) {
-    Vec<IN, VEC> a[kBatch], b[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (hb + i < h1) {
-        const int64_t at = r.i0 + (hb + i) * r.i_hs;
-        a[i].load(r.in, at + p.e0);
-        if (p.second) b[i].load(r.in, at + p.e1);
-      }
+__device__ __forceinline__ void put(void* out, int64_t to, const Vec<IN, VEC>& a,
+                                    const Vec<IN, VEC>& b, const Part& p, const float (&cs)[VEC],
+                                    const float (&sn)[VEC], const Quant& quant) {
+  if constexpr (KV == IN) {
+    if (!p.turn) {
+      a.store(out, to + p.e0);
+      if (p.second) b.store(out, to + p.e1);
+      return;
     }
+  }
+  float x[VEC], y[VEC];
+  a.get(x);
+  if (p.second) b.get(y);
+  if (p.turn) {
+    if constexpr (INTER && VEC > 1) {
+      // pairs (0, 1), (2, 3) ... of each vector
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (hb + i >= h1) break;
-      const int64_t to = r.o0 + (hb + i) * r.o_hs;
-      if constexpr (KV == IN) {
-        if (!p.turn) {
-          a[i].store(r.out, to + p.e0);
-          if (p.second) b[i].store(r.out, to + p.e1);
-          continue;
-        }
+      for (int j = 0; j < VEC; j += 2) {
+        const float u = x[j], v = x[j + 1], s = y[j], t = y[j + 1];
+        const int k = j / 2, l = VEC / 2 + j / 2;
+        x[j] = u * cs[k] - v * sn[k];
+        x[j + 1] = u * sn[k] + v * cs[k];
+        y[j] = s * cs[l] - t * sn[l];
+        y[j + 1] = s * sn[l] + t * cs[l];
       }
-      const float sc = scales ? scales[hb + i] : scale;
-      float x[VEC], y[VEC];
-      a[i].get(x);
-      if (p.second) b[i].get(y);
-      if (p.turn) {
-        if constexpr (INTER && VEC > 1) {
-          // pairs (0, 1), (2, 3) ... of each vector
+    } else {
 #pragma unroll
-          for (int j = 0; j < VEC; j += 2) {
-            const float u = x[j], v = x[j + 1], s = y[j], t = y[j + 1];
-            const int k = j / 2, l = VEC / 2 + j / 2;
-            x[j] = u * cs[k] - v * sn[k];
-            x[j + 1] = u * sn[k] + v * cs[k];
-            y[j] = s * cs[l] - t * sn[l];
-            y[j + 1] = s * sn[l] + t * cs[l];
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const float u = x[j], v = y[j];
-            x[j] = u * cs[j] - v * sn[j];
-            y[j] = u * sn[j] + v * cs[j];
-          }
-        }
-      }
-      Vec<KV, VEC> o;
-      o.set(x, sc);
-      o.store(r.out, to + p.e0);
-      if (p.second) {
-        o.set(y, sc);
-        o.store(r.out, to + p.e1);
+      for (int j = 0; j < VEC; ++j) {
+        const float u = x[j], v = y[j];
+        x[j] = u * cs[j] - v * sn[j];
+        y[j] = u * sn[j] + v * cs[j];
       }
     }
   }
+  Vec<KV, VEC> o;
+  o.set(x, quant);
+  o.store(out, to + p.e0);
+  if (p.second) {
+    o.set(y, quant);
+    o.store(out, to + p.e1);
+  }
 }
 
-// grid (token groups, head groups): head groups of q first, then of k, then (with a
-// pool) of v; block (parts of a row, tokens).
-template <int IN, int KV, int VEC, bool INTER>
-__global__ void __launch_bounds__(512) rope_kernel(const RopeArgs a, int hpt) {
+// grid (token groups, head groups, part groups): head groups of q first, then of k,
+// then (with a pool) of v; block (parts of a row, tokens).
+template <int IN, int KV, int VEC, bool INTER, bool MANY>
+__global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
+    rope_kernel(const RopeArgs a, int parts) {
+  constexpr int N = MANY ? kManyHeads : 1;
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  if (t >= a.T) return;
-  const int pos = __ldg(a.positions + t);
-  if (pos < 0) return;                       // padding: no token
+  const int c = blockIdx.z * blockDim.x + threadIdx.x;
+  if (t >= a.T || c >= parts) return;
   int g = blockIdx.y;
   const int kind = g < a.groups_q ? 0 : g < a.groups_q + a.groups_k ? 1 : 2;
-  const int c = threadIdx.x, turning = a.rd / (2 * VEC);
+  if (kind > 0) g -= a.groups_q + (kind == 2 ? a.groups_k : 0);
+  const int turning = a.rd / (2 * VEC);
   Part p;
   if (c < turning) {
     // one interleaved pair when VEC is 1; else the same two vectors in both layouts
@@ -200,6 +241,16 @@ __global__ void __launch_bounds__(512) rope_kernel(const RopeArgs a, int hpt) {
     p.second = c - turning + half < rest;
     p.turn = false;
   }
+  // the heads' loads go out before the position is known
+  const void* in = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+  const int64_t i0 = t * (kind == 0 ? a.q_ts : kind == 1 ? a.k_ts : a.v_ts);
+  const int64_t i_hs = kind == 0 ? a.q_hs : kind == 1 ? a.k_hs : a.v_hs;
+  const int h = g * N;
+  const int h1 = min(kind == 0 ? a.Hq : a.Hk, h + N);
+  const int pos = __ldg(a.positions + t);
+  Loaded<IN, VEC, N> x;
+  x.load(in, i0, i_hs, h, h1, p);
+  if (pos < 0) return;                       // padding: no token
   float cs[VEC], sn[VEC];
   if (p.turn) {
 #pragma unroll
@@ -213,17 +264,14 @@ __global__ void __launch_bounds__(512) rope_kernel(const RopeArgs a, int hpt) {
       sn[j] *= a.sign;
     }
   }
-  Rows r;
-  if (kind == 0) {
-    r = {a.q, a.qo, t * a.q_ts, t * a.qo_ts, a.q_hs, a.qo_hs};
-    rows_of<IN, IN, VEC, INTER>(r, g * hpt, min(a.Hq, (g + 1) * hpt), p, cs, sn, nullptr, 1.f);
-    return;
-  }
-  g -= a.groups_q + (kind == 2 ? a.groups_k : 0);
-  const int h0 = g * hpt, h1 = min(a.Hk, h0 + hpt);
-  if (a.pool == nullptr) {
-    r = {a.k, a.ko, t * a.k_ts, t * a.ko_ts, a.k_hs, a.ko_hs};
-    rows_of<IN, IN, VEC, INTER>(r, h0, h1, p, cs, sn, nullptr, 1.f);
+  if (kind == 0 || a.pool == nullptr) {
+    void* out = kind == 0 ? a.qo : a.ko;
+    const int64_t o0 = t * (kind == 0 ? a.qo_ts : a.ko_ts);
+    const int64_t o_hs = kind == 0 ? a.qo_hs : a.ko_hs;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (N == 1 || h + i < h1)
+        put<IN, IN, VEC, INTER>(out, o0 + (h + i) * o_hs, x.a[i], x.b[i], p, cs, sn, Quant::of(1.f));
     return;
   }
   const int64_t s = a.seq_ids ? __ldg(a.seq_ids + t) : t;
@@ -237,16 +285,15 @@ __global__ void __launch_bounds__(512) rope_kernel(const RopeArgs a, int hpt) {
     return;
   }
   const int64_t tile = (((int64_t)blk * 2 + (kind - 1)) * a.L + a.layer) * a.Hk;
-  r.in = kind == 1 ? a.k : a.v;
-  r.i0 = t * (kind == 1 ? a.k_ts : a.v_ts);
-  r.i_hs = kind == 1 ? a.k_hs : a.v_hs;
-  r.out = a.pool;
-  r.o_hs = (int64_t)a.BS * a.D;
-  r.o0 = tile * r.o_hs + (int64_t)(pos % a.BS) * a.D;
-  rows_of<IN, KV, VEC, INTER>(r, h0, h1, p, cs, sn,
-                              KV == PKV_FP8_E4M3 && a.block_scales ? a.block_scales + tile
-                                                                   : nullptr,
-                              kind == 1 ? a.k_scale : a.v_scale);
+  const int64_t o_hs = (int64_t)a.BS * a.D;
+  const int64_t o0 = tile * o_hs + (int64_t)(pos % a.BS) * a.D;
+  const float scale = kind == 1 ? a.k_scale : a.v_scale;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (N == 1 || h + i < h1)
+      put<IN, KV, VEC, INTER>(
+          a.pool, o0 + (h + i) * o_hs, x.a[i], x.b[i], p, cs, sn,
+          Quant::of(KV == PKV_FP8_E4M3 && a.block_scales ? a.block_scales[tile + h + i] : scale));
 }
 
 // The widest part (elements) every row can be loaded and stored in: parts lie in
@@ -266,41 +313,42 @@ int widest(const RopeArgs& a) {
   return 1;
 }
 
-template <int IN, int KV, int VEC, bool INTER>
-cudaError_t run(const RopeArgs& a, dim3 grid, dim3 block, int hpt, cudaStream_t stream) {
-  rope_kernel<IN, KV, VEC, INTER><<<grid, block, 0, stream>>>(a, hpt);
+template <int IN, int KV, int VEC, bool MANY>
+cudaError_t run(RopeArgs& a, int parts, cudaStream_t stream) {
+  const int across = std::min(parts, kThreads), rows = kThreads / across;
+  const int heads = MANY ? kManyHeads : 1;
+  a.groups_q = (a.Hq + heads - 1) / heads;
+  a.groups_k = (a.Hk + heads - 1) / heads;
+  const int64_t gx = (a.T + rows - 1) / rows;
+  const int64_t gy = (int64_t)a.groups_q + a.groups_k * (a.pool ? 2 : 1);
+  if (gx > 0x7fffffff || gy > 65535) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)gx, (unsigned)gy, (parts + kThreads - 1) / kThreads);
+  const dim3 block(across, rows);
+  if (a.interleaved) rope_kernel<IN, KV, VEC, true, MANY><<<grid, block, 0, stream>>>(a, parts);
+  else rope_kernel<IN, KV, VEC, false, MANY><<<grid, block, 0, stream>>>(a, parts);
   return cudaGetLastError();
 }
 
 template <int IN, int KV, int VEC>
-cudaError_t pick_layout(RopeArgs& a, int sms, cudaStream_t stream) {
+cudaError_t pick_shape(RopeArgs& a, int sms, cudaStream_t stream) {
   // parts of a row: the turning ones, then the copied rest (not copied in place)
   const int parts = a.rd / (2 * VEC) + (a.copy_tail ? ((a.D - a.rd) / VEC + 1) / 2 : 0);
-  const int rows = std::max(1, 256 / parts);
-  // heads a thread visits: as many as leave every SM 1024 threads, so that a
-  // sine is reused without idling SMs (a decode step visits one head a thread)
   const int64_t heads = (int64_t)a.Hq + a.Hk * (a.pool ? 2 : 1);
-  int hpt = 1;
-  while (hpt < 8 && a.T * heads * parts / (2 * hpt) >= (int64_t)sms * 1024) hpt *= 2;
-  a.groups_q = (a.Hq + hpt - 1) / hpt;
-  a.groups_k = (a.Hk + hpt - 1) / hpt;
-  const int64_t gx = (a.T + rows - 1) / rows;
-  const int64_t gy = (int64_t)a.groups_q + a.groups_k * (a.pool ? 2 : 1);
-  if (gx > 0x7fffffff || gy > 65535) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)gx, (unsigned)gy), block(parts, rows);
-  return a.interleaved ? run<IN, KV, VEC, true>(a, grid, block, hpt, stream)
-                       : run<IN, KV, VEC, false>(a, grid, block, hpt, stream);
+  // one head a thread while that is one wave of blocks (beyond it, 33 instead of 27 us
+  // on the 8K-token prompt)
+  const bool many = a.T * heads * parts > (int64_t)sms * kFewBlocks * kThreads;
+  return many ? run<IN, KV, VEC, true>(a, parts, stream) : run<IN, KV, VEC, false>(a, parts, stream);
 }
 
 template <int IN, int KV>
 cudaError_t pick_width(RopeArgs& a, int sms, cudaStream_t stream) {
   switch (widest(a)) {
     case 8:
-      if constexpr (IN != PKV_F32) return pick_layout<IN, KV, 8>(a, sms, stream);
+      if constexpr (IN != PKV_F32) return pick_shape<IN, KV, 8>(a, sms, stream);
       return cudaErrorInvalidValue;
-    case 4: return pick_layout<IN, KV, 4>(a, sms, stream);
-    case 2: return pick_layout<IN, KV, 2>(a, sms, stream);
-    default: return pick_layout<IN, KV, 1>(a, sms, stream);
+    case 4: return pick_shape<IN, KV, 4>(a, sms, stream);
+    case 2: return pick_shape<IN, KV, 2>(a, sms, stream);
+    default: return pick_shape<IN, KV, 1>(a, sms, stream);
   }
 }
 

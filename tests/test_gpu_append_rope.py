@@ -215,6 +215,44 @@ def test_e4m3_saturation_and_non_finite_values(pkv):
     assert got[blk, 1, 0, 0, off + 1, :3].tolist() == [0x7F, 0x7E, 0xFE]
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_e4m3_codes_equal_those_of_append(pkv, dt):
+    """Every 16-bit value (and fp32 values around the boundaries between codes) under
+    scales that put them anywhere: the same bytes as append_tokens stores, values in
+    any position, keys at position 0 (angle 0)."""
+    hk, D, bs = 4, 128, 16
+    if dt == "f32":
+        # quotients within a few steps of the midpoint between two codes, times the scale
+        codes = np.arange(0x08, 0x7E, dtype=np.uint8)
+        mid = (oracle.e4m3_decode(codes) + oracle.e4m3_decode(codes + 1)) / 2
+        u = mid.astype(np.float32).view(np.uint32).astype(np.int64)[:, None] + np.arange(-24, 25)
+        base = torch.from_numpy(u.astype(np.uint32).view(np.float32).reshape(-1).copy())
+    else:
+        base = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(IN[dt])
+    for scale in (1.0, 1.0 / 448, 0.0123456, 3.7e-5, 55.5, 2.0 ** -130, 2.0 ** 110):
+        x = base if dt != "f32" else (base.double() * scale).float()
+        T = -(-x.numel() // (hk * D))
+        v = torch.zeros(T * hk * D, dtype=x.dtype)
+        v[:x.numel()] = x
+        v = v.view(T, hk, D).cuda()
+        k = torch.where(torch.isfinite(v), v, torch.zeros_like(v))
+        geom = pkv.geometry(1, hk, hk, D, bs, T, "e4m3")
+        a, b = (pkv.KVPool(geom, storage=torch.zeros(pkv.kv_pool_bytes(geom), dtype=torch.uint8,
+                                                     device="cuda")) for _ in range(2))
+        # every token at position 0 of a sequence of its own
+        tab = torch.arange(T, dtype=torch.int32, device="cuda").view(T, 1)
+        pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+        seq = torch.arange(T, dtype=torch.int32, device="cuda")
+        a.append_tokens(0, k, v, tab, seq, pos, scale, scale)
+        b.append_rope(0, None, None, k, v, pkv.Rope(D), tab, pos, k_scale=scale, v_scale=scale)
+        got, want = b.view(), a.view()
+        assert torch.equal(got[:, 1], want[:, 1]), scale
+        # x * 1 - y * 0: a zero's sign may differ
+        zero = (got[:, 0] & 0x7F) == 0
+        assert torch.equal(got[:, 0][~zero], want[:, 0][~zero])
+        assert bool(((want[:, 0] & 0x7F) == 0)[zero].all())
+
+
 def test_many_tokens_in_a_long_pool(pkv):
     """More than 2^31 elements between a pool's ends: 64-bit slot offsets."""
     nb, hk, D, bs = 20000, 8, 128, 64                        # 2.6e9 elements of one byte

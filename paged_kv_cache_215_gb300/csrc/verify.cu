@@ -25,8 +25,6 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 16;            // CTAs of a cluster
 constexpr int kStep = 16;               // elements a lane loads at a time, of each row
 constexpr int kWalk = 4;                // consecutive elements a thread takes in the search
@@ -227,73 +225,70 @@ __device__ __forceinline__ uint64_t piece_sum(const Row& r, int64_t lo, int64_t 
              : piece_sum<DT, false, false>(r, lo, hi, lane);
 }
 
-// The entry of x[0 .. n) (n <= 32) whose range of the running sum holds t, given that
-// one does; `before` (the sum ahead of x[0]) becomes the sum ahead of that entry.
-// Whole warps.
-__device__ __forceinline__ int entry_of(const uint64_t* x, int n, uint64_t t, uint64_t& before,
-                                        int lane) {
-  const uint64_t upto = add_sat(before, warp_scan_sat(lane < n ? x[lane] : 0, lane));
-  const uint32_t over = __ballot_sync(0xffffffffu, upto > t);
-  const int e = over ? __ffs(over) - 1 : n;
-  const uint64_t ahead = __shfl_sync(0xffffffffu, upto, e > 0 ? min(e, 32) - 1 : 0);
-  if (e > 0) before = ahead;
-  return e;
-}
-
-// Write the token that holds target t (`before` <= t: the sum ahead of the CTA's slice
-// at `base`): the warp's piece from the pieces' sums, then its elements, kWalk
-// consecutive ones a thread and round.  All threads of the CTA.
-template <int DT>
-__device__ __forceinline__ void search(const Row& r, uint64_t t, uint64_t before,
-                                       const uint64_t* sums, int64_t base, int64_t piece, int64_t V,
-                                       int32_t* token) {
-  __shared__ uint64_t found[kWarps];
+// Write the token that holds target t of a CTA's slice at `base`: the warp's piece
+// from the pieces' running sums `upto`, then its elements, kWalk consecutive ones a
+// thread and round.  All threads of the CTA; t is below the slice's sum.
+template <int DT, int WARPS>
+__device__ __forceinline__ void search(const Row& r, uint64_t t, const uint64_t* upto, int64_t base,
+                                       int piece, int64_t V, int32_t* token) {
+  __shared__ uint64_t found[WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int w = entry_of(sums, kWarps, t, before, lane);
-  const int64_t lo = base + w * piece, hi = min(V, lo + piece);
-  for (int64_t i0 = lo; i0 < hi; i0 += kThreads * kWalk) {
-    // a short piece is spread over all threads
-    const int each = (int)min((int64_t)kWalk, (hi - i0 + kThreads - 1) / kThreads);
-    const int64_t i = i0 + tid * each;
+  const int w =
+      __ffs(__ballot_sync(0xffffffffu, upto[lane < WARPS ? lane : WARPS - 1] > t)) - 1;
+  uint64_t before = w > 0 ? upto[w - 1] : 0;         // the sum ahead of the round
+  const int64_t lo = base + (int64_t)w * piece;
+  const int n = (int)min((int64_t)piece, V - lo);
+  // a short piece is spread over all threads
+  const int each = min(kWalk, (n + WARPS * 32 - 1) / (WARPS * 32));
+  for (int i0 = 0; i0 < n; i0 += WARPS * 32 * kWalk) {
+    const int i = i0 + tid * each;
+    const int zero = (int)max((int64_t)-1, min(r.zero - lo, (int64_t)n));
     float p[kWalk], q[kWalk];
 #pragma unroll
     for (int j = 0; j < kWalk; ++j) {
-      const bool in = j < each && i + j < hi && i + j != r.zero;
-      p[j] = in ? prob<DT>(r.p, i + j) : 0.f;
-      q[j] = in && r.q ? prob<DT>(r.q, i + j) : 0.f;
+      const bool in = j < each && i + j < n && i + j != zero;
+      p[j] = in ? prob<DT>(r.p, lo + i + j) : 0.f;
+      q[j] = in && r.q ? prob<DT>(r.q, lo + i + j) : 0.f;
     }
     uint64_t v[kWalk], s = 0;
 #pragma unroll
     for (int j = 0; j < kWalk; ++j) s += v[j] = weight(p[j], q[j]);
-    const uint64_t upto = warp_scan_sat(s, lane);
-    if (lane == 31) found[warp] = upto;
+    const uint64_t mine = warp_scan_sat(s, lane);
+    if (lane == 31) found[warp] = mine;
     __syncthreads();
-    const int hit = entry_of(found, kWarps, t, before, lane);
-    if (hit < kWarps) {
-      if (warp != hit) return;
-      const uint64_t end = add_sat(before, upto);
-      const uint32_t over = __ballot_sync(0xffffffffu, end > t);
+    // every warp for itself: the warps' running sums, one a lane
+    const uint64_t sum = add_sat(before, warp_scan_sat(lane < WARPS ? found[lane] : 0, lane));
+    const uint32_t over = __ballot_sync(0xffffffffu, sum > t);
+    const uint64_t ahead = __shfl_sync(0xffffffffu, sum, warp > 0 ? warp - 1 : 0);
+    if (over) {
+      if (warp != __ffs(over) - 1) return;
+      if (warp > 0) before = ahead;
+      const uint64_t end = add_sat(before, mine);
       const uint64_t prev = __shfl_up_sync(0xffffffffu, end, 1);
-      if (lane == __ffs(over) - 1) {
-        uint64_t ahead = lane > 0 ? prev : before;
+      if (lane == __ffs(__ballot_sync(0xffffffffu, end > t)) - 1) {
+        uint64_t x = lane > 0 ? prev : before;
         int at = 0;
 #pragma unroll
         for (int j = 0; j < kWalk; ++j) {
-          ahead = add_sat(ahead, v[j]);
-          if (ahead <= t) at = j + 1;
+          x = add_sat(x, v[j]);
+          if (x <= t) at = j + 1;
         }
-        *token = (int32_t)(i + at);
+        *token = (int32_t)(lo + i + at);
       }
       return;
     }
+    before = __shfl_sync(0xffffffffu, sum, 31);
     __syncthreads();                         // found is written again
   }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a, int ctas) {
+// THREADS threads a CTA, `ctas` of them (one cluster) to a sequence.
+template <int DT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+    verify_kernel(const VerifyArgs a, int ctas, int piece) {
+  constexpr int WARPS = THREADS / 32;
   __shared__ int first;
-  __shared__ uint64_t sums[kWarps];
+  __shared__ uint64_t sums[WARPS];           // the warps' sums, then their running sums
   __shared__ uint64_t totals[2][kMaxCtas];   // every CTA's slice, of either pass
   const int b = blockIdx.x / ctas, rank = blockIdx.x % ctas;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -312,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
   const char* target = static_cast<const char*>(a.target) + (int64_t)b * a.t_seq * esize;
   const char* draft =
       a.draft ? static_cast<const char*>(a.draft) + (int64_t)b * a.d_seq * esize : nullptr;
-  for (int j = tid; j < a.K; j += kThreads) {
+  for (int j = tid; j < a.K; j += THREADS) {
     const int x = __ldg(a.drafts + (int64_t)b * a.K + j);
     const float ua = __ldg(a.u_accept + (int64_t)b * a.K + j);
     if (j >= n) break;
@@ -343,10 +338,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
   row.q = refused && draft ? draft + (int64_t)acc * a.d_row * esize : nullptr;
   row.zero = refused && !draft ? __ldg(a.drafts + (int64_t)b * a.K + acc) : -1;
 
-  // every warp a contiguous piece of the CTA's slice, a multiple of 128 elements
-  const int64_t unit = (int64_t)ctas * kWarps * 128;
-  const int64_t piece = ((int64_t)a.V + unit - 1) / unit * 128;
-  const int64_t lo = min((int64_t)a.V, ((int64_t)rank * kWarps + warp) * piece);
+  // every warp a contiguous piece of the CTA's slice
+  const int64_t base = (int64_t)rank * WARPS * piece;
+  const int64_t lo = min((int64_t)a.V, base + (int64_t)warp * piece);
   const int64_t hi = min((int64_t)a.V, lo + piece);
 
   uint64_t all = 0;
@@ -356,7 +350,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     __syncthreads();
     if (ctas > 1 && pass == 0) cluster_wait();   // all CTAs run
     if (warp == 0) {
-      const uint64_t mine = warp_sum_sat(lane < kWarps ? sums[lane] : 0);
+      const uint64_t upto = warp_scan_sat(lane < WARPS ? sums[lane] : 0, lane);
+      const uint64_t mine = __shfl_sync(0xffffffffu, upto, WARPS - 1);
+      if (lane < WARPS) sums[lane] = upto;
       if (ctas > 1) {
         if (lane < ctas) store_to_cta(&totals[pass][rank], lane, mine);
       } else if (lane == 0) {
@@ -375,19 +371,19 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     if (all > 0) {
       const uint64_t t = __umul64hi(u64, all);        // floor(u * all) < all
       const int owner = __ffs(__ballot_sync(0xffffffffu, upto > t)) - 1;
-      const uint64_t before =
-          owner > 0 ? __shfl_sync(0xffffffffu, upto, owner - 1) : 0;
+      const uint64_t before = owner > 0 ? __shfl_sync(0xffffffffu, upto, owner - 1) : 0;
       if (owner == rank)
-        search<DT>(row, t, before, sums, (int64_t)rank * kWarps * piece, piece, a.V,
-                   a.tokens + (int64_t)b * (a.K + 1) + acc);
+        search<DT, WARPS>(row, t - before, sums, base, piece, a.V,
+                          a.tokens + (int64_t)b * (a.K + 1) + acc);
       break;
     }
     if (row.q == nullptr && row.zero < 0) break;
     row.q = nullptr;                         // a residual without mass: the target itself
     row.zero = -1;
+    __syncthreads();                         // sums are written again
   }
   if (rank == 0) {
-    for (int j = tid; j <= a.K; j += kThreads)
+    for (int j = tid; j <= a.K; j += THREADS)
       if (j != acc || all == 0)
         a.tokens[(int64_t)b * (a.K + 1) + j] =
             j < acc ? __ldg(a.drafts + (int64_t)b * a.K + j) : -1;
@@ -398,20 +394,23 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
   }
 }
 
-template <int DT>
+template <int DT, int THREADS>
 cudaError_t run(const VerifyArgs& a, int ctas, cudaStream_t stream) {
+  // a warp's piece: a multiple of 128 elements
+  const int64_t unit = (int64_t)ctas * THREADS * 4;
+  const int piece = (int)((a.V + unit - 1) / unit * 128);
   if (ctas == 1) {
-    verify_kernel<DT><<<(unsigned)a.B, kThreads, 0, stream>>>(a, 1);
+    verify_kernel<DT, THREADS><<<(unsigned)a.B, THREADS, 0, stream>>>(a, 1, piece);
     return cudaGetLastError();
   }
   if (ctas > 8) {                            // above the portable cluster size
     const cudaError_t e = cudaFuncSetAttribute(
-        verify_kernel<DT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        verify_kernel<DT, THREADS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.B * ctas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -419,23 +418,30 @@ cudaError_t run(const VerifyArgs& a, int ctas, cudaStream_t stream) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_kernel<DT>, a, ctas);
+  return cudaLaunchKernelEx(&cfg, verify_kernel<DT, THREADS>, a, ctas, piece);
 }
 
-}  // namespace
-
-cudaError_t launch_verify(const VerifyArgs& a, int sms, cudaStream_t stream) {
+template <int DT>
+cudaError_t pick(const VerifyArgs& a, int sms, cudaStream_t stream) {
   // CTAs per sequence: as many as run at the same time (two to an SM), with at least
   // 4096 tokens of the row each
   int ctas = 1;
   while (ctas < kMaxCtas && (int64_t)a.B * ctas * 2 <= 2 * sms && a.V / (2 * ctas) >= 4096)
     ctas *= 2;
   if ((int64_t)a.B * ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  // two to a sequence would be the whole SM: one of twice the threads needs no cluster
+  if (ctas == 2) return run<DT, 1024>(a, 1, stream);
+  return run<DT, 512>(a, ctas, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_verify(const VerifyArgs& a, int sms, cudaStream_t stream) {
   cudaError_t e;
   switch (a.dtype) {
-    case PKV_F32: e = run<PKV_F32>(a, ctas, stream); break;
-    case PKV_F16: e = run<PKV_F16>(a, ctas, stream); break;
-    case PKV_BF16: e = run<PKV_BF16>(a, ctas, stream); break;
+    case PKV_F32: e = pick<PKV_F32>(a, sms, stream); break;
+    case PKV_F16: e = pick<PKV_F16>(a, sms, stream); break;
+    case PKV_BF16: e = pick<PKV_BF16>(a, sms, stream); break;
     default: return cudaErrorInvalidValue;
   }
   if (e == cudaSuccess) count_launch();

@@ -27,7 +27,6 @@ namespace {
 
 constexpr int kMaxCtas = 16;            // CTAs of a cluster
 constexpr int kStep = 16;               // elements a lane loads at a time, of each row
-constexpr int kWalk = 4;                // consecutive elements a thread takes in the search
 constexpr uint64_t kCap = 1ull << 58;   // 16.0: sums saturate here
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -225,51 +224,42 @@ __device__ __forceinline__ uint64_t piece_sum(const Row& r, int64_t lo, int64_t 
              : piece_sum<DT, false, false>(r, lo, hi, lane);
 }
 
-// Write the token that holds target t of a CTA's slice at `base`: the warp's piece
-// from the pieces' running sums `upto`, then its elements, kWalk consecutive ones a
-// thread and round.  All threads of the CTA; t is below the slice's sum.
-template <int DT, int WARPS>
-__device__ __forceinline__ void search(const Row& r, uint64_t t, const uint64_t* upto, int64_t base,
-                                       int piece, int64_t V, int32_t* token) {
-  __shared__ uint64_t found[WARPS];
+// Write the token that holds target t of the n elements from `lo` on, given that one
+// does; `before` is the sum ahead of them.  WALK consecutive elements a thread and
+// round.  All threads of the CTA.
+template <int DT, int WARPS, int WALK>
+__device__ __forceinline__ void walk(const Row& r, uint64_t t, uint64_t before, int64_t lo, int n,
+                                     uint64_t* found, int32_t* token) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int w =
-      __ffs(__ballot_sync(0xffffffffu, upto[lane < WARPS ? lane : WARPS - 1] > t)) - 1;
-  uint64_t before = w > 0 ? upto[w - 1] : 0;         // the sum ahead of the round
-  const int64_t lo = base + (int64_t)w * piece;
-  const int n = (int)min((int64_t)piece, V - lo);
-  // a short piece is spread over all threads
-  const int each = min(kWalk, (n + WARPS * 32 - 1) / (WARPS * 32));
-  for (int i0 = 0; i0 < n; i0 += WARPS * 32 * kWalk) {
-    const int i = i0 + tid * each;
-    const int zero = (int)max((int64_t)-1, min(r.zero - lo, (int64_t)n));
-    float p[kWalk], q[kWalk];
+  const int zero = (int)max((int64_t)-1, min(r.zero - lo, (int64_t)n));
+  for (int i0 = 0; i0 < n; i0 += WARPS * 32 * WALK) {
+    const int i = i0 + tid * WALK;
+    float p[WALK], q[WALK];
 #pragma unroll
-    for (int j = 0; j < kWalk; ++j) {
-      const bool in = j < each && i + j < n && i + j != zero;
+    for (int j = 0; j < WALK; ++j) {
+      const bool in = i + j < n && i + j != zero;
       p[j] = in ? prob<DT>(r.p, lo + i + j) : 0.f;
       q[j] = in && r.q ? prob<DT>(r.q, lo + i + j) : 0.f;
     }
-    uint64_t v[kWalk], s = 0;
+    uint64_t v[WALK], s = 0;
 #pragma unroll
-    for (int j = 0; j < kWalk; ++j) s += v[j] = weight(p[j], q[j]);
+    for (int j = 0; j < WALK; ++j) s += v[j] = weight(p[j], q[j]);
     const uint64_t mine = warp_scan_sat(s, lane);
     if (lane == 31) found[warp] = mine;
     __syncthreads();
     // every warp for itself: the warps' running sums, one a lane
     const uint64_t sum = add_sat(before, warp_scan_sat(lane < WARPS ? found[lane] : 0, lane));
     const uint32_t over = __ballot_sync(0xffffffffu, sum > t);
-    const uint64_t ahead = __shfl_sync(0xffffffffu, sum, warp > 0 ? warp - 1 : 0);
     if (over) {
       if (warp != __ffs(over) - 1) return;
-      if (warp > 0) before = ahead;
+      if (warp > 0) before = __shfl_sync(0xffffffffu, sum, warp - 1);
       const uint64_t end = add_sat(before, mine);
       const uint64_t prev = __shfl_up_sync(0xffffffffu, end, 1);
       if (lane == __ffs(__ballot_sync(0xffffffffu, end > t)) - 1) {
         uint64_t x = lane > 0 ? prev : before;
         int at = 0;
 #pragma unroll
-        for (int j = 0; j < kWalk; ++j) {
+        for (int j = 0; j + 1 < WALK; ++j) {
           x = add_sat(x, v[j]);
           if (x <= t) at = j + 1;
         }
@@ -280,6 +270,24 @@ __device__ __forceinline__ void search(const Row& r, uint64_t t, const uint64_t*
     before = __shfl_sync(0xffffffffu, sum, 31);
     __syncthreads();                         // found is written again
   }
+}
+
+// Write the token that holds target t of a CTA's slice at `base`: the warp's piece
+// from the pieces' running sums `upto`, then its elements, as few a thread as cover it
+// (one to four).  All threads of the CTA; t is below the slice's sum.
+template <int DT, int WARPS>
+__device__ __forceinline__ void search(const Row& r, uint64_t t, const uint64_t* upto, int64_t base,
+                                       int piece, int64_t V, int32_t* token) {
+  __shared__ uint64_t found[WARPS];
+  const int lane = threadIdx.x & 31;
+  const int w =
+      __ffs(__ballot_sync(0xffffffffu, upto[lane < WARPS ? lane : WARPS - 1] > t)) - 1;
+  const uint64_t before = w > 0 ? upto[w - 1] : 0;
+  const int64_t lo = base + (int64_t)w * piece;
+  const int n = (int)min((int64_t)piece, V - lo);
+  if (n <= WARPS * 32) walk<DT, WARPS, 1>(r, t, before, lo, n, found, token);
+  else if (n <= WARPS * 64) walk<DT, WARPS, 2>(r, t, before, lo, n, found, token);
+  else walk<DT, WARPS, 4>(r, t, before, lo, n, found, token);
 }
 
 // THREADS threads a CTA, `ctas` of them (one cluster) to a sequence.
@@ -366,14 +374,22 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
       __syncthreads();
     }
     // every warp for itself: the CTAs' running sums, one a lane
-    const uint64_t upto = warp_scan_sat(lane < ctas ? totals[pass][lane] : 0, lane);
-    all = __shfl_sync(0xffffffffu, upto, 31);
+    uint64_t upto = 0;
+    if (ctas > 1) {
+      upto = warp_scan_sat(lane < ctas ? totals[pass][lane] : 0, lane);
+      all = __shfl_sync(0xffffffffu, upto, 31);
+    } else {
+      all = totals[pass][0];
+    }
     if (all > 0) {
-      const uint64_t t = __umul64hi(u64, all);        // floor(u * all) < all
-      const int owner = __ffs(__ballot_sync(0xffffffffu, upto > t)) - 1;
-      const uint64_t before = owner > 0 ? __shfl_sync(0xffffffffu, upto, owner - 1) : 0;
+      uint64_t t = __umul64hi(u64, all);              // floor(u * all) < all
+      int owner = 0;
+      if (ctas > 1) {
+        owner = __ffs(__ballot_sync(0xffffffffu, upto > t)) - 1;
+        if (owner > 0) t -= __shfl_sync(0xffffffffu, upto, owner - 1);
+      }
       if (owner == rank)
-        search<DT, WARPS>(row, t - before, sums, base, piece, a.V,
+        search<DT, WARPS>(row, t, sums, base, piece, a.V,
                           a.tokens + (int64_t)b * (a.K + 1) + acc);
       break;
     }

@@ -285,8 +285,11 @@ typedef struct {
  * and k.  dtype f32, f16 or bf16; angles, products and sums are fp32 with one
  * rounding to dtype at the end.  head_dim <= 512, rotary_dim <= head_dim.
  * Asynchronous on `stream`; PKV_EINVAL for NULL or misaligned pointers (to the
- * element size), negative counts or strides, overlapping output rows or a bad
- * rotation. */
+ * element size), negative counts or strides, overlapping output rows, a bad
+ * rotation, or more than 65535 heads.  rope_apply, kv_append_rope and verify_drafts
+ * are launched with programmatic dependent launch: a call is scheduled while the
+ * launch before it finishes and waits for it (and all before) ahead of any access,
+ * so it runs as any call in the stream does. */
 PKV_API int rope_apply(const pkv_rows* q_out, const pkv_rows* q, int num_q_heads,
                        const pkv_rows* k_out, const pkv_rows* k, int num_k_heads, pkv_dtype dtype,
                        int head_dim, const int32_t* d_positions, int64_t num_tokens,
@@ -305,7 +308,8 @@ PKV_API int rope_apply(const pkv_rows* q_out, const pkv_rows* q, int num_q_heads
  * position past the table or a block id out of range records PKV_EBOUNDS and skips
  * the store; the token's q is still rotated.  Heads, head_dim and block size are
  * the pool's; other arguments and errors as in kv_append_tokens and rope_apply,
- * except that k and v have strides and need only their elements' alignment. */
+ * except that k and v have strides and need only their elements' alignment.  A
+ * decode call behind it that reads q_out is not one for opts.pdl. */
 PKV_API int kv_append_rope(pkv_pool* pool, int layer, const pkv_rows* q_out, const pkv_rows* q,
                            const pkv_rows* k, const pkv_rows* v, pkv_dtype in_dtype,
                            const pkv_rope* rope, const int32_t* d_block_tables,

@@ -1180,7 +1180,7 @@ int rope_apply(const pkv_rows* q_out, const pkv_rows* q, int num_q_heads, const 
                const int32_t* d_positions, int64_t num_tokens, const pkv_rope* rope, int backward,
                cudaStream_t stream) {
   if (num_tokens < 0 || num_q_heads < 1 || num_k_heads < 0 || num_q_heads > 65535 ||
-      num_k_heads > 65535 || head_dim < 2 || head_dim > 512 || !act_dtype(dtype) || backward < 0 ||
+      num_k_heads > 65535 - num_q_heads || head_dim < 2 || head_dim > 512 || !act_dtype(dtype) || backward < 0 ||
       backward > 1 || !rope_ok(rope, head_dim))
     return PKV_EINVAL;
   if (num_tokens == 0) return PKV_OK;
@@ -1223,7 +1223,8 @@ int kv_append_rope(pkv_pool* p, int layer, const pkv_rows* q_out, const pkv_rows
   if (!p || layer < 0 || layer >= p->g.num_layers || batch < 0 || num_tokens < 0)
     return PKV_EINVAL;
   const pkv_geometry& g = p->g;
-  if (!rope_ok(rope, g.head_dim) || !q != !q_out || g.num_q_heads > 65535) return PKV_EINVAL;
+  if (!rope_ok(rope, g.head_dim) || !q != !q_out) return PKV_EINVAL;
+  if ((int64_t)g.num_q_heads + 2 * (int64_t)g.num_kv_heads > 65535) return PKV_EINVAL;
   const bool fp8 = g.kv_dtype == PKV_FP8_E4M3;
   if (fp8 ? !act_dtype(in_dtype) : (int)in_dtype != g.kv_dtype) return PKV_EINVAL;
   if (fp8 && !p->d_block_scales &&

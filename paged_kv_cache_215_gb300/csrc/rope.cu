@@ -220,6 +220,8 @@ template <int IN, int KV, int VEC, bool INTER, bool MANY>
 __global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
     rope_kernel(const RopeArgs a, int parts) {
   constexpr int N = MANY ? kManyHeads : 1;
+  grid_dependency_wait();                    // everything below reads or writes memory
+  grid_launch_dependents();
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int c = blockIdx.z * blockDim.x + threadIdx.x;
   if (t >= a.T || c >= parts) return;
@@ -324,9 +326,9 @@ cudaError_t run(RopeArgs& a, int parts, cudaStream_t stream) {
   if (gx > 0x7fffffff || gy > 65535) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)gx, (unsigned)gy, (parts + kThreads - 1) / kThreads);
   const dim3 block(across, rows);
-  if (a.interleaved) rope_kernel<IN, KV, VEC, true, MANY><<<grid, block, 0, stream>>>(a, parts);
-  else rope_kernel<IN, KV, VEC, false, MANY><<<grid, block, 0, stream>>>(a, parts);
-  return cudaGetLastError();
+  return launch_chained(a.interleaved ? rope_kernel<IN, KV, VEC, true, MANY>
+                                      : rope_kernel<IN, KV, VEC, false, MANY>,
+                        grid, block, 1, stream, a, parts);
 }
 
 template <int IN, int KV, int VEC>

@@ -301,6 +301,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   const int b = blockIdx.x / ctas, rank = blockIdx.x % ctas;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (ctas > 1) cluster_arrive();            // this CTA runs: its shared memory may be written
+  grid_dependency_wait();                    // everything below reads or writes memory
+  grid_launch_dependents();
 
   // accepted drafts: the first refused one, every CTA for itself
   int n = a.num_drafts ? __ldg(a.num_drafts + b) : a.K;
@@ -415,26 +417,13 @@ cudaError_t run(const VerifyArgs& a, int ctas, cudaStream_t stream) {
   // a warp's piece: a multiple of 128 elements
   const int64_t unit = (int64_t)ctas * THREADS * 4;
   const int piece = (int)((a.V + unit - 1) / unit * 128);
-  if (ctas == 1) {
-    verify_kernel<DT, THREADS><<<(unsigned)a.B, THREADS, 0, stream>>>(a, 1, piece);
-    return cudaGetLastError();
-  }
   if (ctas > 8) {                            // above the portable cluster size
     const cudaError_t e = cudaFuncSetAttribute(
         verify_kernel<DT, THREADS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.B * ctas));
-  cfg.blockDim = dim3(THREADS);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_kernel<DT, THREADS>, a, ctas, piece);
+  return launch_chained(verify_kernel<DT, THREADS>, dim3((unsigned)(a.B * ctas)), dim3(THREADS),
+                        ctas, stream, a, ctas, piece);
 }
 
 template <int DT>

@@ -244,6 +244,30 @@ def test_another_stream_and_graph_replay(pkv):
         ref.check_rotated(out, q, positions, freqs, m, 64, False)
 
 
+@pytest.mark.parametrize("T,H", [(3, 2), (1500, 40)])
+def test_calls_in_a_row_see_each_other(pkv, T, H):
+    """Consecutive calls overlap on the device but each waits for the one before: 40
+    rotations in place, a copy in between, equal one by 40 times the position.  A step
+    is off by at most (2^-21 + 2^-24) (|a| + |b|) an element, (|a| + |b|) at most sqrt 2
+    times the pair's norm, and rotations keep the norm of what is off: 40 steps of two
+    elements each give 80 (2^-21 + 2^-24) (|a| + |b|)."""
+    D, n = 32, 40
+    x0 = _x((T, H, D), torch.float32, 30)
+    x, y = x0.clone(), torch.empty_like(x0)
+    positions = _pos([i % 91 for i in range(T)])
+    rope = pkv.Rope(D)
+    for i in range(n // 2):
+        pkv.rope_apply(x, x, positions, rope)
+        pkv.rope_apply(y, x, positions, rope)
+        x.copy_(y)
+    torch.cuda.synchronize()
+    freqs, m = ref.frequencies(D)
+    rows = slice(None, None, max(1, T // 40))
+    want, size = ref.rotate(x0[rows], positions[rows] * n, freqs, m, D, False)
+    lim = 2 * n * (2.0 ** -21 + 2.0 ** -24) * size
+    assert np.all(np.abs(x[rows].double().cpu().numpy() - want) <= lim)
+
+
 def test_no_tokens(pkv):
     q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
     pkv.rope_apply(q, q, _pos([]), pkv.Rope(64))

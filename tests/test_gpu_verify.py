@@ -206,6 +206,29 @@ def test_another_stream_and_graph_replay(pkv):
         assert tokens.tolist() == want and acc.tolist() == n
 
 
+@pytest.mark.parametrize("B,V", [(1, 131072), (90, 20000), (400, 700)])
+def test_calls_in_a_row_see_each_other(pkv, B, V):
+    """Consecutive calls overlap on the device but each waits for the one before: the
+    same buffers take another step's inputs between two calls, and each call's outputs
+    are copied before the next overwrites them."""
+    steps = [_case(B, 2, V, seed=s) for s in (21, 22, 23)]
+    bufs = [t.clone() for t in steps[0]]
+    tokens = torch.empty(B, 3, dtype=torch.int32, device="cuda")
+    acc = torch.empty(B, dtype=torch.int32, device="cuda")
+    got = []
+    for i in range(9):
+        for b, t in zip(bufs, steps[i % 3]):
+            b.copy_(t)
+        pkv.verify_drafts(tokens, acc, *bufs)
+        pkv.verify_drafts(tokens, acc, *bufs)
+        got.append((tokens.clone(), acc.clone()))
+    torch.cuda.synchronize()
+    for i in range(3):
+        want, n = ref.verify(*steps[i])
+        for j in range(i, 9, 3):
+            assert got[j][0].tolist() == want and got[j][1].tolist() == n
+
+
 def test_binding_refusals(pkv):
     t, q, x, ua, us = _case(3, 2, 100, seed=16)
     tok = torch.empty(3, 3, dtype=torch.int32, device="cuda")

@@ -102,7 +102,8 @@ def test_rope_apply_refusals(pkv):
            dict(qo=_rows(pkv, data=2 * BASE, ts=255)),       # a token's last head overlaps
            dict(qo=_rows(pkv, data=2 * BASE, ts=64, hs=319)),   # heads outermost, overlapping
            dict(qo=_rows(pkv, ts=512)),                      # in place with other strides
-           dict(T=1 << 31)]
+           dict(T=1 << 31), dict(H=65536, qo=_rows(pkv, heads=65536, data=2 * BASE)),
+           dict(H=65535, Hk=1, qo=_rows(pkv, heads=65535, data=2 * BASE))]
     for kw in bad:
         assert call(**kw) == pkv.PKV_EINVAL, kw
 

@@ -150,7 +150,7 @@ struct Part {
 // are the fastest of 4 to 10 for each type.
 constexpr int kThreads = 128, kFewBlocks = 10, kManyHeads = 4;
 __host__ __device__ constexpr int blocks_of(int in, int kv, bool many) {
-  return !many ? kFewBlocks : kv == PKV_FP8_E4M3 ? 5 : in == PKV_F32 ? 7 : 6;
+  return !many ? kFewBlocks : kv == PKV_FP8_E4M3 ? 5 : in == PKV_F32 ? 9 : 6;
 }
 
 template <int IN, int VEC, int N>
@@ -221,7 +221,6 @@ __global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
     rope_kernel(const RopeArgs a, int parts) {
   constexpr int N = MANY ? kManyHeads : 1;
   grid_dependency_wait();                    // everything below reads or writes memory
-  grid_launch_dependents();
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int c = blockIdx.z * blockDim.x + threadIdx.x;
   if (t >= a.T || c >= parts) return;

@@ -302,7 +302,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (ctas > 1) cluster_arrive();            // this CTA runs: its shared memory may be written
   grid_dependency_wait();                    // everything below reads or writes memory
-  grid_launch_dependents();
 
   // accepted drafts: the first refused one, every CTA for itself
   int n = a.num_drafts ? __ldg(a.num_drafts + b) : a.K;

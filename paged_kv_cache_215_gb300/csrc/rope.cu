@@ -4,9 +4,16 @@
 // Pair i of a row at position p turns by p * f_i:
 //   (a, b) -> m (a cos - b sin, a sin + b cos).
 // f_i is held in 2^-64 turns, so p * f_i modulo 2^64 (one 64-bit multiply) is the
-// angle reduced to one turn, exactly; its upper 32 bits, as a signed fraction of a
-// turn, go to sincospi.  Products and sums are fp32, rounded once to the output's
-// type (for an E4M3 pool straight from fp32).
+// angle reduced to one turn, exactly; its upper 32 bits are a signed fraction of a
+// turn.  Products and sums are fp32, rounded once to the output's type (for an E4M3
+// pool straight from fp32).
+//
+// Every element is read and written once with a few operations, so memory bounds the
+// long calls and the launch and one round of loads the short ones.  Measured (one
+// call after another): 16384 tokens of 64 + 2 x 8 heads of 128 in bf16 into the pool,
+// 671 MB, 100 us (6.7 TB/s, 0.99 of the copy rate); 8192 tokens of 32 + 8 heads, 168 MB,
+// 27.9 us (0.89); 4099 tokens of 16 + 4 fp32 heads of 64, 42 MB, 7.4 us (0.83); 256
+// tokens into an E4M3 pool, 10 MB, 4.1 us; one token, 2.1 us.
 //
 // A thread owns one part of a token's rows: two vectors of VEC elements, at offset
 // e0 and half the rotated part further on, the same for both layouts (their pairs
@@ -122,8 +129,8 @@ struct Vec {
 
 // Sine and cosine of `turns` (2^-32 of a full turn, signed) times m.  fp32 rows take
 // sincospi (1 ulp).  16-bit rows, and E4M3 pools filled from them, take the
-// special-function unit on the reduced angle, off by 2^-20.9 at most: a 2^-9 share
-// of bf16's half step, 2^-12 of f16's being the nearest.
+// special-function unit on the reduced angle: with the angle's rounding off by 2^-20 at
+// most, 2^-9 of the half step (2^-11) that storing f16 costs anyway.
 template <int IN>
 __device__ __forceinline__ void sine(int32_t turns, float m, float& s, float& c) {
   if constexpr (IN == PKV_F32) {

@@ -15,8 +15,12 @@
 //
 // Turning a float into 64-bit fixed point with shifts, and summing that, took 75
 // instructions an element and bound the kernel (9700 of 25000 cycles for one row of
-// 131072); two fp32 additions that truncate into the significand give the same
-// integers in 14, see Limbs.
+// 131072); additions that truncate into the significand give the same integers in 14,
+// see Limbs.  What is left is a chain of latencies: the drafts and their probabilities
+// (1 us), the row (1.5 us of one row on 16 SMs), the cluster's barrier (0.8 us), the
+// search (1 us).  Measured (one call after another): one sequence, 4 drafts, 131072
+// tokens 5.8 us; 32 sequences, up to 5 drafts, 131071 tokens (rows not aligned) 9.4 us;
+// 128 sequences, 3 looked-up drafts, 32768 tokens 7.8 us.
 #include <algorithm>
 
 #include "device.cuh"

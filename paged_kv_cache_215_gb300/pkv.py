@@ -251,8 +251,20 @@ class Rope:
         self.rotary_dim, self.interleaved = rotary_dim, bool(interleaved)
         self.attn_scale = scale.value if attn_scale is None else float(attn_scale)
         self.freqs = torch.frombuffer(bytearray(table), dtype=torch.int64).to(device)
-        self.ref = RopeRef(self.freqs.data_ptr(), rotary_dim, int(interleaved), self.attn_scale)
-        self.address = ctypes.addressof(self.ref)
+        self._bind()
+
+    def _bind(self):
+        """The structure the calls take: it points at this object's own table."""
+        self._ref = RopeRef(self.freqs.data_ptr(), self.rotary_dim, int(self.interleaved),
+                            self.attn_scale)
+        self.address = ctypes.addressof(self._ref)
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k not in ("_ref", "address")}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._bind()
 
 
 def rope_apply(q_out, q, positions, rope: Rope, k_out=None, k=None, backward=False, stream=None):

@@ -268,6 +268,34 @@ def test_calls_in_a_row_see_each_other(pkv, T, H):
     assert np.all(np.abs(x[rows].double().cpu().numpy() - want) <= lim)
 
 
+def test_more_than_2_31_elements(pkv):
+    T, H, D = 131200, 128, 128
+    x = torch.zeros(T, H, D, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = _x((3, H, D), torch.bfloat16, 31)
+    assert x.numel() > 2 ** 31
+    out = torch.empty_like(x)
+    positions = torch.arange(T, dtype=torch.int32, device="cuda")
+    pkv.rope_apply(out, x, positions, pkv.Rope(D))
+    freqs, m = ref.frequencies(D)
+    ref.check_rotated(out[-3:], x[-3:], positions[-3:], freqs, m, D, False)
+    assert int(torch.count_nonzero(out[:-3])) == 0
+
+
+def test_copies_of_a_rotation(pkv):
+    import copy
+    import pickle
+    rope = pkv.Rope(16, scaling="yarn", factor=2.0, original_positions=100, interleaved=True)
+    copies = [copy.copy(rope), copy.deepcopy(rope), pickle.loads(pickle.dumps(rope))]
+    q = _x((4, 2, 16), torch.float32, 32)
+    want = torch.empty_like(q)
+    pkv.rope_apply(want, q, _pos([1, 2, 3, 4]), rope)
+    del rope
+    for r in copies:
+        out = torch.empty_like(q)
+        pkv.rope_apply(out, q, _pos([1, 2, 3, 4]), r)
+        assert torch.equal(out, want)
+
+
 def test_no_tokens(pkv):
     q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
     pkv.rope_apply(q, q, _pos([]), pkv.Rope(64))

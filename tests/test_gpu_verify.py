@@ -159,6 +159,22 @@ def test_strides_and_odd_bases(pkv):
     _check(pkv, t[:1].expand(B, K + 1, V), q[:1].expand(B, K, V), x, ua, us)
 
 
+def test_more_than_2_31_elements(pkv):
+    """The last sequences of 4096 x 5 rows of 131072; the rows ahead have no mass."""
+    B, K, V = 4096, 4, 131072
+    t = torch.zeros(B, K + 1, V, dtype=torch.float16, device="cuda")
+    q = torch.zeros(B, K, V, dtype=torch.float16, device="cuda")
+    x = torch.zeros(B, K, dtype=torch.int32, device="cuda")
+    ua, us = torch.zeros(B, K, device="cuda"), torch.zeros(B, device="cuda")
+    few = _case(3, K, V, torch.float16, seed=30)
+    for a, b in zip((t, q, x, ua, us), few):
+        a[-3:] = b
+    tokens, acc = _run(pkv, t, q, x, ua, us)
+    want, n = ref.verify(*few)
+    assert tokens[-3:].tolist() == want and acc[-3:].tolist() == n
+    assert bool((tokens[:-3] == -1).all()) and int(acc[:-3].sum()) == 0
+
+
 def test_the_same_answer_in_any_batch(pkv):
     """One sequence's row is cut differently in a batch of another size."""
     t, q, x, ua, us = _case(400, 2, 20000, seed=11)

@@ -597,9 +597,9 @@ typedef struct {
  * saturates at 16; a draft of p = 0 is refused; a NaN u refuses
  * (u_accept) or counts as 0 (u_sample), a u_sample of 1 or more as the largest
  * value below 1.  d_status: device int32 (zero: no error) that takes the first error,
- * as a pool's status word does, or NULL.  A refused-by-range draft (an id outside
- * [0, vocab)) counts as refused and records PKV_EBOUNDS, as does a d_num_drafts
- * outside [0, max_drafts], which is limited to it; a row without any mass gives the
+ * as a pool's status word does, or NULL.  A draft outside [0, vocab) is
+ * refused and records PKV_EBOUNDS where every draft before it was accepted; a
+ * d_num_drafts outside [0, max_drafts] is limited to it and records PKV_EBOUNDS; a row without any mass gives the
  * next token -1 and records PKV_EINVAL.  Asynchronous on `stream`, no workspace;
  * PKV_EINVAL for NULL pointers, negative sizes or strides, vocab < 1 or dtype. */
 PKV_API int verify_drafts(int32_t* d_tokens, int32_t* d_num_accepted, const pkv_probs* target,

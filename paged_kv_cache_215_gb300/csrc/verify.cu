@@ -277,16 +277,14 @@ __device__ __forceinline__ void walk(const Row& r, uint64_t t, uint64_t before, 
 }
 
 // Write the token that holds target t of a CTA's slice at `base`: the warp's piece
-// from the pieces' running sums `upto`, then its elements, as few a thread as cover it
-// (one to four).  All threads of the CTA; t is below the slice's sum.
+// from the pieces' running sums (`upto`, one a lane), then its elements, as few a
+// thread as cover it (one to four).  All threads of the CTA; t is below the slice's sum.
 template <int DT, int WARPS>
-__device__ __forceinline__ void search(const Row& r, uint64_t t, const uint64_t* upto, int64_t base,
+__device__ __forceinline__ void search(const Row& r, uint64_t t, uint64_t upto, int64_t base,
                                        int piece, int64_t V, int32_t* token) {
   __shared__ uint64_t found[WARPS];
-  const int lane = threadIdx.x & 31;
-  const int w =
-      __ffs(__ballot_sync(0xffffffffu, upto[lane < WARPS ? lane : WARPS - 1] > t)) - 1;
-  const uint64_t before = w > 0 ? upto[w - 1] : 0;
+  const int w = __ffs(__ballot_sync(0xffffffffu, upto > t)) - 1;
+  const uint64_t before = w > 0 ? __shfl_sync(0xffffffffu, upto, w - 1) : 0;
   const int64_t lo = base + (int64_t)w * piece;
   const int n = (int)min((int64_t)piece, V - lo);
   if (n <= WARPS * 32) walk<DT, WARPS, 1>(r, t, before, lo, n, found, token);
@@ -299,43 +297,55 @@ template <int DT, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     verify_kernel(const VerifyArgs a, int ctas, int piece) {
   constexpr int WARPS = THREADS / 32;
-  __shared__ int first;
-  __shared__ uint64_t sums[WARPS];           // the warps' sums, then their running sums
+  __shared__ uint64_t sums[WARPS];           // the warps' sums (a cluster's: running sums)
   __shared__ uint64_t totals[2][kMaxCtas];   // every CTA's slice, of either pass
   const int b = blockIdx.x / ctas, rank = blockIdx.x % ctas;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (ctas > 1) cluster_arrive();            // this CTA runs: its shared memory may be written
   grid_dependency_wait();                    // everything below reads or writes memory
 
-  // accepted drafts: the first refused one, every CTA for itself
-  int n = a.num_drafts ? __ldg(a.num_drafts + b) : a.K;
+  // accepted drafts: the first refused one, every warp for itself, 32 drafts at a time
+  // (the first ones are loaded together with their number)
+  const int* drafts = a.drafts + (int64_t)b * a.K;
+  const float* u_accept = a.u_accept + (int64_t)b * a.K;
+  int x = lane < a.K ? __ldg(drafts + lane) : 0;
+  float ua = lane < a.K ? __ldg(u_accept + lane) : 0.f;
   const float u = __ldg(a.u_sample + b);
+  int n = a.num_drafts ? __ldg(a.num_drafts + b) : a.K;
+  const bool first_warp = rank == 0 && warp == 0;
   if (n < 0 || n > a.K) {
-    if (rank == 0 && tid == 0) record_error(a.status, PKV_EBOUNDS);
+    if (first_warp && lane == 0) record_error(a.status, PKV_EBOUNDS);
     n = min(max(n, 0), a.K);
   }
-  if (tid == 0) first = n;
-  __syncthreads();
   const int esize = DT == PKV_F32 ? 4 : 2;
   const char* target = static_cast<const char*>(a.target) + (int64_t)b * a.t_seq * esize;
   const char* draft =
       a.draft ? static_cast<const char*>(a.draft) + (int64_t)b * a.d_seq * esize : nullptr;
-  for (int j = tid; j < a.K; j += THREADS) {
-    const int x = __ldg(a.drafts + (int64_t)b * a.K + j);
-    const float ua = __ldg(a.u_accept + (int64_t)b * a.K + j);
-    if (j >= n) break;
-    bool ok = x >= 0 && x < a.V;
-    if (ok) {
+  int acc = n, refused_token = -1;
+  for (int j0 = 0; j0 < n; j0 += 32) {
+    const int j = j0 + lane;
+    if (j0 > 0 && j < n) {
+      x = __ldg(drafts + j);
+      ua = __ldg(u_accept + j);
+    }
+    const bool in = x >= 0 && x < a.V;
+    bool ok = j >= n;
+    if (!ok && in) {
       const float p = clean(prob<DT>(target, j * a.t_row + x)) * 0x1p60f;
       const float q = (draft ? clean(prob<DT>(draft, j * a.d_row + x)) : 1.f) * 0x1p60f;
       // u q < p exactly: the rounded product decides unless it equals p, then its
       // rounding error does (2^60 keeps that error a normal number)
       const float h = ua * q, l = fmaf(ua, q, -h);
       ok = p > 0.f && (h < p || (h == p && l < 0.f));
-    } else {
-      record_error(a.status, PKV_EBOUNDS);
     }
-    if (!ok) atomicMin(&first, j);
+    const uint32_t bad = __ballot_sync(0xffffffffu, !ok);
+    if (bad) {
+      const int at = __ffs(bad) - 1;
+      acc = j0 + at;
+      refused_token = __shfl_sync(0xffffffffu, x, at);
+      if (first_warp && lane == at && !in) record_error(a.status, PKV_EBOUNDS);
+      break;
+    }
   }
   // u in units of 2^-64: NaN and negative 0, 1 and above the largest value below 1
   const uint32_t ub = __float_as_uint(u);
@@ -343,13 +353,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
                        : u >= 1.f ? ~0ull
                                   : (uint64_t)((ub & 0x7fffffu) | (ub >> 23 ? 0x800000u : 0u)) << 40
                                         >> min(126u - (ub >> 23), 63u);
-  __syncthreads();
-  const int acc = first;
   const bool refused = acc < n;
   Row row;
   row.p = target + (int64_t)acc * a.t_row * esize;
   row.q = refused && draft ? draft + (int64_t)acc * a.d_row * esize : nullptr;
-  row.zero = refused && !draft ? __ldg(a.drafts + (int64_t)b * a.K + acc) : -1;
+  row.zero = refused && !draft ? refused_token : -1;
 
   // every warp a contiguous piece of the CTA's slice
   const int64_t base = (int64_t)rank * WARPS * piece;
@@ -362,29 +370,23 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     if (lane == 0) sums[warp] = s;
     __syncthreads();
     if (ctas > 1 && pass == 0) cluster_wait();   // all CTAs run
-    if (warp == 0) {
-      const uint64_t upto = warp_scan_sat(lane < WARPS ? sums[lane] : 0, lane);
-      const uint64_t mine = __shfl_sync(0xffffffffu, upto, WARPS - 1);
-      if (lane < WARPS) sums[lane] = upto;
-      if (ctas > 1) {
-        if (lane < ctas) store_to_cta(&totals[pass][rank], lane, mine);
-      } else if (lane == 0) {
-        totals[pass][0] = mine;
-      }
-    }
+    // running sums, one a lane, every warp for itself: of the CTAs, of this CTA's warps
+    uint64_t upto = 0, running;
     if (ctas > 1) {
+      if (warp == 0) {
+        const uint64_t mine = warp_scan_sat(lane < WARPS ? sums[lane] : 0, lane);
+        if (lane < WARPS) sums[lane] = mine;
+        const uint64_t total = __shfl_sync(0xffffffffu, mine, WARPS - 1);
+        if (lane < ctas) store_to_cta(&totals[pass][rank], lane, total);
+      }
       cluster_arrive();
       cluster_wait();
-    } else {
-      __syncthreads();
-    }
-    // every warp for itself: the CTAs' running sums, one a lane
-    uint64_t upto = 0;
-    if (ctas > 1) {
+      running = sums[min(lane, WARPS - 1)];
       upto = warp_scan_sat(lane < ctas ? totals[pass][lane] : 0, lane);
       all = __shfl_sync(0xffffffffu, upto, 31);
     } else {
-      all = totals[pass][0];
+      running = warp_scan_sat(lane < WARPS ? sums[lane] : 0, lane);
+      all = __shfl_sync(0xffffffffu, running, 31);
     }
     if (all > 0) {
       uint64_t t = __umul64hi(u64, all);              // floor(u * all) < all
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         if (owner > 0) t -= __shfl_sync(0xffffffffu, upto, owner - 1);
       }
       if (owner == rank)
-        search<DT, WARPS>(row, t, sums, base, piece, a.V,
+        search<DT, WARPS>(row, t, running, base, piece, a.V,
                           a.tokens + (int64_t)b * (a.K + 1) + acc);
       break;
     }
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     for (int j = tid; j <= a.K; j += THREADS)
       if (j != acc || all == 0)
         a.tokens[(int64_t)b * (a.K + 1) + j] =
-            j < acc ? __ldg(a.drafts + (int64_t)b * a.K + j) : -1;
+            j < acc ? __ldg(drafts + j) : -1;
     if (tid == 0) {
       a.num_accepted[b] = acc;
       if (all == 0) record_error(a.status, PKV_EINVAL);

@@ -140,36 +140,49 @@ __device__ __forceinline__ uint64_t weight(float p, float q) {
   return fixed(p) - fixed(fminf(fmaxf(q, 0.f), p));
 }
 
-// The sum of a lane's weights, each max(p - q, 0) = p - min(p, q).
+// The sum of a lane's weights, each max(p - q, 0) = p - min(p, q).  The bits of a
+// float from 0 to 2^-8, as an integer, are at most 2^-8's; negative ones and NaN are
+// above every other: one integer maximum tells whether all values are as they should
+// be and small enough for Limbs.
 template <bool Q>
 __device__ __forceinline__ uint64_t lane_sum(float (&p)[kStep], float (&q)[kStep]) {
-  float top = 0.f;
+  uint32_t top = 0, top_q = 0;
 #pragma unroll
   for (int j = 0; j < kStep; ++j) {
-    p[j] = fmaxf(p[j], 0.f);         // NaN: 0
-    if (Q) q[j] = fminf(fmaxf(q[j], 0.f), p[j]);
-    top = fmaxf(top, p[j]);
+    top = max(top, __float_as_uint(p[j]));
+    if (Q) top_q = max(top_q, __float_as_uint(q[j]));
   }
-  if (top > kSmall) {                // rare in a long row: at most 256 such probabilities
-    uint64_t s = 0;
-#pragma unroll 1
-    for (int j = 0; j < kStep; ++j) {
-      s += fixed(fminf(p[0], 1.f)) - (Q ? fixed(fminf(q[0], 1.f)) : 0);
+  uint64_t s = 0;
+  if (top > __float_as_uint(kSmall) || top_q > 0x7f800000u) {
+    // the few larger ones (at most 256 of a row) are taken out, one at a time
+    uint32_t large = 0;
 #pragma unroll
-      for (int i = 0; i + 1 < kStep; ++i) {      // shifted down: no indexed registers
-        p[i] = p[i + 1];
-        if (Q) q[i] = q[i + 1];
-      }
+    for (int j = 0; j < kStep; ++j) {
+      p[j] = clean(p[j]);
+      if (Q) q[j] = fmaxf(q[j], 0.f);
+      if (p[j] > kSmall) large |= 1u << j;
     }
-    return s;
+    while (large) {
+      const int j = __ffs(large) - 1;
+      large &= large - 1;
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int i = 0; i < kStep; ++i)
+        if (i == j) {
+          x = p[i];
+          p[i] = 0.f;
+          if (Q) y = q[i];
+        }
+      s += weight(x, y);
+    }
   }
   Limbs sum;
 #pragma unroll
   for (int j = 0; j < kStep; ++j) {
-    if (Q) sum.add_difference(p[j], q[j]);
+    if (Q) sum.add_difference(p[j], fminf(q[j], p[j]));
     else sum.add(p[j]);
   }
-  return sum.value(Q ? 0 : kStep);
+  return s + sum.value(Q ? 0 : kStep);
 }
 
 // A lane's share of elements [i0, i0 + left); FULL: left is 32 kStep.

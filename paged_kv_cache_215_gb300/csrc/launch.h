@@ -140,7 +140,9 @@ struct RopeArgs {
   int in_dtype, kv_dtype;    // kv_dtype: the pool's
   float k_scale, v_scale;
   const float* block_scales;
-  int groups_q, groups_k;    // set by the launcher: grid rows of q and of k (then of v)
+  // set by the launcher: head groups of q and of k (and of v); head groups in all where
+  // neighbouring blocks are one token's head groups, else 0
+  int groups_q, groups_k, heads_first;
 };
 cudaError_t launch_rope(RopeArgs a, int sms, cudaStream_t stream);
 

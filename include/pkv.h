@@ -233,10 +233,9 @@ PKV_API int kv_fp8_scale(const float* d_amax, int n, float* d_scale, cudaStream_
  *   (a, b) -> attn_scale * (a cos - b sin, a sin + b cos),
  * with (a, b) = (x[i], x[i + rotary_dim / 2]) in the half layout and
  * (x[2i], x[2i + 1]) in the interleaved one; elements from rotary_dim on are
- * unchanged.  A frequency is held as the fraction of a full turn per position,
+ * unchanged.A frequency is held as the fraction of a full turn per position,
  * in units of 2^-64 turns (uint64): p times it, modulo 2^64, is the angle reduced
- * to one turn without rounding, so positions far out (up to 2^31 - 1) turn as
- * exactly as the first ones. */
+ * to one turn, off by at most p 2^-63 turns (2^-32 at the largest position). */
 typedef enum {
   PKV_ROPE_NONE = 0,   /* f_i = base^(-2 i / r), r = rotary_dim */
   PKV_ROPE_LINEAR = 1, /* position interpolation: f_i / factor */
@@ -256,8 +255,8 @@ typedef struct {
 /* The table of rotary_dim / 2 frequencies and the attention scale (1 except for
  * YaRN) of a configuration, on the host; the caller uploads the table. */
 PKV_API int pkv_rope_freqs(const pkv_rope_config* config, uint64_t* h_freqs, float* h_attn_scale);
-/* The table of n frequencies given in radians per position (any finite values:
- * scalings other than the ones above). */
+/* The table of n frequencies given in radians per position (magnitudes up to 2^32):
+ * scalings other than the ones above. */
 PKV_API int pkv_rope_freqs_from(const double* h_radians, int n, uint64_t* h_freqs);
 
 /* A rotation: the table on the device (rotary_dim / 2 values, 8-byte aligned), the

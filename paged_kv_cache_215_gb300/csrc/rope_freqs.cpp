@@ -2,9 +2,8 @@
 //
 // A frequency f (radians per position) is held as the fraction of a full turn,
 // f / (2 pi) modulo 1, in units of 2^-64: the product with a position, taken
-// modulo 2^64, is then the angle modulo one turn, exact for the stored value.
-// fp64 leaves f / (2 pi) off by 2^-53 of itself, so a position of 2^20 at the
-// fastest pair (one radian) is off by less than 2^-35 turns.
+// modulo 2^64, is then the angle modulo one turn.  The quotient is formed in two
+// fp64 parts, so a position p is off by at most p 2^-63 turns from p f.
 #include <cmath>
 #include <cstdint>
 
@@ -12,13 +11,21 @@
 
 namespace {
 
+// 2 pi in two parts
 constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr double kTwoPiRest = 2.4492935982947064e-16;
+constexpr double kMost = 4294967296.0;   // radians a position: the parts below stay in range
 
 uint64_t turns(double radians) {
-  double t = radians / kTwoPi;
-  t -= std::floor(t);                    // [0, 1); rounding may give 1
-  const double x = std::ldexp(t, 64);
-  return x >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(x);
+  if (radians < 0) return 0 - turns(-radians);
+  const double hi = radians / kTwoPi;
+  // what hi leaves over: exact up to its own rounding
+  const double rest = std::fma(-hi, kTwoPi, radians) - hi * kTwoPiRest;
+  const double whole = hi - std::floor(hi);                  // [0, 1], exact below 2^53
+  const double x = std::ldexp(whole, 64);
+  const uint64_t t = x >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(x);
+  // the rest is far below a turn; modulo 2^64 it may be taken off as well
+  return t + static_cast<uint64_t>(static_cast<int64_t>(std::ldexp(rest / kTwoPi, 64)));
 }
 
 }  // namespace
@@ -28,7 +35,7 @@ extern "C" {
 int pkv_rope_freqs_from(const double* h_radians, int n, uint64_t* h_freqs) {
   if (!h_radians || !h_freqs || n < 1) return PKV_EINVAL;
   for (int i = 0; i < n; ++i)
-    if (!std::isfinite(h_radians[i])) return PKV_EINVAL;
+    if (!(std::fabs(h_radians[i]) <= kMost)) return PKV_EINVAL;
   for (int i = 0; i < n; ++i) h_freqs[i] = turns(h_radians[i]);
   return PKV_OK;
 }
@@ -58,7 +65,7 @@ int pkv_rope_freqs(const pkv_rope_config* c, uint64_t* h_freqs, float* h_attn_sc
       g = g < 0 ? 0 : g > 1 ? 1 : g;
       f = f * (g + (1 - g) / c->factor);
     }
-    if (!std::isfinite(f)) return PKV_EINVAL;
+    if (!(f <= kMost)) return PKV_EINVAL;
     h_freqs[i] = turns(f);
   }
   *h_attn_scale = yarn ? (float)(0.1 * std::log(c->factor) + 1.0) : 1.f;

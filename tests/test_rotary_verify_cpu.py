@@ -41,6 +41,21 @@ def test_frequency_table(pkv, rotary, scaling):
     assert np.all(np.abs(got - f / (2 * math.pi)) <= 2.0 ** -48 * f + 2.0 ** -63)
 
 
+def test_table_follows_the_given_frequency_to_the_last_bits(pkv):
+    """The table against f / (2 pi) in 60-digit arithmetic: within two units of 2^-64 of
+    a turn (two truncations)."""
+    from fractions import Fraction
+    pi = Fraction(3141592653589793238462643383279502884197169399375105820974944592307816406286,
+                  10 ** 75)
+    x = [1.0, 0.7498942093324559, 1e-4, 3.3e-9, 5.0, 123456.789, -0.1, -2e-7]
+    t = (ctypes.c_uint64 * len(x))()
+    assert pkv.lib().pkv_rope_freqs_from((ctypes.c_double * len(x))(*x), len(x), t) == 0
+    for f, got in zip(x, t):
+        want = Fraction(f) / (2 * pi) % 1 * 2 ** 64
+        off = abs(Fraction(got) - want)
+        assert min(off, 2 ** 64 - off) <= 2, f
+
+
 def test_given_frequencies_wrap_to_one_turn(pkv):
     t = (ctypes.c_uint64 * 4)()
     x = (ctypes.c_double * 4)(0.0, 2 * math.pi * 1.25, -2 * math.pi * 0.25, math.pi)
@@ -58,8 +73,8 @@ def test_frequency_refusals(pkv):
         rc, _, _ = _table(pkv, **dict(dict(rotary=8), **kw))
         assert rc == pkv.PKV_EINVAL, kw
     t = (ctypes.c_uint64 * 1)()
-    assert pkv.lib().pkv_rope_freqs_from((ctypes.c_double * 1)(float("inf")), 1, t) == \
-        pkv.PKV_EINVAL
+    for f in (float("inf"), float("nan"), 1e10, -1e10):
+        assert pkv.lib().pkv_rope_freqs_from((ctypes.c_double * 1)(f), 1, t) == pkv.PKV_EINVAL
     assert pkv.lib().pkv_rope_freqs_from((ctypes.c_double * 1)(1.0), 0, t) == pkv.PKV_EINVAL
 
 

@@ -599,7 +599,8 @@ typedef struct {
  * as a pool's status word does, or NULL.  A draft outside [0, vocab) is
  * refused and records PKV_EBOUNDS where every draft before it was accepted; a
  * d_num_drafts outside [0, max_drafts] is limited to it and records PKV_EBOUNDS; a row without any mass gives the
- * next token -1 and records PKV_EINVAL.  Asynchronous on `stream`, no workspace;
+ * next token -1 and records PKV_EINVAL.  The outputs overlap no input.
+ * Asynchronous on `stream`, no workspace;
  * PKV_EINVAL for NULL pointers, negative sizes or strides, vocab < 1 or dtype. */
 PKV_API int verify_drafts(int32_t* d_tokens, int32_t* d_num_accepted, const pkv_probs* target,
                           const pkv_probs* draft, pkv_dtype dtype, const int32_t* d_drafts,

@@ -11,8 +11,8 @@
 // Every element is read and written once with a few operations, so memory bounds the
 // long calls and the launch and one round of loads the short ones.  Measured (one
 // call after another): 16384 tokens of 64 + 2 x 8 heads of 128 in bf16 into the pool,
-// 671 MB, 100 us (6.7 TB/s, 0.99 of the copy rate); 8192 tokens of 32 + 8 heads, 168 MB,
-// 27.9 us (0.89); 4099 tokens of 16 + 4 fp32 heads of 64, 42 MB, 7.4 us (0.83); 256
+// 671 MB, 97.5 us (6.9 TB/s, 1.01 of the copy rate); 8192 tokens of 32 + 8 heads, 168 MB,
+// 27.3 us (0.90); 4099 tokens of 16 + 4 fp32 heads of 64, 42 MB, 7.4 us (0.83); 256
 // tokens into an E4M3 pool, 10 MB, 4.1 us; one token, 2.1 us.
 //
 // A thread owns one part of a token's rows: two vectors of VEC elements, at offset
@@ -153,7 +153,7 @@ struct Part {
 // little code, so that a decode step is one wave of short blocks.  Many: a thread
 // takes kManyHeads heads, all loaded before the first is used, and its sines serve
 // them all.  Blocks of 128 threads drain and refill the SMs evenly (256 threads at
-// the same occupancy: 29 instead of 27 us on the 8K-token prompt); the blocks per SM
+// the same occupancy: 29 instead of 27 us on 8192 tokens of 32 + 8 bf16 heads of 128); the blocks per SM
 // are the fastest of 4 to 10 for each type.
 constexpr int kThreads = 128, kFewBlocks = 10, kManyHeads = 4;
 __host__ __device__ constexpr int blocks_of(int in, int kv, bool many) {
@@ -228,7 +228,9 @@ template <int IN, int KV, int VEC, bool INTER, bool MANY>
 __global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
     rope_kernel(const RopeArgs a, int parts) {
   constexpr int N = MANY ? kManyHeads : 1;
-  grid_dependency_wait();                    // everything below reads or writes memory
+  // everything below reads or writes memory (with plain loads: what the launch before
+  // wrote was not read-only while this grid was scheduled)
+  grid_dependency_wait();
   unsigned tokens = blockIdx.x, g = blockIdx.y;
   if (MANY && a.heads_first) {
     g = blockIdx.x % (unsigned)a.heads_first;
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
   const int64_t i_hs = kind == 0 ? a.q_hs : kind == 1 ? a.k_hs : a.v_hs;
   const int h = (int)g * N;
   const int h1 = min(kind == 0 ? a.Hq : a.Hk, h + N);
-  const int pos = __ldg(a.positions + t);
+  const int pos = a.positions[t];
   Loaded<IN, VEC, N> x;
   x.load(in, i0, i_hs, h, h1, p);
   if (pos < 0) return;                       // padding: no token
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
       // one after the other in the interleaved one
       const int i = INTER && VEC > 1 ? (j < VEC / 2 ? p.e0 / 2 + j : p.e1 / 2 + j - VEC / 2)
                                      : VEC * c + j;
-      const uint64_t turns = (uint64_t)(uint32_t)pos * __ldg(a.freqs + i);
+      const uint64_t turns = (uint64_t)(uint32_t)pos * a.freqs[i];
       sine<IN>((int32_t)(turns >> 32), a.m, sn[j], cs[j]);
       sn[j] *= a.sign;
     }
@@ -287,12 +289,12 @@ __global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
         put<IN, IN, VEC, INTER>(out, o0 + (h + i) * o_hs, x.a[i], x.b[i], p, cs, sn, Quant::of(1.f));
     return;
   }
-  const int64_t s = a.seq_ids ? __ldg(a.seq_ids + t) : t;
+  const int64_t s = a.seq_ids ? a.seq_ids[t] : t;
   if (s < 0 || s >= a.B || pos / a.BS >= a.max_blocks) {
     record_error(a.status, PKV_EBOUNDS);
     return;
   }
-  const int blk = __ldg(a.tables + s * a.max_blocks + pos / a.BS);
+  const int blk = a.tables[s * a.max_blocks + pos / a.BS];
   if (blk < 0 || blk >= a.num_blocks) {
     record_error(a.status, PKV_EBOUNDS);
     return;
@@ -354,7 +356,7 @@ cudaError_t pick_shape(RopeArgs& a, int sms, cudaStream_t stream) {
   const int parts = a.rd / (2 * VEC) + (a.copy_tail ? ((a.D - a.rd) / VEC + 1) / 2 : 0);
   const int64_t heads = (int64_t)a.Hq + a.Hk * (a.pool ? 2 : 1);
   // one head a thread while that is one wave of blocks (beyond it, 33 instead of 27 us
-  // on the 8K-token prompt)
+  // on 8192 tokens of 32 + 8 bf16 heads of 128)
   const bool many = a.T * heads * parts > (int64_t)sms * kFewBlocks * kThreads;
   return many ? run<IN, KV, VEC, true>(a, parts, stream) : run<IN, KV, VEC, false>(a, parts, stream);
 }

@@ -15,12 +15,12 @@
 //
 // Turning a float into 64-bit fixed point with shifts, and summing that, took 75
 // instructions an element and bound the kernel (9700 of 25000 cycles for one row of
-// 131072); additions that truncate into the significand give the same integers in 14,
+// 131072); additions that truncate into the significand give the same integers in 12,
 // see Limbs.  What is left is a chain of latencies: the drafts and their probabilities
-// (1 us), the row (1.5 us of one row on 16 SMs), the cluster's barrier (0.8 us), the
-// search (1 us).  Measured (one call after another): one sequence, 4 drafts, 131072
-// tokens 5.8 us; 32 sequences, up to 5 drafts, 131071 tokens (rows not aligned) 9.4 us;
-// 128 sequences, 3 looked-up drafts, 32768 tokens 7.8 us.
+// (0.9 us), the row (1.2 us of one row on 16 SMs), the cluster's barrier (0.8 us), the
+// search (0.8 us).  Measured (one call after another): one sequence, 4 drafts, 131072
+// tokens 5.0 us; 32 sequences, up to 5 drafts, 131071 tokens (rows not aligned) 8.5 us;
+// 128 sequences, 3 looked-up drafts, 32768 tokens 6.9 us.
 #include <algorithm>
 
 #include "device.cuh"
@@ -48,7 +48,7 @@ __device__ __forceinline__ void store_to_cta(uint64_t* p, int rank, uint64_t x) 
 
 template <int DT>
 __device__ __forceinline__ float prob(const void* p, int64_t i) {
-  if constexpr (DT == PKV_F32) return __ldg(static_cast<const float*>(p) + i);
+  if constexpr (DT == PKV_F32) return static_cast<const float*>(p)[i];
   else if constexpr (DT == PKV_F16) return __half2float(static_cast<const __half*>(p)[i]);
   else return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
@@ -56,10 +56,10 @@ __device__ __forceinline__ float prob(const void* p, int64_t i) {
 template <int DT>
 __device__ __forceinline__ void load4(const void* p, int64_t i, float* x) {
   if constexpr (DT == PKV_F32) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
+    const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
     x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
   } else {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i));
+    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
     const float2 f = unpack2<DT == PKV_BF16>(v.x), g = unpack2<DT == PKV_BF16>(v.y);
     x[0] = f.x; x[1] = f.y; x[2] = g.x; x[3] = g.y;
   }
@@ -315,16 +315,18 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   const int b = blockIdx.x / ctas, rank = blockIdx.x % ctas;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (ctas > 1) cluster_arrive();            // this CTA runs: its shared memory may be written
-  grid_dependency_wait();                    // everything below reads or writes memory
+  // everything below reads or writes memory (with plain loads: what the launch before
+  // wrote was not read-only while this grid was scheduled)
+  grid_dependency_wait();
 
   // accepted drafts: the first refused one, every warp for itself, 32 drafts at a time
   // (the first ones are loaded together with their number)
   const int* drafts = a.drafts + (int64_t)b * a.K;
   const float* u_accept = a.u_accept + (int64_t)b * a.K;
-  int x = lane < a.K ? __ldg(drafts + lane) : 0;
-  float ua = lane < a.K ? __ldg(u_accept + lane) : 0.f;
-  const float u = __ldg(a.u_sample + b);
-  int n = a.num_drafts ? __ldg(a.num_drafts + b) : a.K;
+  int x = lane < a.K ? drafts[lane] : 0;
+  float ua = lane < a.K ? u_accept[lane] : 0.f;
+  const float u = a.u_sample[b];
+  int n = a.num_drafts ? a.num_drafts[b] : a.K;
   const bool first_warp = rank == 0 && warp == 0;
   if (n < 0 || n > a.K) {
     if (first_warp && lane == 0) record_error(a.status, PKV_EBOUNDS);
@@ -338,8 +340,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   for (int j0 = 0; j0 < n; j0 += 32) {
     const int j = j0 + lane;
     if (j0 > 0 && j < n) {
-      x = __ldg(drafts + j);
-      ua = __ldg(u_accept + j);
+      x = drafts[j];
+      ua = u_accept[j];
     }
     const bool in = x >= 0 && x < a.V;
     bool ok = j >= n;
@@ -422,7 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     for (int j = tid; j <= a.K; j += THREADS)
       if (j != acc || all == 0)
         a.tokens[(int64_t)b * (a.K + 1) + j] =
-            j < acc ? __ldg(drafts + j) : -1;
+            j < acc ? drafts[j] : -1;
     if (tid == 0) {
       a.num_accepted[b] = acc;
       if (all == 0) record_error(a.status, PKV_EINVAL);

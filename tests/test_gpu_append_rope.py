@@ -155,6 +155,45 @@ def test_rotated_once_equals_rope_then_append(pkv):
     assert torch.equal(q, s.q_out) and torch.equal(other.storage, s.pool.storage)
 
 
+@pytest.mark.parametrize("kv,dt", [("bf16", "bf16"), ("f32", "f32"), ("e4m3", "f16")])
+@pytest.mark.parametrize("inter", [False, True])
+def test_odd_bases_and_strides(pkv, kv, dt, inter):
+    """k one element off, v with an odd token stride, q as [heads, tokens] in memory."""
+    s = Step(pkv, [13, 60], [7, 4], hq=4, hk=2, D=48, kv=kv, dt=dt, seed=50, joint=False)
+    s.k = _x((s.T * 2 * 48 + 1,), s.dt, 51)[1:].view(s.T, 2, 48)
+    s.v = _x((s.T, 2 * 48 + 1), s.dt, 52)[:, :96].unflatten(1, (2, 48))
+    s.q = _x((4, s.T, 48), s.dt, 53).transpose(0, 1)
+    for rd in (48, 20):
+        s.pool.storage.copy_(s.before)
+        freqs, m = ref.frequencies(rd)
+        s.pool.append_rope(0, s.q_out, s.q, s.k, s.v, pkv.Rope(rd, interleaved=inter), s.tables,
+                           s.pos, seq_ids=s.seq, k_scale=0.01, v_scale=0.02)
+        assert s.pool.check_status() == 0
+        s.check(0, freqs, m, rd, inter, 0.01, 0.02)
+
+
+def test_two_streams_at_once(pkv):
+    a = Step(pkv, [100, 3], [900, 800], hq=16, hk=4, D=128, seed=54)
+    b = Step(pkv, [7], [1500], hq=16, hk=4, D=128, kv="e4m3", seed=55)
+    rope = pkv.Rope(128)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, st in zip((a, b), streams):
+            s.pool.append_rope(0, s.q_out, s.q, s.k, s.v, rope, s.tables, s.pos, seq_ids=s.seq,
+                               k_scale=0.01, v_scale=0.01, stream=st)
+    torch.cuda.synchronize()
+    freqs, m = ref.frequencies(128)
+    for s in (a, b):
+        assert s.pool.check_status() == 0
+        other = pkv.KVPool(s.geom, storage=s.before.clone())
+        q = torch.empty_like(s.q_out)
+        other.append_rope(0, q, s.q, s.k, s.v, rope, s.tables, s.pos, seq_ids=s.seq,
+                          k_scale=0.01, v_scale=0.01)
+        assert torch.equal(q, s.q_out) and torch.equal(other.storage, s.pool.storage)
+        ref.check_rotated(s.q_out[::113], s.q[::113], s.pos[::113], freqs, m, 128, False)
+
+
 def test_in_place_queries(pkv):
     s = Step(pkv, [50], [20], seed=42)
     q0 = s.q.clone()

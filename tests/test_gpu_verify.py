@@ -199,6 +199,31 @@ def test_kept_tokens_follow_the_target(pkv):
     assert bool(((freq - p.double()).abs() <= 5 * sd).all())
 
 
+def test_two_streams_at_once(pkv):
+    cases = [_case(20, 3, 50000, seed=40), _case(1, 4, 131072, seed=41)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [(torch.empty(c[2].shape[0], c[2].shape[1] + 1, dtype=torch.int32, device="cuda"),
+             torch.empty(c[2].shape[0], dtype=torch.int32, device="cuda")) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, o, st in zip(cases, outs, streams):
+            pkv.verify_drafts(*o, *c, stream=st)
+    torch.cuda.synchronize()
+    for c, o in zip(cases, outs):
+        want, n = ref.verify(*c)
+        assert o[0].tolist() == want and o[1].tolist() == n
+
+
+@pytest.mark.parametrize("lookup", [False, True])
+@pytest.mark.parametrize("sharp", [6.0, 30.0])
+def test_peaked_rows(pkv, sharp, lookup):
+    """Most of the mass on a few tokens, among them ones above 2^-8 next to one another."""
+    t, q, x, ua, us = _case(30, 4, 40001, seed=42, sharp=sharp, noise=1.0)
+    t[:10, :, 500:530] += 0.5 / 30
+    q[:10, :, 505:520] += 0.1
+    _check(pkv, t, None if lookup else q, x, ua, us)
+
+
 def test_another_stream_and_graph_replay(pkv):
     args = _case(4, 3, 9000, seed=13)
     t, q, x, ua, us = args

@@ -76,35 +76,46 @@ __device__ __forceinline__ uint64_t fixed(float x) {
   return sig >> min(127u - e, 63u);
 }
 
-// A sum of floor(x 2^54) in two limbs, 2^-31 and 2^-54, for x in [0, 2^-8]:
-// 2^-8 + x rounded toward zero has floor(x 2^31) in its significand, and 2^-31 plus
-// the rest of x (exact) the lower limb.  The words are added with their exponent
-// bits, which `value` takes off again: n additions, at most 511.
+// A sum of floor(x 2^54) in limbs.  Small values, x in [0, 2^-8]: 2^-8 + x rounded
+// toward zero has floor(x 2^31) in its significand, and 2^-31 plus the rest of x
+// (exact) the 23 bits behind it.  Any value, x in [0, 1]: the same from 1 and 2^-23,
+// units of 2^-23 and 2^-46, and 2^-46 plus what is still left has the last 8 bits on
+// top of its significand.  The words are added with their exponent bits, which `value`
+// takes off again: n additions, at most 255.
 constexpr float kSmall = 0x1p-8f;
+template <bool SMALL>
 struct Limbs {
-  uint32_t hi = 0, lo = 0;
-  __device__ __forceinline__ static void split(float x, uint32_t& h, uint32_t& l) {
-    const float t = __fadd_rz(x, 0x1p-8f);
+  uint32_t hi = 0, lo = 0, last = 0;
+  __device__ __forceinline__ static void split(float x, uint32_t& h, uint32_t& l, uint32_t& m) {
+    constexpr float A = SMALL ? 0x1p-8f : 1.f, B = SMALL ? 0x1p-31f : 0x1p-23f;
+    const float t = __fadd_rz(x, A), r = x - (t - A), u = __fadd_rz(r, B);
     h = __float_as_uint(t);
-    l = __float_as_uint(__fadd_rz(x - (t - 0x1p-8f), 0x1p-31f));
+    l = __float_as_uint(u);
+    if (!SMALL) m = (__float_as_uint(__fadd_rz(r - (u - B), 0x1p-46f)) & 0x7fffffu) >> 15;
   }
   __device__ __forceinline__ void add(float x) {
-    uint32_t h, l;
-    split(x, h, l);
+    uint32_t h, l, m = 0;
+    split(x, h, l, m);
     hi += h;
     lo += l;
+    if (!SMALL) last += m;
   }
-  __device__ __forceinline__ void add_difference(float x, float y) {   // x >= y
-    uint32_t h, l, g, k;
-    split(x, h, l);
-    split(y, g, k);
+  // x >= y; limbs modulo 2^32, negative sums of the lower ones sign-extended below
+  __device__ __forceinline__ void add_difference(float x, float y) {
+    uint32_t h, l, m = 0, g, k, o = 0;
+    split(x, h, l, m);
+    split(y, g, k, o);
     hi += h - g;
-    lo += l - k;       // modulo 2^32: a negative sum of the limb is sign-extended below
+    lo += l - k;
+    if (!SMALL) last += m - o;
   }
   // n: the additions whose exponent bits did not cancel
   __device__ __forceinline__ uint64_t value(int n) const {
-    const int32_t l = (int32_t)(lo - (uint32_t)n * 0x30000000u);
-    return ((uint64_t)(hi - (uint32_t)n * 0x3b800000u) << 23) + (uint64_t)(int64_t)l;
+    constexpr uint32_t A = SMALL ? 0x3b800000u : 0x3f800000u, B = SMALL ? 0x30000000u : 0x34000000u;
+    const uint64_t h = hi - (uint32_t)n * A;
+    const int64_t l = (int32_t)(lo - (uint32_t)n * B);
+    return SMALL ? (h << 23) + (uint64_t)l
+                 : (h << 31) + ((uint64_t)l << 8) + (uint64_t)(int64_t)(int32_t)last;
   }
 };
 
@@ -140,10 +151,21 @@ __device__ __forceinline__ uint64_t weight(float p, float q) {
   return fixed(p) - fixed(fminf(fmaxf(q, 0.f), p));
 }
 
+template <bool Q, bool SMALL>
+__device__ __forceinline__ uint64_t limb_sum(const float (&p)[kStep], const float (&q)[kStep]) {
+  Limbs<SMALL> sum;
+#pragma unroll
+  for (int j = 0; j < kStep; ++j) {
+    if (Q) sum.add_difference(p[j], fminf(q[j], p[j]));
+    else sum.add(p[j]);
+  }
+  return sum.value(Q ? 0 : kStep);
+}
+
 // The sum of a lane's weights, each max(p - q, 0) = p - min(p, q).  The bits of a
 // float from 0 to 2^-8, as an integer, are at most 2^-8's; negative ones and NaN are
 // above every other: one integer maximum tells whether all values are as they should
-// be and small enough for Limbs.
+// be and small.  Whole warps.
 template <bool Q>
 __device__ __forceinline__ uint64_t lane_sum(float (&p)[kStep], float (&q)[kStep]) {
   uint32_t top = 0, top_q = 0;
@@ -152,37 +174,15 @@ __device__ __forceinline__ uint64_t lane_sum(float (&p)[kStep], float (&q)[kStep
     top = max(top, __float_as_uint(p[j]));
     if (Q) top_q = max(top_q, __float_as_uint(q[j]));
   }
-  uint64_t s = 0;
-  if (top > __float_as_uint(kSmall) || top_q > 0x7f800000u) {
-    // the few larger ones (at most 256 of a row) are taken out, one at a time
-    uint32_t large = 0;
-#pragma unroll
-    for (int j = 0; j < kStep; ++j) {
-      p[j] = clean(p[j]);
-      if (Q) q[j] = fmaxf(q[j], 0.f);
-      if (p[j] > kSmall) large |= 1u << j;
-    }
-    while (large) {
-      const int j = __ffs(large) - 1;
-      large &= large - 1;
-      float x = 0.f, y = 0.f;
-#pragma unroll
-      for (int i = 0; i < kStep; ++i)
-        if (i == j) {
-          x = p[i];
-          p[i] = 0.f;
-          if (Q) y = q[i];
-        }
-      s += weight(x, y);
-    }
-  }
-  Limbs sum;
+  if (!__any_sync(0xffffffffu, top > __float_as_uint(kSmall) || top_q > 0x7f800000u))
+    return limb_sum<Q, true>(p, q);
+  // a long row has at most 256 probabilities above 2^-8
 #pragma unroll
   for (int j = 0; j < kStep; ++j) {
-    if (Q) sum.add_difference(p[j], fminf(q[j], p[j]));
-    else sum.add(p[j]);
+    p[j] = clean(p[j]);
+    if (Q) q[j] = fmaxf(q[j], 0.f);
   }
-  return s + sum.value(Q ? 0 : kStep);
+  return limb_sum<Q, false>(p, q);
 }
 
 // A lane's share of elements [i0, i0 + left); FULL: left is 32 kStep.

@@ -22,6 +22,7 @@
 // tokens 5.0 us; 32 sequences, up to 5 drafts, 131071 tokens (rows not aligned) 8.5 us;
 // 128 sequences, 3 looked-up drafts, 32768 tokens 6.9 us.
 #include <algorithm>
+#include <atomic>
 
 #include "device.cuh"
 #include "launch.h"
@@ -432,31 +433,71 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
   }
 }
 
+// Clusters of this size may be launched (above 8 only when asked for).
+template <int DT, int THREADS>
+cudaError_t allow_clusters(int ctas) {
+  return ctas <= 8 ? cudaSuccess
+                   : cudaFuncSetAttribute(verify_kernel<DT, THREADS>,
+                                          cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+}
+
 template <int DT, int THREADS>
 cudaError_t run(const VerifyArgs& a, int ctas, cudaStream_t stream) {
   // a warp's piece: a multiple of 128 elements
   const int64_t unit = (int64_t)ctas * THREADS * 4;
   const int piece = (int)((a.V + unit - 1) / unit * 128);
-  if (ctas > 8) {                            // above the portable cluster size
-    const cudaError_t e = cudaFuncSetAttribute(
-        verify_kernel<DT, THREADS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_clusters<DT, THREADS>(ctas);
+  if (e != cudaSuccess) return e;
   return launch_chained(verify_kernel<DT, THREADS>, dim3((unsigned)(a.B * ctas)), dim3(THREADS),
                         ctas, stream, a, ctas, piece);
 }
 
+// Clusters of 2^k CTAs that the current device holds at once (0 if it cannot say).
+template <int DT>
+int clusters_at_once(int k) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][5];       // the number + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
+  int n = known[dev][k].load(std::memory_order_relaxed) - 1;
+  if (n >= 0) return n;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1u << k);
+  cfg.blockDim = dim3(512);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 1u << k;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (allow_clusters<DT, 512>(1 << k) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, verify_kernel<DT, 512>, &cfg) != cudaSuccess)
+    n = 0;
+  known[dev][k].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+// CTAs of 512 threads to a sequence.  A CTA wants 5120 tokens of the row or more (16384
+// where that saves the cluster: one CTA has nothing to exchange, 0.8 us), and more
+// clusters than run at once cost a second wave (32 rows of 116985: 8.1 us with 8 CTAs
+// each, 14.2 with 16).  CTAs that would share an SM are halved in number while the
+// rest's slices stay short (64 rows of 24576: 6.2 us with 2, 6.5 with 4; 100 rows of
+// 32768: 6.9 us with 1, 7.8 with 2; but 64 rows of 65536: 8.9 with 2, 8.1 with 4).  A
+// long row that one SM takes alone gets 1024 threads (100 rows of 116985: 21.7 us,
+// 24.3 with 2 CTAs of 512; for 32768 tokens 512 are 5 to 10% faster).
 template <int DT>
 cudaError_t pick(const VerifyArgs& a, int sms, cudaStream_t stream) {
-  // CTAs per sequence: as many as run at the same time (two to an SM), with at least
-  // 4096 tokens of the row each
-  int ctas = 1;
-  while (ctas < kMaxCtas && (int64_t)a.B * ctas * 2 <= 2 * sms && a.V / (2 * ctas) >= 4096)
-    ctas *= 2;
-  if ((int64_t)a.B * ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  // two to a sequence would be the whole SM: one of twice the threads needs no cluster
-  if (ctas == 2) return run<DT, 1024>(a, 1, stream);
-  return run<DT, 512>(a, ctas, stream);
+  constexpr int kAlone = 40960;
+  int k = 0;
+  if (a.V > 16384)
+    while (1 << k < kMaxCtas && a.V >> (k + 1) >= 5120) ++k;
+  while (k > 0 && a.B > clusters_at_once<DT>(k)) --k;
+  while (k > 0 && k < 4 && ((int64_t)a.B << k) > sms &&
+         a.V >> (k - 1) <= (k == 1 ? kAlone : 24576))
+    --k;
+  if (k == 1 && 2 * (int64_t)a.B > sms) k = 0;
+  if (k == 0 && a.B <= sms && a.V > kAlone) return run<DT, 1024>(a, 1, stream);
+  return run<DT, 512>(a, 1 << k, stream);
 }
 
 }  // namespace

@@ -126,7 +126,9 @@ inline cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, u
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  if (e != cudaSuccess) cudaGetLastError();   // the caller gets e, not the next launch
+  return e;
 }
 
 // ---------------------------------------------------------------- ldmatrix / movmatrix / mma

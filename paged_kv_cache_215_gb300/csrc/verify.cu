@@ -19,8 +19,8 @@
 // see Limbs.  What is left is a chain of latencies: the drafts and their probabilities
 // (0.9 us), the row (1.2 us of one row on 16 SMs), the cluster's barrier (0.8 us), the
 // search (0.8 us).  Measured (one call after another): one sequence, 4 drafts, 131072
-// tokens 5.0 us; 32 sequences, up to 5 drafts, 131071 tokens (rows not aligned) 8.5 us;
-// 128 sequences, 3 looked-up drafts, 32768 tokens 6.9 us.
+// tokens 4.9 us; 32 sequences, up to 5 drafts, 131071 tokens (rows not aligned) 8.5 us;
+// 128 sequences, 3 looked-up drafts, 32768 tokens 6.0 us.
 #include <algorithm>
 #include <atomic>
 
@@ -471,8 +471,10 @@ int clusters_at_once(int k) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if (allow_clusters<DT, 512>(1 << k) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, verify_kernel<DT, 512>, &cfg) != cudaSuccess)
+      cudaOccupancyMaxActiveClusters(&n, verify_kernel<DT, 512>, &cfg) != cudaSuccess) {
     n = 0;
+    cudaGetLastError();
+  }
   known[dev][k].store(n + 1, std::memory_order_relaxed);
   return n;
 }

@@ -228,14 +228,14 @@ PKV_API int kv_fp8_scale(const float* d_amax, int n, float* d_scale, cudaStream_
 /* ---------------------------------------------------------------- rotary positions */
 
 /* Rotary positions ([UNLOCK], RoPE extrapolation: position interpolation, NTK-aware
- * scaling and YaRN): the pairs i < rotary_dim / 2 of a head's row at position p turn by the
- * angle p * f_i,
+ * scaling and YaRN): the pairs i < rotary_dim / 2 of a head's row at position p turn
+ * by the angle p * f_i,
  *   (a, b) -> attn_scale * (a cos - b sin, a sin + b cos),
  * with (a, b) = (x[i], x[i + rotary_dim / 2]) in the half layout and
  * (x[2i], x[2i + 1]) in the interleaved one; elements from rotary_dim on are
- * unchanged.A frequency is held as the fraction of a full turn per position,
- * in units of 2^-64 turns (uint64): p times it, modulo 2^64, is the angle reduced
- * to one turn, off by at most p 2^-63 turns (2^-32 at the largest position). */
+ * unchanged.  A frequency is held as the fraction of a full turn per position, in
+ * units of 2^-64 turns (uint64): p times it, modulo 2^64, is the angle reduced to
+ * one turn, off by at most p 2^-63 turns (2^-32 at the largest position). */
 typedef enum {
   PKV_ROPE_NONE = 0,   /* f_i = base^(-2 i / r), r = rotary_dim */
   PKV_ROPE_LINEAR = 1, /* position interpolation: f_i / factor */
@@ -598,10 +598,10 @@ typedef struct {
  * value below 1.  d_status: device int32 (zero: no error) that takes the first error,
  * as a pool's status word does, or NULL.  A draft outside [0, vocab) is
  * refused and records PKV_EBOUNDS where every draft before it was accepted; a
- * d_num_drafts outside [0, max_drafts] is limited to it and records PKV_EBOUNDS; a row without any mass gives the
- * next token -1 and records PKV_EINVAL.  The outputs overlap no input.
- * Asynchronous on `stream`, no workspace;
- * PKV_EINVAL for NULL pointers, negative sizes or strides, vocab < 1 or dtype. */
+ * d_num_drafts outside [0, max_drafts] is limited to it and records PKV_EBOUNDS; a
+ * row without any mass gives the next token -1 and records PKV_EINVAL.  The outputs
+ * overlap no input.  Asynchronous on `stream`, no workspace; PKV_EINVAL for NULL
+ * pointers, negative sizes or strides, vocab < 1 or dtype. */
 PKV_API int verify_drafts(int32_t* d_tokens, int32_t* d_num_accepted, const pkv_probs* target,
                           const pkv_probs* draft, pkv_dtype dtype, const int32_t* d_drafts,
                           const int32_t* d_num_drafts, const float* d_u_accept,

@@ -1180,8 +1180,8 @@ int rope_apply(const pkv_rows* q_out, const pkv_rows* q, int num_q_heads, const 
                const int32_t* d_positions, int64_t num_tokens, const pkv_rope* rope, int backward,
                cudaStream_t stream) {
   if (num_tokens < 0 || num_q_heads < 1 || num_k_heads < 0 || num_q_heads > 65535 ||
-      num_k_heads > 65535 - num_q_heads || head_dim < 2 || head_dim > 512 || !act_dtype(dtype) || backward < 0 ||
-      backward > 1 || !rope_ok(rope, head_dim))
+      num_k_heads > 65535 - num_q_heads || head_dim < 2 || head_dim > 512 || !act_dtype(dtype) ||
+      backward < 0 || backward > 1 || !rope_ok(rope, head_dim))
     return PKV_EINVAL;
   if (num_tokens == 0) return PKV_OK;
   if (num_tokens > 0x7fffffffLL || !d_positions) return PKV_EINVAL;

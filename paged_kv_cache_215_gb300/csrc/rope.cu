@@ -153,8 +153,8 @@ struct Part {
 // little code, so that a decode step is one wave of short blocks.  Many: a thread
 // takes kManyHeads heads, all loaded before the first is used, and its sines serve
 // them all.  Blocks of 128 threads drain and refill the SMs evenly (256 threads at
-// the same occupancy: 29 instead of 27 us on 8192 tokens of 32 + 8 bf16 heads of 128); the blocks per SM
-// are the fastest of 4 to 10 for each type.
+// the same occupancy: 29 instead of 27 us on 8192 tokens of 32 + 8 bf16 heads of 128);
+// the blocks per SM are the fastest of 4 to 10 for each type.
 constexpr int kThreads = 128, kFewBlocks = 10, kManyHeads = 4;
 __host__ __device__ constexpr int blocks_of(int in, int kv, bool many) {
   return !many ? kFewBlocks : kv == PKV_FP8_E4M3 ? 5 : in == PKV_F32 ? 9 : 6;
@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (N == 1 || h + i < h1)
-        put<IN, IN, VEC, INTER>(out, o0 + (h + i) * o_hs, x.a[i], x.b[i], p, cs, sn, Quant::of(1.f));
+        put<IN, IN, VEC, INTER>(out, o0 + (h + i) * o_hs, x.a[i], x.b[i], p, cs, sn,
+                                Quant::of(1.f));
     return;
   }
   const int64_t s = a.seq_ids ? a.seq_ids[t] : t;
@@ -358,7 +359,8 @@ cudaError_t pick_shape(RopeArgs& a, int sms, cudaStream_t stream) {
   // one head a thread while that is one wave of blocks (beyond it, 33 instead of 27 us
   // on 8192 tokens of 32 + 8 bf16 heads of 128)
   const bool many = a.T * heads * parts > (int64_t)sms * kFewBlocks * kThreads;
-  return many ? run<IN, KV, VEC, true>(a, parts, stream) : run<IN, KV, VEC, false>(a, parts, stream);
+  return many ? run<IN, KV, VEC, true>(a, parts, stream)
+              : run<IN, KV, VEC, false>(a, parts, stream);
 }
 
 template <int IN, int KV>

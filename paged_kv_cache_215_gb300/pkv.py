@@ -396,9 +396,9 @@ class KVPool:
         q_out, in one launch.  q, k, v and q_out are [tokens, heads, head_dim] with
         unit stride along head_dim (views of a joint projection are fine; q_out may
         be q); q_out = q = None stores keys and values only."""
-        rc = _tensors.append_rope(self.handle.value if self.handle else 0, self.storage, layer, q_out, q, k, v,
-                                  rope.freqs, rope.address, tables, positions, seq_ids, k_scale,
-                                  v_scale, stream)
+        rc = _tensors.append_rope(self.handle.value if self.handle else 0, self.storage, layer,
+                                  q_out, q, k, v, rope.freqs, rope.address, tables, positions,
+                                  seq_ids, k_scale, v_scale, stream)
         if rc:
             raise PkvError(rc, "kv_append_rope")
         return q_out

@@ -8,8 +8,8 @@ attention scale (2^-24 of the product) and the value (2^-24), plus the final
 addition (2^-24 of a sum up to |a| + |b|): below 2^-21 (|a| + |b|) m together.
 The angle itself is off by the roundings of the frequency, of its quotient by 2 pi
 and of this reference's product, 2^-53 of it each: 2^-51 radians per position in all
-(frequencies up to 1).  16-bit outputs may take the special-function unit's sine, off by up to 2^-20.9 in
-[-pi, pi], so 2^-19 is allowed there.  Storing rounds once: half a step,
+(frequencies up to 1).  16-bit outputs may take the special-function unit's sine, off
+by up to 2^-20.9 in [-pi, pi], so 2^-19 is allowed there.  Storing rounds once: half a step,
 torch.finfo(dtype).eps / 2 of the value, and half the smallest subnormal."""
 import math
 

@@ -15,11 +15,11 @@
 // 27.3 us (0.90); 4099 tokens of 16 + 4 fp32 heads of 64, 42 MB, 7.4 us (0.83); 256
 // tokens into an E4M3 pool, 10 MB, 4.1 us; one token, 2.1 us.
 //
-// A thread owns one part of a token's rows: two vectors of VEC elements, at offset
-// e0 and half the rotated part further on, the same for both layouts (their pairs
-// lie across the two vectors or within each), so that neighbouring threads read
-// neighbouring 16 bytes.  Its sines and cosines are computed once and used for every
-// head it visits.
+// A thread owns one part of a token's rows: two vectors of VEC elements, so that
+// neighbouring threads read neighbouring 16 bytes.  In the half layout they lie half
+// the rotated part apart and hold VEC pairs across them; in the interleaved one they
+// lie half the row apart and hold their pairs within them.  Its sines and cosines are
+// computed once and used for every head it visits.
 #include <algorithm>
 
 #include "device.cuh"
@@ -144,10 +144,14 @@ __device__ __forceinline__ void sine(int32_t turns, float m, float& s, float& c)
 
 // One part of a row.
 struct Part {
-  int e0, e1;       // offsets of its vectors in the head
-  bool second;      // the vector at e1 exists
-  bool turn;        // rotate, otherwise copy
+  int e0, e1;        // offsets of its vectors in the head
+  bool second;       // the vector at e1 exists
+  bool turn0, turn1; // rotate the vector (both or none but in a mixed row), else copy
 };
+
+// How a row's pairs lie.  kMixed rows (interleaved, not turned from end to end) are
+// taken vector by vector: turned, copied, or turned up to where the rotated part ends.
+enum Rowing { kHalf, kInter, kMixed };
 
 // Two shapes of the kernel.  Few: a thread takes one head, with few registers and
 // little code, so that a decode step is one wave of short blocks.  Many: a thread
@@ -176,55 +180,99 @@ struct Loaded {
   }
 };
 
-// One head's part, rotated or copied, and stored as type KV.
-template <int IN, int KV, int VEC, bool INTER>
-__device__ __forceinline__ void put(void* out, int64_t to, const Vec<IN, VEC>& a,
-                                    const Vec<IN, VEC>& b, const Part& p, const float (&cs)[VEC],
-                                    const float (&sn)[VEC], const Quant& quant) {
-  if constexpr (KV == IN) {
-    if (!p.turn) {
-      a.store(out, to + p.e0);
-      if (p.second) b.store(out, to + p.e1);
-      return;
-    }
+// (u, v) turned, rounded the same way in every shape of the kernel, so that a token's
+// values do not depend on the tokens beside it.
+__device__ __forceinline__ void turn_pair(float u, float v, float c, float s, float& x, float& y) {
+  x = fmaf(u, c, -__fmul_rn(v, s));
+  y = fmaf(u, s, __fmul_rn(v, c));
+}
+
+// The first n pairs (0, 1), (2, 3) ... of a vector turned.
+template <int VEC>
+__device__ __forceinline__ void turn_within(float (&x)[VEC], const float* cs, const float* sn,
+                                            int n) {
+#pragma unroll
+  for (int j = 0; j < VEC / 2; ++j) {
+    if (j < n) turn_pair(x[2 * j], x[2 * j + 1], cs[j], sn[j], x[2 * j], x[2 * j + 1]);
   }
-  float x[VEC], y[VEC];
-  a.get(x);
-  if (p.second) b.get(y);
-  if (p.turn) {
-    if constexpr (INTER && VEC > 1) {
-      // pairs (0, 1), (2, 3) ... of each vector
-#pragma unroll
-      for (int j = 0; j < VEC; j += 2) {
-        const float u = x[j], v = x[j + 1], s = y[j], t = y[j + 1];
-        const int k = j / 2, l = VEC / 2 + j / 2;
-        x[j] = u * cs[k] - v * sn[k];
-        x[j + 1] = u * sn[k] + v * cs[k];
-        y[j] = s * cs[l] - t * sn[l];
-        y[j + 1] = s * sn[l] + t * cs[l];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float u = x[j], v = y[j];
-        x[j] = u * cs[j] - v * sn[j];
-        y[j] = u * sn[j] + v * cs[j];
-      }
+}
+
+// A vector stored as type KV: as it came, or (turned) from x with its first n pairs
+// changed.
+template <int IN, int KV, int VEC>
+__device__ __forceinline__ void put_vector(void* out, int64_t to, const Vec<IN, VEC>& raw,
+                                           const float (&x)[VEC], bool turned, int n,
+                                           const Quant& quant) {
+  if constexpr (KV == IN) {
+    if (!turned) {
+      raw.store(out, to);
+      return;
     }
   }
   Vec<KV, VEC> o;
   o.set(x, quant);
-  o.store(out, to + p.e0);
-  if (p.second) {
-    o.set(y, quant);
-    o.store(out, to + p.e1);
+  if constexpr (KV == IN && VEC > 1) {
+    // elements behind the rotated part bit for bit (NaN among them)
+    if (n < VEC / 2) {
+      constexpr int W = elem_size(IN) / 2;     // words a pair
+#pragma unroll
+      for (int j = 0; j < VEC / 2 * W; ++j)
+        if (j >= n * W) o.w[j] = raw.w[j];
+    }
+  }
+  o.store(out, to);
+}
+
+// One head's part, rotated or copied, and stored as type KV.  rd: the rotated elements.
+template <int IN, int KV, int VEC, int ROW>
+__device__ __forceinline__ void put(void* out, int64_t to, const Vec<IN, VEC>& a,
+                                    const Vec<IN, VEC>& b, const Part& p, int rd,
+                                    const float (&cs)[VEC], const float (&sn)[VEC],
+                                    const Quant& quant) {
+  if constexpr (ROW == kMixed) {
+    float x[VEC];
+    if (KV != IN || p.turn0) a.get(x);
+    const int n0 = min(VEC / 2, (rd - p.e0) / 2), n1 = min(VEC / 2, (rd - p.e1) / 2);
+    if (p.turn0) turn_within<VEC>(x, cs, sn, n0);
+    put_vector<IN, KV, VEC>(out, to + p.e0, a, x, p.turn0, n0, quant);
+    if (!p.second) return;
+    if (KV != IN || p.turn1) b.get(x);
+    if (p.turn1) turn_within<VEC>(x, cs + VEC / 2, sn + VEC / 2, n1);
+    put_vector<IN, KV, VEC>(out, to + p.e1, b, x, p.turn1, n1, quant);
+  } else {
+    if constexpr (KV == IN) {
+      if (!p.turn0) {
+        a.store(out, to + p.e0);
+        if (p.second) b.store(out, to + p.e1);
+        return;
+      }
+    }
+    float x[VEC], y[VEC];
+    a.get(x);
+    if (p.second) b.get(y);
+    if (p.turn0) {
+      if constexpr (ROW == kInter && VEC > 1) {
+        turn_within<VEC>(x, cs, sn, VEC / 2);
+        turn_within<VEC>(y, cs + VEC / 2, sn + VEC / 2, VEC / 2);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) turn_pair(x[j], y[j], cs[j], sn[j], x[j], y[j]);
+      }
+    }
+    Vec<KV, VEC> o;
+    o.set(x, quant);
+    o.store(out, to + p.e0);
+    if (p.second) {
+      o.set(y, quant);
+      o.store(out, to + p.e1);
+    }
   }
 }
 
 // grid (token groups, head groups, part groups), or with heads_first (both, the
 // heads_first head groups of some tokens next to one another; 1; part groups).  Head
 // groups of q first, then of k, then (with a pool) of v; block (parts of a row, tokens).
-template <int IN, int KV, int VEC, bool INTER, bool MANY>
+template <int IN, int KV, int VEC, int ROW, bool MANY>
 __global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
     rope_kernel(const RopeArgs a, int parts) {
   constexpr int N = MANY ? kManyHeads : 1;
@@ -241,20 +289,29 @@ __global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
   if (t >= a.T || c >= parts) return;
   const int kind = g < (unsigned)a.groups_q ? 0 : g < (unsigned)(a.groups_q + a.groups_k) ? 1 : 2;
   if (kind > 0) g -= a.groups_q + (kind == 2 ? a.groups_k : 0);
-  const int turning = a.rd / (2 * VEC);
   Part p;
-  if (c < turning) {
-    // one interleaved pair when VEC is 1; else the same two vectors in both layouts
-    p.e0 = INTER && VEC == 1 ? 2 * c : VEC * c;
-    p.e1 = INTER && VEC == 1 ? 2 * c + 1 : VEC * c + a.rd / 2;
-    p.second = true;
-    p.turn = kind < 2;
+  if constexpr (ROW == kMixed) {
+    const int vectors = a.D / VEC, half = (vectors + 1) / 2;
+    p.e0 = VEC * c;
+    p.e1 = VEC * (c + half);
+    p.second = c + half < vectors;
+    p.turn0 = kind < 2 && p.e0 < a.rd;
+    p.turn1 = kind < 2 && p.second && p.e1 < a.rd;
   } else {
-    const int rest = (a.D - a.rd) / VEC, half = (rest + 1) / 2;
-    p.e0 = a.rd + VEC * (c - turning);
-    p.e1 = p.e0 + VEC * half;
-    p.second = c - turning + half < rest;
-    p.turn = false;
+    const int turning = a.rd / (2 * VEC);
+    if (c < turning) {
+      // one pair of neighbours where VEC is 1
+      p.e0 = ROW == kInter && VEC == 1 ? 2 * c : VEC * c;
+      p.e1 = ROW == kInter && VEC == 1 ? 2 * c + 1 : VEC * c + a.rd / 2;
+      p.second = true;
+      p.turn0 = p.turn1 = kind < 2;
+    } else {
+      const int rest = (a.D - a.rd) / VEC, half = (rest + 1) / 2;
+      p.e0 = a.rd + VEC * (c - turning);
+      p.e1 = p.e0 + VEC * half;
+      p.second = c - turning + half < rest;
+      p.turn0 = p.turn1 = false;
+    }
   }
   // the heads' loads go out before the position is known
   const void* in = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
@@ -267,13 +324,15 @@ __global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
   x.load(in, i0, i_hs, h, h1, p);
   if (pos < 0) return;                       // padding: no token
   float cs[VEC], sn[VEC];
-  if (p.turn) {
+  if (p.turn0) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      // the pair's index: element e0 + j of the half layout; pairs of the two vectors
-      // one after the other in the interleaved one
-      const int i = INTER && VEC > 1 ? (j < VEC / 2 ? p.e0 / 2 + j : p.e1 / 2 + j - VEC / 2)
-                                     : VEC * c + j;
+      // the pair's index; interleaved: the pairs of one vector, then of the other (of a
+      // mixed row's last pair again where the rotated part ends inside)
+      if (ROW == kMixed && j >= VEC / 2 && !p.turn1) break;
+      int i = VEC * c + j;
+      if (ROW != kHalf && VEC > 1) i = j < VEC / 2 ? p.e0 / 2 + j : p.e1 / 2 + j - VEC / 2;
+      if (ROW == kMixed) i = min(i, a.rd / 2 - 1);
       const uint64_t turns = (uint64_t)(uint32_t)pos * a.freqs[i];
       sine<IN>((int32_t)(turns >> 32), a.m, sn[j], cs[j]);
       sn[j] *= a.sign;
@@ -286,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (N == 1 || h + i < h1)
-        put<IN, IN, VEC, INTER>(out, o0 + (h + i) * o_hs, x.a[i], x.b[i], p, cs, sn,
+        put<IN, IN, VEC, ROW>(out, o0 + (h + i) * o_hs, x.a[i], x.b[i], p, a.rd, cs, sn,
                                 Quant::of(1.f));
     return;
   }
@@ -307,13 +366,14 @@ __global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (N == 1 || h + i < h1)
-      put<IN, KV, VEC, INTER>(
-          a.pool, o0 + (h + i) * o_hs, x.a[i], x.b[i], p, cs, sn,
+      put<IN, KV, VEC, ROW>(
+          a.pool, o0 + (h + i) * o_hs, x.a[i], x.b[i], p, a.rd, cs, sn,
           Quant::of(KV == PKV_FP8_E4M3 && a.block_scales ? a.block_scales[tile + h + i] : scale));
 }
 
-// The widest part (elements) every row can be loaded and stored in: parts lie in
-// the halves (pairs) of the rotated part and in the rest, 16 bytes at most.
+// The widest vector (elements, 16 bytes at most) every row can be loaded and stored
+// in: the vectors tile the row (interleaved), or the halves of the rotated part and the
+// rest (half layout).
 int widest(const RopeArgs& a) {
   const int e = elem_size(a.in_dtype);
   for (int vec = 16 / e; vec > 1; vec /= 2) {
@@ -321,12 +381,28 @@ int widest(const RopeArgs& a) {
     auto ok = [&](const void* p, int64_t ts, int64_t hs) {
       return p == nullptr || ((uintptr_t)p % bytes == 0 && ts % vec == 0 && hs % vec == 0);
     };
-    if (a.rd % (2 * vec) == 0 && (a.D - a.rd) % vec == 0 && ok(a.q, a.q_ts, a.q_hs) &&
-        ok(a.qo, a.qo_ts, a.qo_hs) && ok(a.k, a.k_ts, a.k_hs) && ok(a.ko, a.ko_ts, a.ko_hs) &&
-        ok(a.v, a.v_ts, a.v_hs))
+    const bool tiles = a.D % vec == 0 && (a.interleaved || a.rd % (2 * vec) == 0);
+    if (tiles && ok(a.q, a.q_ts, a.q_hs) && ok(a.qo, a.qo_ts, a.qo_hs) &&
+        ok(a.k, a.k_ts, a.k_hs) && ok(a.ko, a.ko_ts, a.ko_hs) && ok(a.v, a.v_ts, a.v_hs))
       return vec;
   }
   return 1;
+}
+
+template <int VEC>
+int row_of(const RopeArgs& a) {
+  if (!a.interleaved) return kHalf;
+  return VEC == 1 || (a.rd == a.D && a.D % (2 * VEC) == 0) ? kInter : kMixed;
+}
+
+// Parts of a row.  In place (no tail to copy) those that turn come first and are all.
+template <int VEC>
+int parts_of(const RopeArgs& a) {
+  if (row_of<VEC>(a) == kMixed) {
+    const int half = (a.D / VEC + 1) / 2;
+    return a.copy_tail ? half : std::min(half, (a.rd + VEC - 1) / VEC);
+  }
+  return a.rd / (2 * VEC) + (a.copy_tail ? ((a.D - a.rd) / VEC + 1) / 2 : 0);
 }
 
 template <int IN, int KV, int VEC, bool MANY>
@@ -346,15 +422,16 @@ cudaError_t run(RopeArgs& a, int parts, cudaStream_t stream) {
   const dim3 grid((unsigned)(a.heads_first ? gx * gy : gx), a.heads_first ? 1 : (unsigned)gy,
                   (parts + kThreads - 1) / kThreads);
   const dim3 block(across, rows);
-  return launch_chained(a.interleaved ? rope_kernel<IN, KV, VEC, true, MANY>
-                                      : rope_kernel<IN, KV, VEC, false, MANY>,
-                        grid, block, 1, stream, a, parts);
+  void (*kernel)(RopeArgs, int) = rope_kernel<IN, KV, VEC, kHalf, MANY>;
+  if (row_of<VEC>(a) == kInter) kernel = rope_kernel<IN, KV, VEC, kInter, MANY>;
+  if constexpr (VEC > 1)
+    if (row_of<VEC>(a) == kMixed) kernel = rope_kernel<IN, KV, VEC, kMixed, MANY>;
+  return launch_chained(kernel, grid, block, 1, stream, a, parts);
 }
 
 template <int IN, int KV, int VEC>
 cudaError_t pick_shape(RopeArgs& a, int sms, cudaStream_t stream) {
-  // parts of a row: the turning ones, then the copied rest (not copied in place)
-  const int parts = a.rd / (2 * VEC) + (a.copy_tail ? ((a.D - a.rd) / VEC + 1) / 2 : 0);
+  const int parts = parts_of<VEC>(a);
   const int64_t heads = (int64_t)a.Hq + a.Hk * (a.pool ? 2 : 1);
   // one head a thread while that is one wave of blocks (beyond it, 33 instead of 27 us
   // on 8192 tokens of 32 + 8 bf16 heads of 128); already above eight blocks an SM four

@@ -169,6 +169,34 @@ def test_non_finite_values_stay_in_their_pairs(pkv):
 
 
 @pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T", [9, 4000])
+@pytest.mark.parametrize("rd", [2, 20, 36, 78])
+@pytest.mark.parametrize("dtype", DT, ids=str)
+def test_the_rest_of_a_head_is_copied_bit_for_bit(pkv, dtype, rd, T, interleaved):
+    """Any bits behind the rotated part (NaN payloads, infinities, -0), also where it ends
+    inside a vector; out of place, and untouched in place."""
+    bits = torch.int32 if dtype == torch.float32 else torch.int16
+    info = torch.iinfo(bits)
+    g = torch.Generator().manual_seed(rd)
+    raw = torch.randint(info.min, info.max, (T, 5, 80), generator=g).to(bits).cuda()
+    raw[..., :rd] = _x((T, 5, rd), dtype, 33).view(bits)
+    x = raw.view(dtype)
+    out = torch.zeros_like(x)
+    positions = _pos([i % 1000 for i in range(T)])
+    rope = pkv.Rope(rd, interleaved=interleaved)
+    pkv.rope_apply(out, x, positions, rope)
+    assert torch.equal(out.view(bits)[..., rd:], raw[..., rd:])
+    freqs, m = ref.frequencies(rd)
+    rows = slice(None, None, max(1, T // 9))
+    ref.check_rotated(out[rows, :, :rd], x[rows, :, :rd], positions[rows], freqs, m, rd,
+                      interleaved)
+    keep = raw.clone()
+    pkv.rope_apply(x, x, positions, rope)
+    assert torch.equal(raw[..., rd:], keep[..., rd:])
+    assert torch.equal(x[..., :rd], out[..., :rd])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("dtype", DT, ids=str)
 def test_gradient_against_the_formula(pkv, dtype, interleaved):
     freqs, m = ref.frequencies(48, scaling="yarn", factor=4.0, original=2048.0)

@@ -165,6 +165,16 @@ T* address(PyObject* o, const char* name) {
   return static_cast<T*>(p);
 }
 
+// A rotation from its table [rotary_dim / 2], rotary_dim, interleaved and attn_scale,
+// as they are at the call.
+pkv_rope rotation(Call& c, PyObject* const* a) {
+  const at::Tensor* freqs = c.tensor(a[0], "rope.freqs");
+  const int rotary = small(a[1], "rope.rotary_dim");
+  return {reinterpret_cast<const uint64_t*>(
+              c.flat<int64_t>(freqs, "rope.freqs", at::kLong, rotary / 2)),
+          rotary, small(a[2], "rope.interleaved"), number(a[3], "rope.attn_scale")};
+}
+
 // No C++ exception leaves a function of the module.
 template <typename F>
 PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
@@ -184,19 +194,19 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
   return nullptr;
 }
 
-// rope_apply(q_out, q, positions, freqs, rope address, k_out, k, backward, stream)
+// rope_apply(q_out, q, positions, freqs, rotary_dim, interleaved, attn_scale, k_out, k,
+//            backward, stream)
 PyObject* rope_apply_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 9, [&]() -> PyObject* {
-    if ((a[5] == Py_None) != (a[6] == Py_None))
+  return guarded(n, 11, [&]() -> PyObject* {
+    if ((a[7] == Py_None) != (a[8] == Py_None))
       throw Bad("rope_apply takes k and k_out together");
     Call c;
     const at::Tensor& q = *c.tensor(a[1], "q");
     const at::Tensor& qo = *c.tensor(a[0], "q_out");
     const at::Tensor* pos = c.tensor(a[2], "positions");
-    c.tensor(a[3], "rope");
-    const pkv_rope* rope = address<const pkv_rope>(a[4], "rope");
-    const at::Tensor* ko = c.tensor(a[5], "k_out", true);
-    const at::Tensor* k = c.tensor(a[6], "k", true);
+    const pkv_rope rope = rotation(c, a + 3);
+    const at::Tensor* ko = c.tensor(a[7], "k_out", true);
+    const at::Tensor* k = c.tensor(a[8], "k", true);
     const pkv_dtype dt = act_code(q.scalar_type());
     if (q.dim() != 3) throw Bad("q: [tokens, heads, head_dim] is needed, got " +
                                 shape_text(q.sizes()));
@@ -214,18 +224,18 @@ PyObject* rope_apply_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
       rko = c.rows(*ko, "k_out", T, Hk, D, q.scalar_type());
     }
     const int32_t* p = c.flat<int32_t>(pos, "positions", at::kInt, T);
-    const int backward = small(a[7], "backward");
-    return c.run(a[8], [&](cudaStream_t s) {
+    const int backward = small(a[9], "backward");
+    return c.run(a[10], [&](cudaStream_t s) {
       return rope_apply(&rqo, &rq, static_cast<int>(H), &rko, &rk, static_cast<int>(Hk), dt,
-                        static_cast<int>(D), p, T, rope, backward, s);
+                        static_cast<int>(D), p, T, &rope, backward, s);
     });
   });
 }
 
-// append_rope(pool handle, pool storage, layer, q_out, q, k, v, freqs, rope address,
-//             tables, positions, seq_ids, k_scale, v_scale, stream)
+// append_rope(pool handle, pool storage, layer, q_out, q, k, v, freqs, rotary_dim,
+//             interleaved, attn_scale, tables, positions, seq_ids, k_scale, v_scale, stream)
 PyObject* append_rope_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 15, [&]() -> PyObject* {
+  return guarded(n, 17, [&]() -> PyObject* {
     if ((a[3] == Py_None) != (a[4] == Py_None))
       throw Bad("append_rope takes q and q_out together");
     pkv_pool* pool = address<pkv_pool>(a[0], "pool");
@@ -236,11 +246,10 @@ PyObject* append_rope_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor* q = c.tensor(a[4], "q", true);
     const at::Tensor& k = *c.tensor(a[5], "k");
     const at::Tensor& v = *c.tensor(a[6], "v");
-    c.tensor(a[7], "rope");
-    const pkv_rope* rope = address<const pkv_rope>(a[8], "rope");
-    const at::Tensor* tables = c.tensor(a[9], "tables");
-    const at::Tensor* positions = c.tensor(a[10], "positions");
-    const at::Tensor* seq = c.tensor(a[11], "seq_ids", true);
+    const pkv_rope rope = rotation(c, a + 7);
+    const at::Tensor* tables = c.tensor(a[11], "tables");
+    const at::Tensor* positions = c.tensor(a[12], "positions");
+    const at::Tensor* seq = c.tensor(a[13], "seq_ids", true);
     pkv_geometry g;
     if (kv_pool_geometry(pool, &g) != PKV_OK) throw Bad("pool: not open");
     const at::ScalarType type = k.scalar_type();
@@ -261,10 +270,10 @@ PyObject* append_rope_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* tab = c.flat<int32_t>(tables, "tables", at::kInt, B, W);
     const int32_t* pos = c.flat<int32_t>(positions, "positions", at::kInt, T);
     const int32_t* ids = c.flat<int32_t>(seq, "seq_ids", at::kInt, T);
-    const float ks = number(a[12], "k_scale"), vs = number(a[13], "v_scale");
-    return c.run(a[14], [&](cudaStream_t s) {
+    const float ks = number(a[14], "k_scale"), vs = number(a[15], "v_scale");
+    return c.run(a[16], [&](cudaStream_t s) {
       return kv_append_rope(pool, layer, q ? &rqo : nullptr, q ? &rq : nullptr, &rk, &rv, dt,
-                            rope, tab, W, B, ids, pos, T, ks, vs, s);
+                            &rope, tab, W, B, ids, pos, T, ks, vs, s);
     });
   });
 }

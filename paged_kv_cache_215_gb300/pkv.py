@@ -224,7 +224,10 @@ class Rope:
     ``factor`` the ratio of the served to the trained length and, for "yarn",
     ``original_positions`` the trained length.  ``frequencies`` (radians per
     position, rotary_dim / 2 numbers) gives the table of any other scaling;
-    ``attn_scale`` replaces the factor on the rotated pairs."""
+    ``attn_scale`` replaces the factor on the rotated pairs.
+
+    A call goes by what the attributes rotary_dim, interleaved, attn_scale and freqs
+    (int64 [rotary_dim / 2] on the call's device, 2^-64 turns) hold when it is made."""
 
     def __init__(self, rotary_dim: int, base: float = 10000.0, interleaved: bool = False,
                  scaling: str = "none", factor: float = 1.0, original_positions: float = 0.0,
@@ -251,20 +254,6 @@ class Rope:
         self.rotary_dim, self.interleaved = rotary_dim, bool(interleaved)
         self.attn_scale = scale.value if attn_scale is None else float(attn_scale)
         self.freqs = torch.frombuffer(bytearray(table), dtype=torch.int64).to(device)
-        self._bind()
-
-    def _bind(self):
-        """The structure the calls take: it points at this object's own table."""
-        self._ref = RopeRef(self.freqs.data_ptr(), self.rotary_dim, int(self.interleaved),
-                            self.attn_scale)
-        self.address = ctypes.addressof(self._ref)
-
-    def __getstate__(self):
-        return {k: v for k, v in self.__dict__.items() if k not in ("_ref", "address")}
-
-    def __setstate__(self, state):
-        self.__dict__.update(state)
-        self._bind()
 
 
 def rope_apply(q_out, q, positions, rope: Rope, k_out=None, k=None, backward=False, stream=None):
@@ -272,8 +261,8 @@ def rope_apply(q_out, q, positions, rope: Rope, k_out=None, k=None, backward=Fal
     token t at positions[t] (int32; negative: padding, its rows are left alone).
     Any strides with a unit one along head_dim; q_out may be q.  backward: the
     gradients of q_out and k_out come in as q and k, those of q and k go out."""
-    rc = _tensors.rope_apply(q_out, q, positions, rope.freqs, rope.address, k_out, k, backward,
-                             stream)
+    rc = _tensors.rope_apply(q_out, q, positions, rope.freqs, rope.rotary_dim, rope.interleaved,
+                             rope.attn_scale, k_out, k, backward, stream)
     if rc:
         raise PkvError(rc, "rope_apply")
     return q_out if k is None else (q_out, k_out)
@@ -397,8 +386,9 @@ class KVPool:
         unit stride along head_dim (views of a joint projection are fine; q_out may
         be q); q_out = q = None stores keys and values only."""
         rc = _tensors.append_rope(self.handle.value if self.handle else 0, self.storage, layer,
-                                  q_out, q, k, v, rope.freqs, rope.address, tables, positions,
-                                  seq_ids, k_scale, v_scale, stream)
+                                  q_out, q, k, v, rope.freqs, rope.rotary_dim,
+                                  rope.interleaved, rope.attn_scale, tables, positions, seq_ids,
+                                  k_scale, v_scale, stream)
         if rc:
             raise PkvError(rc, "kv_append_rope")
         return q_out

@@ -1,0 +1,64 @@
+"""The rotation that the rotary and append calls are given."""
+import pytest
+import torch
+
+from tests import rotary_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pkv():
+    from paged_kv_cache_215_gb300 import pkv as mod
+    return mod
+
+
+def _x(*shape, dtype=torch.float32):
+    g = torch.Generator().manual_seed(sum(shape))
+    return torch.randn(shape, generator=g).to(dtype).cuda()
+
+
+def _ints(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+def _pool(pkv, blocks=4, heads=2, dim=64):
+    geom = pkv.geometry(1, heads, heads, dim, 16, blocks, "f32")
+    return pkv.KVPool(geom, storage=torch.zeros(pkv.kv_pool_bytes(geom), dtype=torch.uint8,
+                                                device="cuda"))
+
+
+def test_a_rotation_changed_after_it_was_made(pkv):
+    """Each call goes by what the rotation holds then."""
+    q, pos = _x(5, 3, 64), _ints([3, 9, 27, 81, 243])
+    rope, other = pkv.Rope(64), pkv.Rope(64, base=500.0)
+    out, pool, table = torch.empty_like(q), _pool(pkv, 5, 3), _ints([[0], [1], [2], [3], [4]])
+    kept = rope.freqs                       # stays alive
+    for change, base, m, inter in (
+            (lambda: setattr(rope, "attn_scale", 0.25), 10000.0, 0.25, False),
+            (lambda: setattr(rope, "interleaved", True), 10000.0, 0.25, True),
+            (lambda: setattr(rope, "freqs", other.freqs), 500.0, 0.25, True)):
+        change()
+        freqs, _ = ref.frequencies(64, base=base)
+        pkv.rope_apply(out, q, pos, rope)
+        ref.check_rotated(out, q, pos, freqs, m, 64, inter)
+        pool.append_rope(0, None, None, q, q, rope, table, pos % 16)
+        for t, p in enumerate((pos % 16).tolist()):
+            ref.check_rotated(pool.view()[t, 0, 0, :, p][None], q[t:t + 1],
+                              (pos % 16)[t:t + 1], freqs, m, 64, inter)
+    assert kept is not rope.freqs
+    with pytest.raises(AttributeError):
+        pkv.rope_apply(out, q, pos, None)
+
+
+def test_a_table_that_does_not_fit_is_refused(pkv):
+    q, pos = _x(2, 3, 64), _ints([3, 9])
+    out, pool, table = torch.empty_like(q), _pool(pkv, heads=3), _ints([[0], [1]])
+    good = pkv.Rope(64).freqs
+    for bad in (good[:31], good.float(), good.cpu(), good.view(2, 16), good.repeat(2)[::2], None):
+        rope = pkv.Rope(64)
+        rope.freqs = bad
+        with pytest.raises(ValueError, match="rope"):
+            pkv.rope_apply(out, q, pos, rope)
+        with pytest.raises(ValueError, match="rope"):
+            pool.append_rope(0, None, None, q, q, rope, table, pos)

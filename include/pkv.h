@@ -281,11 +281,12 @@ typedef struct {
  * position is padding: its output rows are left as they were.  backward = 1 turns
  * by the opposite angle (attn_scale stays a factor): the gradient with respect to
  * q and k of a loss whose gradients with respect to q_out and k_out are given as q
- * and k.  dtype f32, f16 or bf16; angles, products and sums are fp32 with one
- * rounding to dtype at the end.  head_dim <= 512, rotary_dim <= head_dim.
- * Asynchronous on `stream`; PKV_EINVAL for NULL or misaligned pointers (to the
- * element size), negative counts or strides, overlapping output rows, a bad
- * rotation, or more than 65535 heads.  rope_apply, kv_append_rope and verify_drafts
+ * and k.  dtype f32, f16 or bf16; angles, sines, products and sums are fp32 with one
+ * rounding to dtype at the end, in every dtype (ahead of it an output is off by at most
+ * 2^-21 of the two products that it is the sum of, beside what the angle is off).
+ * head_dim <= 512, rotary_dim <= head_dim.  Asynchronous on `stream`;
+ * PKV_EINVAL for NULL or misaligned pointers (to the element size), negative counts or
+ * strides, overlapping output rows, a bad rotation, or more than 65535 heads.  rope_apply, kv_append_rope and verify_drafts
  * are launched with programmatic dependent launch: a call is scheduled while the
  * launch before it finishes and waits for it (and all before) ahead of any access,
  * so it runs as any call in the stream does. */

@@ -4,8 +4,7 @@
 // Pair i of a row at position p turns by p * f_i:
 //   (a, b) -> m (a cos - b sin, a sin + b cos).
 // f_i is held in 2^-64 turns, so p * f_i modulo 2^64 (one 64-bit multiply) is the
-// angle reduced to one turn, exactly; its upper 32 bits are a signed fraction of a
-// turn.  Products and sums are fp32, rounded once to the output's type (for an E4M3
+// angle reduced to one turn, exactly.  Products and sums are fp32, rounded once to the output's type (for an E4M3
 // pool straight from fp32).
 //
 // Every element is read and written once with a few operations, so memory bounds the
@@ -127,19 +126,81 @@ struct Vec {
   }
 };
 
-// Sine and cosine of `turns` (2^-32 of a full turn, signed) times m.  fp32 rows take
-// sincospi (1 ulp).  16-bit rows, and E4M3 pools filled from them, take the
-// special-function unit on the reduced angle: with the angle's rounding off by 2^-20 at
-// most, 2^-9 of the half step (2^-11) that storing f16 costs anyway.
-template <int IN>
-__device__ __forceinline__ void sine(int32_t turns, float m, float& s, float& c) {
-  if constexpr (IN == PKV_F32) {
-    sincospif((float)turns * 0x1p-31f, &s, &c);
-  } else {
-    __sincosf((float)turns * 1.46291807926715968e-9f, &s, &c);   // 2 pi 2^-32
+// An angle in 2^-64 turns as its nearest quarter turn and the rest, -1/2 to 1/2 of a
+// quarter, in units of 2^-30 quarters (hi) and 2^-62 (lo).
+struct Angle {
+  uint32_t at;       // the angle plus an eighth of a turn: bits 30 and 31 count quarters
+  float hi, lo;
+  __device__ __forceinline__ static Angle of(uint64_t turns) {
+    const uint32_t at = (uint32_t)(turns >> 32) + 0x20000000u;
+    return {at, (float)((int32_t)(at & 0x3fffffffu) - 0x20000000), (float)(uint32_t)turns};
   }
-  s *= m;
-  c *= m;
+  // m times sine and cosine, from those of the rest
+  __device__ __forceinline__ void out(float sin_rest, float cos_rest, float m, float& s,
+                                      float& c) const {
+    const bool odd = at & 0x40000000u;
+    const uint32_t bits = __float_as_uint(m);
+    s = (odd ? cos_rest : sin_rest) * __uint_as_float(bits ^ (at & 0x80000000u));
+    c = (odd ? sin_rest : cos_rest) * __uint_as_float(bits ^ ((at ^ at << 1) & 0x80000000u));
+  }
+};
+
+// sin(t pi / 2) = t S(t^2) and cos(t pi / 2) = 1 + t^2 C(t^2) for |t| <= 1/2: S and C are
+// the cubics of least relative error (2^-28 and 2^-34, an exchange iteration on t^2),
+// rounded to fp32.  Evaluated in fp32, sines are within 2^-22.8 of themselves and
+// cosines within 2^-23.5, so that small results keep their digits in every type: the
+// special-function unit's sine is off by 2^-21 of 1, eight f16 steps of a result near
+// 1e-4.  (Its time: 8192 bf16 tokens of 32 + 8 heads 27.1 us instead of 27.5, 256 tokens
+// into an E4M3 pool 4.0 instead of 4.3; sincospi, as exact as this: 27.8 and 4.8.)
+constexpr float kS0 = 1.57079637f, kS1 = -0.64596343f, kS2 = 0.0796800181f,
+                kS3 = -0.00460162666f;
+constexpr float kC0 = -1.23370051f, kC1 = 0.253669232f, kC2 = -0.0208602883f,
+                kC3 = 0.00090402161f;
+
+// Sine and cosine of `turns` (2^-64 of a full turn) times m.
+__device__ __forceinline__ void sine(uint64_t turns, float m, float& s, float& c) {
+  const Angle a = Angle::of(turns);
+  const float t = fmaf(a.lo, 0x1p-62f, a.hi * 0x1p-30f), y = t * t;
+  a.out(t * fmaf(fmaf(fmaf(kS3, y, kS2), y, kS1), y, kS0),
+        fmaf(fmaf(fmaf(fmaf(kC3, y, kC2), y, kC1), y, kC0), y, 1.f), m, s, c);
+}
+
+// Two fp32 numbers in one register pair, and their operations (two in one instruction).
+struct Two {
+  uint64_t r;
+  __device__ __forceinline__ Two(float a, float b) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  }
+  __device__ __forceinline__ explicit Two(float a) : Two(a, a) {}
+  __device__ __forceinline__ void get(float& a, float& b) const {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+  }
+  __device__ __forceinline__ Two operator*(Two b) const {
+    Two x = b;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x.r) : "l"(r), "l"(b.r));
+    return x;
+  }
+  // *this b + c
+  __device__ __forceinline__ Two fma(Two b, Two c) const {
+    Two x = b;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x.r) : "l"(r), "l"(b.r), "l"(c.r));
+    return x;
+  }
+};
+
+// `sine` of two angles, with the same roundings.
+__device__ __forceinline__ void sine2(uint64_t turns0, uint64_t turns1, float m, float* s,
+                                      float* c) {
+  const Angle a = Angle::of(turns0), b = Angle::of(turns1);
+  const Two t = Two(a.lo, b.lo).fma(Two(0x1p-62f), Two(a.hi, b.hi) * Two(0x1p-30f));
+  const Two y = t * t;
+  const Two u = t * Two(kS3).fma(y, Two(kS2)).fma(y, Two(kS1)).fma(y, Two(kS0));
+  const Two v = Two(kC3).fma(y, Two(kC2)).fma(y, Two(kC1)).fma(y, Two(kC0)).fma(y, Two(1.f));
+  float u0, u1, v0, v1;
+  u.get(u0, u1);
+  v.get(v0, v1);
+  a.out(u0, v0, m, s[0], c[0]);
+  b.out(u1, v1, m, s[1], c[1]);
 }
 
 // One part of a row.
@@ -325,18 +386,25 @@ __global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
   if (pos < 0) return;                       // padding: no token
   float cs[VEC], sn[VEC];
   if (p.turn0) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
+    auto turns = [&](int j) {
       // the pair's index; interleaved: the pairs of one vector, then of the other (of a
       // mixed row's last pair again where the rotated part ends inside)
-      if (ROW == kMixed && j >= VEC / 2 && !p.turn1) break;
       int i = VEC * c + j;
       if (ROW != kHalf && VEC > 1) i = j < VEC / 2 ? p.e0 / 2 + j : p.e1 / 2 + j - VEC / 2;
       if (ROW == kMixed) i = min(i, a.rd / 2 - 1);
-      const uint64_t turns = (uint64_t)(uint32_t)pos * a.freqs[i];
-      sine<IN>((int32_t)(turns >> 32), a.m, sn[j], cs[j]);
-      sn[j] *= a.sign;
+      return (uint64_t)(uint32_t)pos * a.freqs[i];
+    };
+    // two at a time, except in mixed rows: there the registers that takes cost more
+    // (5005 f16 tokens of 16 + 2 x 2 heads of 96, half rotated: 8.3 instead of 7.6 us)
+    constexpr bool kTwo = VEC > 1 && ROW != kMixed;
+#pragma unroll
+    for (int j = 0; j < VEC; j += kTwo ? 2 : 1) {
+      if (ROW == kMixed && j >= VEC / 2 && !p.turn1) break;
+      if constexpr (kTwo) sine2(turns(j), turns(j + 1), a.m, sn + j, cs + j);
+      else sine(turns(j), a.m, sn[j], cs[j]);
     }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) sn[j] *= a.sign;
   }
   if (kind == 0 || a.pool == nullptr) {
     void* out = kind == 0 ? a.qo : a.ko;

@@ -10,6 +10,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -33,7 +34,8 @@ std::string shape_text(at::IntArrayRef v) {
   return s + ")";
 }
 
-// The tensors of one call: all on one CUDA device, none recording a gradient.
+// The tensors of one call: all on one CUDA device, none recording a gradient or
+// carrying a tangent (both would end here unnoticed).
 class Call {
  public:
   // The tensor behind `o`; nullptr for None where that is allowed.
@@ -49,7 +51,7 @@ class Call {
       throw Bad(std::string(name) + " on " + t.device().str() +
                 ": plain tensors on one CUDA device are needed");
     device_ = t.get_device();
-    if (grad_ && t.requires_grad())
+    if ((grad_ && t.requires_grad()) || (tangents_ && t._fw_grad(0).defined()))
       throw Bad(std::string(name) + ": this call records no gradient, detach its tensors "
                 "(rope_apply with backward is the gradient of rope_apply)");
     return &t;
@@ -119,6 +121,7 @@ class Call {
   }
   int64_t device_ = -1;
   const bool grad_ = c10::GradMode::is_enabled();
+  const bool tangents_ = c10::AutogradState::get_tls_state().get_fw_grad_mode();
 };
 
 pkv_dtype act_code(at::ScalarType t) {

@@ -1,6 +1,8 @@
-"""The rotation that the rotary and append calls are given."""
+"""What torch knows of the rotary, append and verification calls: the rotation that
+they are given and tensors that carry a tangent."""
 import pytest
 import torch
+import torch.autograd.forward_ad as fwd
 
 from tests import rotary_reference as ref
 
@@ -26,6 +28,15 @@ def _pool(pkv, blocks=4, heads=2, dim=64):
     geom = pkv.geometry(1, heads, heads, dim, 16, blocks, "f32")
     return pkv.KVPool(geom, storage=torch.zeros(pkv.kv_pool_bytes(geom), dtype=torch.uint8,
                                                 device="cuda"))
+
+
+def _verify_args(B=2, K=2, V=50):
+    p = torch.softmax(_x(B, K + 1, V), -1)
+    q = torch.softmax(_x(B, K, V), -1)
+    return [torch.empty(B, K + 1, dtype=torch.int32, device="cuda"),
+            torch.empty(B, dtype=torch.int32, device="cuda"), p, q,
+            torch.zeros(B, K, dtype=torch.int32, device="cuda"),
+            torch.full((B, K), 0.5, device="cuda"), torch.full((B,), 0.5, device="cuda")]
 
 
 def test_a_rotation_changed_after_it_was_made(pkv):
@@ -62,3 +73,22 @@ def test_a_table_that_does_not_fit_is_refused(pkv):
             pkv.rope_apply(out, q, pos, rope)
         with pytest.raises(ValueError, match="rope"):
             pool.append_rope(0, None, None, q, q, rope, table, pos)
+
+
+def test_tangents_are_refused(pkv):
+    """A forward-mode tangent would be lost, as a recorded gradient would."""
+    q, pos, rope = _x(2, 3, 64), _ints([3, 9]), pkv.Rope(64)
+    out, pool, table = torch.empty_like(q), _pool(pkv, heads=3), _ints([[0], [1]])
+    with fwd.dual_level():
+        dual = fwd.make_dual(q, torch.ones_like(q))
+        with pytest.raises(ValueError, match="gradient"):
+            pkv.rope_apply(out, dual, pos, rope)
+        with pytest.raises(ValueError, match="gradient"):
+            pool.append_rope(0, out, q, dual, q, rope, table, pos)
+        args = _verify_args()
+        args[2] = fwd.make_dual(args[2], torch.ones_like(args[2]))
+        with pytest.raises(ValueError, match="gradient"):
+            pkv.verify_drafts(*args)
+        primal, _ = fwd.unpack_dual(dual)
+        pkv.rope_apply(out, primal, pos, rope)
+    pkv.rope_apply(out, q, pos, rope)

@@ -57,6 +57,13 @@ class Call {
     return &t;
   }
 
+  // A tensor that the call writes.
+  const at::Tensor* output(PyObject* o, const char* name, bool optional = false) {
+    const at::Tensor* t = tensor(o, name, optional);
+    if (t) written_[num_written_++] = t;
+    return t;
+  }
+
   // Rows [tokens, heads, dim] with unit stride along dim.
   pkv_rows rows(const at::Tensor& t, const char* name, int64_t tokens, int64_t heads, int64_t dim,
                 at::ScalarType type) const {
@@ -88,7 +95,8 @@ class Call {
   }
 
   // Run `f(stream)` with the tensors' device current, on the given stream or the
-  // device's current one; the interpreter is free meanwhile.
+  // device's current one; the interpreter is free meanwhile.  The outputs' version
+  // counters go up, so that a graph which saved one raises instead of using it.
   template <typename F>
   PyObject* run(PyObject* stream, F f) const {
     cudaStream_t s;
@@ -101,6 +109,8 @@ class Call {
       Py_DECREF(p);
       if (!s && PyErr_Occurred()) return nullptr;
     }
+    for (int i = 0; i < num_written_; ++i)
+      if (!written_[i]->is_inference()) written_[i]->unsafeGetTensorImpl()->bump_version();
     const int before = c10::cuda::current_device();
     if (before != device_) c10::cuda::set_device(static_cast<c10::DeviceIndex>(device_));
     int rc;
@@ -120,6 +130,8 @@ class Call {
               shape_text(t.strides()));
   }
   int64_t device_ = -1;
+  const at::Tensor* written_[3];   // at most: verify_drafts has three outputs
+  int num_written_ = 0;
   const bool grad_ = c10::GradMode::is_enabled();
   const bool tangents_ = c10::AutogradState::get_tls_state().get_fw_grad_mode();
 };
@@ -205,10 +217,10 @@ PyObject* rope_apply_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
       throw Bad("rope_apply takes k and k_out together");
     Call c;
     const at::Tensor& q = *c.tensor(a[1], "q");
-    const at::Tensor& qo = *c.tensor(a[0], "q_out");
+    const at::Tensor& qo = *c.output(a[0], "q_out");
     const at::Tensor* pos = c.tensor(a[2], "positions");
     const pkv_rope rope = rotation(c, a + 3);
-    const at::Tensor* ko = c.tensor(a[7], "k_out", true);
+    const at::Tensor* ko = c.output(a[7], "k_out", true);
     const at::Tensor* k = c.tensor(a[8], "k", true);
     const pkv_dtype dt = act_code(q.scalar_type());
     if (q.dim() != 3) throw Bad("q: [tokens, heads, head_dim] is needed, got " +
@@ -243,9 +255,9 @@ PyObject* append_rope_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
       throw Bad("append_rope takes q and q_out together");
     pkv_pool* pool = address<pkv_pool>(a[0], "pool");
     Call c;
-    c.tensor(a[1], "pool");
+    c.output(a[1], "pool");
     const int layer = small(a[2], "layer");
-    const at::Tensor* qo = c.tensor(a[3], "q_out", true);
+    const at::Tensor* qo = c.output(a[3], "q_out", true);
     const at::Tensor* q = c.tensor(a[4], "q", true);
     const at::Tensor& k = *c.tensor(a[5], "k");
     const at::Tensor& v = *c.tensor(a[6], "v");
@@ -286,15 +298,15 @@ PyObject* append_rope_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* verify_drafts_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 10, [&]() -> PyObject* {
     Call c;
-    const at::Tensor* tokens = c.tensor(a[0], "tokens");
-    const at::Tensor* accepted = c.tensor(a[1], "num_accepted");
+    const at::Tensor* tokens = c.output(a[0], "tokens");
+    const at::Tensor* accepted = c.output(a[1], "num_accepted");
     const at::Tensor& target = *c.tensor(a[2], "target");
     const at::Tensor* draft = c.tensor(a[3], "draft", true);
     const at::Tensor* drafts = c.tensor(a[4], "drafts");
     const at::Tensor* ua = c.tensor(a[5], "u_accept");
     const at::Tensor* us = c.tensor(a[6], "u_sample");
     const at::Tensor* num = c.tensor(a[7], "num_drafts", true);
-    const at::Tensor* status = c.tensor(a[8], "status", true);
+    const at::Tensor* status = c.output(a[8], "status", true);
     const pkv_dtype dt = act_code(target.scalar_type());
     if (drafts->dim() != 2 || target.dim() != 3 || drafts->size(0) > INT32_MAX ||
         drafts->size(1) >= INT32_MAX || target.size(2) > INT32_MAX)

@@ -1,5 +1,5 @@
 """What torch knows of the rotary, append and verification calls: the rotation that
-they are given and tensors that carry a tangent."""
+they are given, tensors that carry a tangent, and outputs that a graph has saved."""
 import pytest
 import torch
 import torch.autograd.forward_ad as fwd
@@ -92,3 +92,47 @@ def test_tangents_are_refused(pkv):
         primal, _ = fwd.unpack_dual(dual)
         pkv.rope_apply(out, primal, pos, rope)
     pkv.rope_apply(out, q, pos, rope)
+
+
+def test_a_graph_notices_that_its_saved_tensor_was_overwritten(pkv):
+    q, pos, rope = _x(4, 2, 64), _ints([1, 2, 3, 4]), pkv.Rope(64)
+    pool, table = _pool(pkv), _ints([[0], [1], [2], [3]])
+    stored = pool.storage.view(torch.float32)
+    out, ko = torch.zeros_like(q), torch.zeros_like(q)
+
+    def apply():
+        pkv.rope_apply(out, q, pos, rope, k_out=ko, k=q)
+
+    def append():
+        pool.append_rope(0, out, q, q, q, rope, table, pos)
+
+    for call, saved in ((apply, out), (apply, ko), (append, out), (append, stored)):
+        w = torch.ones_like(saved, requires_grad=True)
+        loss = (w * saved).sum()
+        call()
+        with pytest.raises(RuntimeError, match="inplace"):
+            loss.backward()
+        loss = (w * saved).sum()                 # saved behind the call: still good
+        loss.backward()
+        assert torch.equal(w.grad, saved)
+    inputs = [t._version for t in (q, pos, rope.freqs, table)]
+    apply(), append()
+    assert inputs == [t._version for t in (q, pos, rope.freqs, table)]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = _verify_args()
+    before = [t._version for t in (*args, status)]
+    pkv.verify_drafts(*args, status=status)
+    after = [t._version for t in (*args, status)]
+    assert [b > a for a, b in zip(before, after)] == [True, True] + [False] * 5 + [True]
+
+
+def test_inference_mode(pkv):
+    """Tensors without a version counter, and ordinary ones."""
+    q, pos, rope = _x(4, 2, 64), _ints([1, 2, 3, 4]), pkv.Rope(64)
+    want, ordinary = torch.empty_like(q), torch.empty_like(q)
+    pkv.rope_apply(want, q, pos, rope)
+    with torch.inference_mode():
+        out = torch.empty_like(q)
+        pkv.rope_apply(out, q, pos, rope)
+        pkv.rope_apply(ordinary, q, pos, rope)
+        assert torch.equal(out, want) and torch.equal(ordinary, want)

@@ -4,7 +4,8 @@ Each .cu file is compiled by nvcc for sm_103a in parallel, the host C++ file by
 g++, and the objects are linked into one shared library against the CUDA
 runtime.  No CMake, no setuptools: one nvcc invocation per translation unit.
 The module that checks torch tensors for the short calls (csrc/binding) is built
-beside it against the installed torch, and again when that changes.
+beside it against the installed torch, and again when that changes.  Without a torch
+for CUDA and Python's headers it is left out: the C library needs neither.
 """
 from __future__ import annotations
 
@@ -50,15 +51,31 @@ def _stale(deps, target=SO) -> bool:
 
 
 def _torch():
-    """The installed torch's folder and version (without importing it)."""
+    """The installed torch's folder and version (without importing it), or None where
+    the binding cannot be built: no torch, one without CUDA, or no Python headers."""
     spec = importlib.util.find_spec("torch")
-    return os.path.dirname(spec.origin), importlib.metadata.version("torch")
+    if spec is None or not spec.origin:
+        return None
+    where = os.path.dirname(spec.origin)
+    for needed in (os.path.join(where, "lib", "libc10_cuda.so"),
+                   os.path.join(where, "include", "c10", "cuda", "CUDAStream.h"),
+                   os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(needed):
+            return None
+    try:
+        return where, importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:      # not installed as a package
+        return where, where
 
 
 def _binding_job():
-    """(command that compiles the binding, its object), or None if it is up to date."""
+    """(command that compiles the binding, its object), or None if it is up to date or
+    cannot be built."""
     src = os.path.join(CSRC, "binding", "pkv_tensors.cpp")
-    where, version = _torch()
+    torch = _torch()
+    if torch is None:
+        return None
+    where, version = torch
     stamp = BINDING + ".torch"
     built = open(stamp).read() if os.path.exists(stamp) else ""
     if built == version and not _stale([src, os.path.join(INCLUDE, "pkv.h")], BINDING):

@@ -132,14 +132,30 @@ def _load() -> ctypes.CDLL:
     return lib
 
 
+class _NoTensors:
+    """In the place of the compiled module where it cannot be loaded: its calls raise."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(self._why)
+
+
 def _load_tensors():
-    """The compiled module that checks and passes tensors of the short calls."""
+    """The compiled module that checks and passes tensors of the short calls (rope_apply,
+    append_rope, verify_drafts); without it they raise, and every other call works."""
     path = _build.BINDING
     if not os.path.exists(path):
-        raise ImportError(f"{path} is not built; run paged_kv_cache_215_gb300.build.build()")
+        return _NoTensors(f"{path} is not built (it needs a torch for CUDA and Python's headers); "
+                          "run paged_kv_cache_215_gb300.build.build()")
     spec = importlib.util.spec_from_file_location("pkv_tensors", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        return _NoTensors(f"{path} cannot be loaded, run paged_kv_cache_215_gb300.build.build(): "
+                          f"{e}")
     return module
 
 

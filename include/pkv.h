@@ -286,10 +286,10 @@ typedef struct {
  * 2^-21 of the two products that it is the sum of, beside what the angle is off).
  * head_dim <= 512, rotary_dim <= head_dim.  Asynchronous on `stream`;
  * PKV_EINVAL for NULL or misaligned pointers (to the element size), negative counts or
- * strides, overlapping output rows, a bad rotation, or more than 65535 heads.  rope_apply, kv_append_rope and verify_drafts
- * are launched with programmatic dependent launch: a call is scheduled while the
- * launch before it finishes and waits for it (and all before) ahead of any access,
- * so it runs as any call in the stream does. */
+ * strides, overlapping output rows, a bad rotation, or more than 65535 heads.
+ * rope_apply, kv_append_rope and verify_drafts are launched with programmatic dependent
+ * launch: a call is scheduled while the launch before it finishes and waits for it (and
+ * all before) ahead of any access, so it runs as any call in the stream does. */
 PKV_API int rope_apply(const pkv_rows* q_out, const pkv_rows* q, int num_q_heads,
                        const pkv_rows* k_out, const pkv_rows* k, int num_k_heads, pkv_dtype dtype,
                        int head_dim, const int32_t* d_positions, int64_t num_tokens,

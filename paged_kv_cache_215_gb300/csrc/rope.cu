@@ -218,8 +218,11 @@ enum Rowing { kHalf, kInter, kMixed };
 // little code, so that a decode step is one wave of short blocks.  Many: a thread
 // takes kManyHeads heads, all loaded before the first is used, and its sines serve
 // them all.  Blocks of 128 threads drain and refill the SMs evenly (256 threads at
-// the same occupancy: 29 instead of 27 us on 8192 tokens of 32 + 8 bf16 heads of 128);
-// the blocks per SM are the fastest of 4 to 10 for each type.
+// the same occupancy: 29 instead of 27 us on 8192 tokens of 32 + 8 bf16 heads of 128).
+// The blocks per SM are the fastest of 4 to 10 on that prompt and on 2048 tokens into an
+// E4M3 pool.  Nine of fp32 rows take 4099 tokens of 16 + 4 heads of 64 in one wave (7.3
+// us; 8.2 with seven), but their 56 registers spill 32 to 36 bytes a thread, and 1024 to
+// 4096 tokens of 32 + 8 heads of 128 are 2 to 10% faster with seven (26.3 against 27.3 us).
 constexpr int kThreads = 128, kFewBlocks = 10, kManyHeads = 4;
 __host__ __device__ constexpr int blocks_of(int in, int kv, bool many) {
   return !many ? kFewBlocks : kv == PKV_FP8_E4M3 ? 5 : in == PKV_F32 ? 9 : 6;
@@ -481,11 +484,15 @@ cudaError_t run(RopeArgs& a, int parts, cudaStream_t stream) {
   a.groups_k = (a.Hk + heads - 1) / heads;
   const int64_t gx = (a.T + rows - 1) / rows;
   const int64_t gy = (int64_t)a.groups_q + a.groups_k * (a.pool ? 2 : 1);
-  // blocks that run together: other tokens' same heads, or where one token's rows are
-  // long (10 KB), its other heads, which keeps DRAM pages open: 25.9 against 27.9 us for
-  // 8192 tokens of 12 KB, but 1 to 4% slower for 5 to 9 KB a token
+  // blocks that run together: other tokens' same heads, or, where the rows read and
+  // written exceed L2 (129 MB) and DRAM is what bounds the call, the same tokens' other
+  // heads, whose rows lie next to one another (rows of 84 MB, of 32 + 8 bf16 heads of
+  // 128: 27.5 against 28.4 us; of 250 MB, 1.3 to 20 KB a token: 0 to 4% faster).  Up to
+  // 50 MB of rows that is 1% faster to 7% slower, and into E4M3 pools, whose blocks
+  // spend their time on the codes, 2 to 9% slower at any size
   const int64_t row = ((int64_t)a.Hq + a.Hk * (a.pool ? 2 : 1)) * a.D * elem_size(a.in_dtype);
-  a.heads_first = MANY && row >= 10240 && gx * gy <= 0x7fffffff ? (int)gy : 0;
+  a.heads_first = MANY && KV != PKV_FP8_E4M3 && a.T * row >= (64 << 20) && gx * gy <= 0x7fffffff
+                      ? (int)gy : 0;
   if (gx > 0x7fffffff || gy > 65535) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)(a.heads_first ? gx * gy : gx), a.heads_first ? 1 : (unsigned)gy,
                   (parts + kThreads - 1) / kThreads);

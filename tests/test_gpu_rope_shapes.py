@@ -1,5 +1,5 @@
 """The shapes of the rotary kernel that long calls take (four heads a thread, token
-groups or head groups next to one another), alone and into a pool: every row equals
+groups or, above 64 MiB of rows, head groups next to one another), alone and into a pool: every row equals
 what a call of a few tokens gives, bit for bit, and a sample of them the 64-bit
 reference.  Sizes are stated for 152 SMs: a call takes four heads a thread above 152 x 8
 blocks of 128 threads (152 x 10 for an E4M3 pool) with one part of one head each."""
@@ -25,7 +25,8 @@ def _x(shape, dtype, seed):
 
 ROWS = [  # tokens, q heads, k heads, head_dim, rotary_dim
     (3001, 13, 3, 128, 128),      # token groups next to one another
-    (1501, 33, 9, 128, 128),      # 10752 or 21504 bytes a token: head groups
+    (1501, 33, 9, 128, 128),
+    (6401, 33, 9, 128, 128),      # more than 64 MiB of rows: head groups
     (4003, 13, 5, 80, 20),        # a part whose half is no vector; 60 elements behind it
     (2503, 30, 11, 144, 132),     # a part that ends inside a vector
     (3001, 14, 2, 96, 48),
@@ -64,8 +65,9 @@ def test_long_calls(pkv, shape, dtype, interleaved, backward):
 
 APPENDS = [  # (cached, new) per sequence, q heads, kv heads, head_dim, rotary_dim, block size
     dict(lens=[0, 777, 30], new=[1100, 501, 400], hq=15, hk=5, D=96, rd=96, bs=16),
-    dict(lens=[5, 0], new=[1203, 800], hq=36, hk=6, D=128, rd=128, bs=64),   # long rows
+    dict(lens=[5, 0], new=[1203, 800], hq=36, hk=6, D=128, rd=128, bs=64),
     dict(lens=[100], new=[2001], hq=21, hk=3, D=112, rd=36, bs=5),
+    dict(lens=[5, 0], new=[3203, 2600], hq=36, hk=6, D=128, rd=128, bs=64),   # head groups
 ]
 
 

@@ -10,9 +10,9 @@
 // Every element is read and written once with a few operations, so memory bounds the
 // long calls and the launch and one round of loads the short ones.  Measured (one
 // call after another): 16384 tokens of 64 + 2 x 8 heads of 128 in bf16 into the pool,
-// 671 MB, 97.5 us (6.9 TB/s, 1.01 of the copy rate); 8192 tokens of 32 + 8 heads, 168 MB,
-// 27.3 us (0.90); 4099 tokens of 16 + 4 fp32 heads of 64, 42 MB, 7.4 us (0.83); 256
-// tokens into an E4M3 pool, 10 MB, 4.1 us; one token, 2.1 us.
+// 671 MB, 97.2 us (6.9 TB/s, 1.02 of the copy rate); 8192 tokens of 32 + 8 heads, 168 MB,
+// 27.5 us (0.90); 4099 tokens of 16 + 4 fp32 heads of 64, 42 MB, 6.9 us (0.89); 256
+// tokens into an E4M3 pool, 10 MB, 4.3 us; one token, 2.1 us.
 //
 // A thread owns one part of a token's rows: two vectors of VEC elements, so that
 // neighbouring threads read neighbouring 16 bytes.  In the half layout they lie half
@@ -219,13 +219,14 @@ enum Rowing { kHalf, kInter, kMixed };
 // takes kManyHeads heads, all loaded before the first is used, and its sines serve
 // them all.  Blocks of 128 threads drain and refill the SMs evenly (256 threads at
 // the same occupancy: 29 instead of 27 us on 8192 tokens of 32 + 8 bf16 heads of 128).
-// The blocks per SM are the fastest of 4 to 10 on that prompt and on 2048 tokens into an
-// E4M3 pool.  Nine of fp32 rows take 4099 tokens of 16 + 4 heads of 64 in one wave (7.3
-// us; 8.2 with seven), but their 56 registers spill 32 to 36 bytes a thread, and 1024 to
-// 4096 tokens of 32 + 8 heads of 128 are 2 to 10% faster with seven (26.3 against 27.3 us).
+// The blocks per SM: 16-bit rows, six (that prompt 27.4 us, 27.3 with five and 31.4 with
+// seven; 16384 tokens into a pool 97.2, 101.7 and 113); fp32 rows, seven (both layouts,
+// rotated in part or whole, 1024 to 4099 tokens: 6.9 to 26.4 us, 1 to 11% slower with
+// eight, 3 to 17% with six; nine, the most that fit, spill registers); into E4M3 pools,
+// five (8192 tokens of 32 + 2 x 8 heads of 128 37.5 us, 45.1 with four, 41.0 with six).
 constexpr int kThreads = 128, kFewBlocks = 10, kManyHeads = 4;
 __host__ __device__ constexpr int blocks_of(int in, int kv, bool many) {
-  return !many ? kFewBlocks : kv == PKV_FP8_E4M3 ? 5 : in == PKV_F32 ? 9 : 6;
+  return !many ? kFewBlocks : kv == PKV_FP8_E4M3 ? 5 : in == PKV_F32 ? 7 : 6;
 }
 
 template <int IN, int VEC, int N>

@@ -51,7 +51,9 @@ class Call {
       throw Bad(std::string(name) + " on " + t.device().str() +
                 ": plain tensors on one CUDA device are needed");
     device_ = t.get_device();
-    if ((grad_ && t.requires_grad()) || (tangents_ && t._fw_grad(0).defined()))
+    // (tangents: of floating types only; asking costs 10 ns a tensor)
+    if ((grad_ && t.requires_grad()) ||
+        (tangents_ && at::isFloatingType(t.scalar_type()) && t._fw_grad(0).defined()))
       throw Bad(std::string(name) + ": this call records no gradient, detach its tensors "
                 "(rope_apply with backward is the gradient of rope_apply)");
     return &t;

@@ -15,12 +15,19 @@
 //
 // Turning a float into 64-bit fixed point with shifts, and summing that, took 75
 // instructions an element and bound the kernel (9700 of 25000 cycles for one row of
-// 131072); additions that truncate into the significand give the same integers in 12,
-// see Limbs.  What is left is a chain of latencies: the drafts and their probabilities
-// (0.9 us), the row (1.2 us of one row on 16 SMs), the cluster's barrier (0.8 us), the
-// search (0.8 us).  Measured (one call after another): one sequence, 4 drafts, 131072
-// tokens 4.9 us; 32 sequences, up to 5 drafts, 131071 tokens (rows not aligned) 8.5 us;
-// 128 sequences, 3 looked-up drafts, 32768 tokens 6.0 us.
+// 131072); additions that truncate into the significand give the same integers in 9, or
+// 16 with a draft's row (instructions counted on 100 rows of 65536 and 131072), see
+// Limbs.  What is left of a few sequences is a chain of latencies: the drafts and their
+// probabilities (0.9 us), the row (1.2 us of one row on 16 SMs), the cluster's barrier
+// (0.8 us), the search (0.8 us).  Measured (one call after another): one sequence, 4
+// drafts, 131072 tokens 4.9 us; 32 sequences, up to 5 drafts, 131071 tokens (rows not
+// aligned) 8.5 us; 128 sequences, 3 looked-up drafts, 32768 tokens 6.0 us.
+//
+// From 64 sequences of long rows on that chain no longer explains the time: 64 x 131072
+// fp32 with draft rows 12.2 us where the rows alone take 6.7 at the copy rate, 128 of
+// them 23.1 (13.4), 160 of them 32.5 (16.8).  A warp's loads of a step wait for the sums
+// of the one before, whole sequences go to SMs (160 sequences: eight SMs take two rows),
+// and 16-bit rows are read 8 bytes a lane (128 x 131072 in bf16 17.7 us, 6.7).
 #include <algorithm>
 #include <atomic>
 
@@ -486,7 +493,10 @@ int clusters_at_once(int k) {
 // rest's slices stay short (64 rows of 24576: 6.2 us with 2, 6.5 with 4; 100 rows of
 // 32768: 6.9 us with 1, 7.8 with 2; but 64 rows of 65536: 8.9 with 2, 8.1 with 4).  A
 // long row that one SM takes alone gets 1024 threads (100 rows of 116985: 21.7 us,
-// 24.3 with 2 CTAs of 512; for 32768 tokens 512 are 5 to 10% faster).
+// 24.3 with 2 CTAs of 512; for 32768 tokens 512 are 5 to 10% faster).  The limits lie
+// between the sizes that were measured (12288, 16384, 24576, 49152, 65536 and 116985
+// tokens, 1 to 256 sequences); where they cost most: 160 rows of 116985 38.3 us, 31.7
+// with 2 CTAs.
 template <int DT>
 cudaError_t pick(const VerifyArgs& a, int sms, cudaStream_t stream) {
   constexpr int kAlone = 40960;

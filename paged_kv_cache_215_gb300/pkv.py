@@ -238,7 +238,9 @@ class Rope:
 
     scaling: "none", "linear" (position interpolation), "ntk" or "yarn", with
     ``factor`` the ratio of the served to the trained length and, for "yarn",
-    ``original_positions`` the trained length.  ``frequencies`` (radians per
+    ``original_positions`` the trained length.  "yarn" ramps over the turns a pair makes
+    in the trained length, as the method was published; a checkpoint trained with the
+    ramp over the pair's index, or with another scaling, gets its own ``frequencies``.  ``frequencies`` (radians per
     position, rotary_dim / 2 numbers) gives the table of any other scaling;
     ``attn_scale`` replaces the factor on the rotated pairs.
 

@@ -4,15 +4,15 @@
 // Pair i of a row at position p turns by p * f_i:
 //   (a, b) -> m (a cos - b sin, a sin + b cos).
 // f_i is held in 2^-64 turns, so p * f_i modulo 2^64 (one 64-bit multiply) is the
-// angle reduced to one turn, exactly.  Products and sums are fp32, rounded once to the output's type (for an E4M3
-// pool straight from fp32).
+// angle reduced to one turn, exactly.  Products and sums are fp32, rounded once to the
+// output's type (for an E4M3 pool straight from fp32).
 //
 // Every element is read and written once with a few operations, so memory bounds the
 // long calls and the launch and one round of loads the short ones.  Measured (one
 // call after another): 16384 tokens of 64 + 2 x 8 heads of 128 in bf16 into the pool,
 // 671 MB, 97.2 us (6.9 TB/s, 1.02 of the copy rate); 8192 tokens of 32 + 8 heads, 168 MB,
-// 27.5 us (0.90); 4099 tokens of 16 + 4 fp32 heads of 64, 42 MB, 6.9 us (0.89); 256
-// tokens into an E4M3 pool, 10 MB, 4.3 us; one token, 2.1 us.
+// 27.4 us (0.90); 4099 tokens of 16 + 4 fp32 heads of 64, 42 MB, 6.9 us (0.89); 256
+// tokens into an E4M3 pool, 10 MB, 4.2 us; one token, 2.0 us.
 //
 // A thread owns one part of a token's rows: two vectors of VEC elements, so that
 // neighbouring threads read neighbouring 16 bytes.  In the half layout they lie half
@@ -135,13 +135,13 @@ struct Angle {
     const uint32_t at = (uint32_t)(turns >> 32) + 0x20000000u;
     return {at, (float)((int32_t)(at & 0x3fffffffu) - 0x20000000), (float)(uint32_t)turns};
   }
-  // m times sine and cosine, from those of the rest
-  __device__ __forceinline__ void out(float sin_rest, float cos_rest, float m, float& s,
-                                      float& c) const {
+  // ms times the sine and m times the cosine, from those of the rest
+  __device__ __forceinline__ void out(float sin_rest, float cos_rest, float m, float ms,
+                                      float& s, float& c) const {
     const bool odd = at & 0x40000000u;
-    const uint32_t bits = __float_as_uint(m);
-    s = (odd ? cos_rest : sin_rest) * __uint_as_float(bits ^ (at & 0x80000000u));
-    c = (odd ? sin_rest : cos_rest) * __uint_as_float(bits ^ ((at ^ at << 1) & 0x80000000u));
+    s = (odd ? cos_rest : sin_rest) * __uint_as_float(__float_as_uint(ms) ^ (at & 0x80000000u));
+    c = (odd ? sin_rest : cos_rest) *
+        __uint_as_float(__float_as_uint(m) ^ ((at ^ at << 1) & 0x80000000u));
   }
 };
 
@@ -150,19 +150,19 @@ struct Angle {
 // rounded to fp32.  Evaluated in fp32, sines are within 2^-22.8 of themselves and
 // cosines within 2^-23.5, so that small results keep their digits in every type: the
 // special-function unit's sine is off by 2^-21 of 1, eight f16 steps of a result near
-// 1e-4.  (Its time: 8192 bf16 tokens of 32 + 8 heads 27.1 us instead of 27.5, 256 tokens
-// into an E4M3 pool 4.0 instead of 4.3; sincospi, as exact as this: 27.8 and 4.8.)
+// 1e-4.  (Its time: 8192 bf16 tokens of 32 + 8 heads 27.1 us instead of 27.4, 256 tokens
+// into an E4M3 pool 4.0 instead of 4.2; sincospi, as exact as this: 27.8 and 4.8.)
 constexpr float kS0 = 1.57079637f, kS1 = -0.64596343f, kS2 = 0.0796800181f,
                 kS3 = -0.00460162666f;
 constexpr float kC0 = -1.23370051f, kC1 = 0.253669232f, kC2 = -0.0208602883f,
                 kC3 = 0.00090402161f;
 
-// Sine and cosine of `turns` (2^-64 of a full turn) times m.
-__device__ __forceinline__ void sine(uint64_t turns, float m, float& s, float& c) {
+// Sine of `turns` (2^-64 of a full turn) times ms and cosine times m.
+__device__ __forceinline__ void sine(uint64_t turns, float m, float ms, float& s, float& c) {
   const Angle a = Angle::of(turns);
   const float t = fmaf(a.lo, 0x1p-62f, a.hi * 0x1p-30f), y = t * t;
   a.out(t * fmaf(fmaf(fmaf(kS3, y, kS2), y, kS1), y, kS0),
-        fmaf(fmaf(fmaf(fmaf(kC3, y, kC2), y, kC1), y, kC0), y, 1.f), m, s, c);
+        fmaf(fmaf(fmaf(fmaf(kC3, y, kC2), y, kC1), y, kC0), y, 1.f), m, ms, s, c);
 }
 
 // Two fp32 numbers in one register pair, and their operations (two in one instruction).
@@ -189,8 +189,8 @@ struct Two {
 };
 
 // `sine` of two angles, with the same roundings.
-__device__ __forceinline__ void sine2(uint64_t turns0, uint64_t turns1, float m, float* s,
-                                      float* c) {
+__device__ __forceinline__ void sine2(uint64_t turns0, uint64_t turns1, float m, float ms,
+                                      float* s, float* c) {
   const Angle a = Angle::of(turns0), b = Angle::of(turns1);
   const Two t = Two(a.lo, b.lo).fma(Two(0x1p-62f), Two(a.hi, b.hi) * Two(0x1p-30f));
   const Two y = t * t;
@@ -199,8 +199,8 @@ __device__ __forceinline__ void sine2(uint64_t turns0, uint64_t turns1, float m,
   float u0, u1, v0, v1;
   u.get(u0, u1);
   v.get(v0, v1);
-  a.out(u0, v0, m, s[0], c[0]);
-  b.out(u1, v1, m, s[1], c[1]);
+  a.out(u0, v0, m, ms, s[0], c[0]);
+  b.out(u1, v1, m, ms, s[1], c[1]);
 }
 
 // One part of a row.
@@ -222,7 +222,7 @@ enum Rowing { kHalf, kInter, kMixed };
 // The blocks per SM: 16-bit rows, six (that prompt 27.4 us, 27.3 with five and 31.4 with
 // seven; 16384 tokens into a pool 97.2, 101.7 and 113); fp32 rows, seven (both layouts,
 // rotated in part or whole, 1024 to 4099 tokens: 6.9 to 26.4 us, 1 to 11% slower with
-// eight, 3 to 17% with six; nine, the most that fit, spill registers); into E4M3 pools,
+// eight, 3 to 17% with six; with nine registers spill); into E4M3 pools,
 // five (8192 tokens of 32 + 2 x 8 heads of 128 37.5 us, 45.1 with four, 41.0 with six).
 constexpr int kThreads = 128, kFewBlocks = 10, kManyHeads = 4;
 __host__ __device__ constexpr int blocks_of(int in, int kv, bool many) {
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
   Loaded<IN, VEC, N> x;
   x.load(in, i0, i_hs, h, h1, p);
   if (pos < 0) return;                       // padding: no token
-  float cs[VEC], sn[VEC];
+  float cs[VEC] = {}, sn[VEC] = {};
   if (p.turn0) {
     auto turns = [&](int j) {
       // the pair's index; interleaved: the pairs of one vector, then of the other (of a
@@ -398,17 +398,16 @@ __global__ void __launch_bounds__(kThreads, blocks_of(IN, KV, MANY))
       if (ROW == kMixed) i = min(i, a.rd / 2 - 1);
       return (uint64_t)(uint32_t)pos * a.freqs[i];
     };
+    const float ms = a.m * a.sign;
     // two at a time, except in mixed rows: there the registers that takes cost more
-    // (5005 f16 tokens of 16 + 2 x 2 heads of 96, half rotated: 8.3 instead of 7.6 us)
+    // (5005 f16 tokens of 16 + 2 x 2 heads of 96, half rotated: 8.3 instead of 7.4 us)
     constexpr bool kTwo = VEC > 1 && ROW != kMixed;
 #pragma unroll
     for (int j = 0; j < VEC; j += kTwo ? 2 : 1) {
       if (ROW == kMixed && j >= VEC / 2 && !p.turn1) break;
-      if constexpr (kTwo) sine2(turns(j), turns(j + 1), a.m, sn + j, cs + j);
-      else sine(turns(j), a.m, sn[j], cs[j]);
+      if constexpr (kTwo) sine2(turns(j), turns(j + 1), a.m, ms, sn + j, cs + j);
+      else sine(turns(j), a.m, ms, sn[j], cs[j]);
     }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) sn[j] *= a.sign;
   }
   if (kind == 0 || a.pool == nullptr) {
     void* out = kind == 0 ? a.qo : a.ko;
@@ -488,9 +487,10 @@ cudaError_t run(RopeArgs& a, int parts, cudaStream_t stream) {
   // blocks that run together: other tokens' same heads, or, where the rows read and
   // written exceed L2 (129 MB) and DRAM is what bounds the call, the same tokens' other
   // heads, whose rows lie next to one another (rows of 84 MB, of 32 + 8 bf16 heads of
-  // 128: 27.5 against 28.4 us; of 250 MB, 1.3 to 20 KB a token: 0 to 4% faster).  Up to
-  // 50 MB of rows that is 1% faster to 7% slower, and into E4M3 pools, whose blocks
-  // spend their time on the codes, 2 to 9% slower at any size
+  // 128: 27.5 against 28.4 us; of 250 MB, 1.3 to 20 KB a token: 0 to 4% faster).  With
+  // less it is slower more often than not (rows of 50 MB: 4% faster to 3% slower, of 25
+  // MB: 7% faster to 8% slower, of 10 MB: 3% faster to 19% slower), as into E4M3 pools,
+  // whose blocks spend their time on the codes (10 to 250 MB: 1% faster to 9% slower)
   const int64_t row = ((int64_t)a.Hq + a.Hk * (a.pool ? 2 : 1)) * a.D * elem_size(a.in_dtype);
   a.heads_first = MANY && KV != PKV_FP8_E4M3 && a.T * row >= (64 << 20) && gx * gy <= 0x7fffffff
                       ? (int)gy : 0;

@@ -520,6 +520,63 @@ PKV_API size_t paged_decode_workspace_bytes_cascade(const pkv_geometry* geom, in
                                                     int max_blocks_per_seq, int max_seq_len,
                                                     int prefix_len_max);
 
+/* ---------------------------------------------------------------- scored attention */
+
+/* Which keys a query token sees and what becomes of its scores, beyond the causal
+ * softmax of paged_decode_attention_mq.  Query token i of a sequence of n tokens sits
+ * at p = n - q_len + i and sees key j if
+ *   (j <= p, or j < d_prefix_lens[s]: a prefix that sees itself both ways)
+ *   and p - j < window (a sliding window of `window` keys, the query's own included)
+ *   and j >= d_doc_starts[s][i] (the first token of the query's document in a packed
+ *   sequence).
+ * A score x = scale * <q, K_j> becomes cap * tanh(x / cap), then loses
+ * slope_h * |p - j|. */
+typedef struct {
+  float cap;                    /* > 0; 0: scores are not capped */
+  int32_t window;               /* > 0; 0: none */
+  const float* d_slopes;        /* [num_q_heads] or NULL */
+  const int32_t* d_prefix_lens; /* [batch] or NULL (<= 0: none; limited to n) */
+  const int32_t* d_doc_starts;  /* [batch, q_len] or NULL (<= 0: the sequence's start) */
+} pkv_scores;
+/* Accumulated attention weights: fp32 [batch, num_kv_heads, >= max_seq_len], unit
+ * stride along the tokens, other strides in elements (>= 0). */
+typedef struct {
+  float* data;
+  int64_t seq_stride, head_stride;
+} pkv_weights;
+
+/* paged_decode_attention_mq with the rules of `scores` (NULL: none), q_len >= 1, and
+ * the record of where the attention went.  A query that sees no key (or sits before
+ * the sequence's start) gets out = 0.  Only blocks that hold a key some query of the
+ * call sees are read (their table entries too, so entries ahead of a window may be
+ * stale); keys that no query sees may hold anything, NaN included, while a value that
+ * only some queries of a sequence see must be finite for the others' sake.
+ * weights (NULL: none): for every sequence s, KV head h and token j < n
+ *   weights[s, h, j] = weights_in[s, h, j] + the softmax weights of j, summed over the
+ *                      q_len queries and num_q_heads / num_kv_heads query heads of h
+ * in one fixed order (the same bits in every run); columns from n on are left as they
+ * were.  weights_in NULL: 0 in its place; weights_in may be weights (same data and
+ * strides), another overlap gives undefined values; rows of weights must not overlap.
+ * A length above max_seq_len (or below 0) is limited to it and records PKV_EBOUNDS.
+ * d_workspace: paged_decode_scored_workspace_bytes bytes, 16-byte aligned; with weights
+ * it holds every score of the call (4 bytes for each query row and token).
+ * Kernels, types and shapes as in paged_decode_attention_mq with num_splits = 0;
+ * weights take up to 16 query rows per KV head (8 at block size 64), else
+ * PKV_EUNSUPPORTED.  PKV_EINVAL also for a cap or window below 0, a cap that is not
+ * finite, and scale / cap not finite in fp32. */
+PKV_API int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* d_q,
+                                          pkv_dtype q_dtype, int q_len, const pkv_pool* pool,
+                                          int layer, const int32_t* d_block_tables,
+                                          int max_blocks_per_seq, const int32_t* d_seq_lens,
+                                          int batch, int max_seq_len, float scale, float k_scale,
+                                          float v_scale, const pkv_scores* scores,
+                                          const pkv_weights* weights,
+                                          const pkv_weights* weights_in, void* d_workspace,
+                                          size_t ws_bytes, cudaStream_t stream);
+/* Workspace bytes of paged_decode_attention_scored on the current device. */
+PKV_API size_t paged_decode_scored_workspace_bytes(const pkv_geometry* geom, int batch, int q_len,
+                                                   int max_seq_len, int with_weights);
+
 /* Log-sum-exp merge of partial results ([SEQPAR] incremental softmax,
  * [ENG26] 3.1): for each row r = (s, h) of batch x num_q_heads,
  *   M = max_p lse[r,p],  w_p = exp(lse[r,p] - M),

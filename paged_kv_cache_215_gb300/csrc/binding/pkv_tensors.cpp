@@ -1,5 +1,5 @@
-// pkv_tensors.cpp -- torch tensors checked and handed to the rotary, append and
-// verification calls of include/pkv.h, as a CPython module.
+// pkv_tensors.cpp -- torch tensors checked and handed to the rotary, append,
+// verification and scored attention calls of include/pkv.h, as a CPython module.
 //
 // These calls run a few microseconds on the device, so the host's share is what a
 // decode step waits for.  Reading a tensor's device, type, sizes, strides and
@@ -83,6 +83,15 @@ class Call {
     return {t.data_ptr(), t.stride(0), t.stride(1)};
   }
 
+  // Weights [batch, heads, >= tokens] with unit stride along the tokens.
+  pkv_weights weights(const at::Tensor& t, const char* name, int64_t batch, int64_t heads,
+                      int64_t tokens) const {
+    if (t.dim() != 3 || t.size(0) != batch || t.size(1) != heads || t.size(2) < tokens ||
+        t.scalar_type() != at::kFloat || (t.numel() > 0 && t.size(2) > 1 && t.stride(2) != 1))
+      fail(t, name, shape_text({batch, heads, tokens}) + " or longer rows", at::kFloat);
+    return {static_cast<float*>(t.data_ptr()), t.stride(0), t.stride(1)};
+  }
+
   // Contiguous values of `type`, [a] or (b >= 0) [a, b].
   template <typename T>
   T* flat(const at::Tensor* t, const char* name, at::ScalarType type, int64_t a,
@@ -132,7 +141,7 @@ class Call {
               shape_text(t.strides()));
   }
   int64_t device_ = -1;
-  const at::Tensor* written_[3];   // at most: verify_drafts has three outputs
+  const at::Tensor* written_[4];   // at most: evict has four outputs
   int num_written_ = 0;
   const bool grad_ = c10::GradMode::is_enabled();
   const bool tangents_ = c10::AutogradState::get_tls_state().get_fw_grad_mode();
@@ -334,12 +343,76 @@ PyObject* verify_drafts_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// attend_scored(out, q, pool handle, pool storage, layer, tables, seq_lens, max_seq_len, scale,
+//               cap, window, slopes, prefix_lens, doc_starts, k_scale, v_scale, weights,
+//               weights_in, workspace, stream)
+PyObject* attend_scored_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 20, [&]() -> PyObject* {
+    Call c;
+    const at::Tensor& out = *c.output(a[0], "out");
+    const at::Tensor& q = *c.tensor(a[1], "q");
+    pkv_pool* pool = address<pkv_pool>(a[2], "pool");
+    c.tensor(a[3], "pool");
+    const int layer = small(a[4], "layer");
+    const at::Tensor* tables = c.tensor(a[5], "tables");
+    const at::Tensor* lens = c.tensor(a[6], "seq_lens");
+    const int most = small(a[7], "max_seq_len");
+    const float scale = number(a[8], "scale");
+    pkv_scores sc{};
+    sc.cap = number(a[9], "scores.cap");
+    sc.window = small(a[10], "scores.window");
+    const at::Tensor* slopes = c.tensor(a[11], "scores.slopes", true);
+    const at::Tensor* prefix = c.tensor(a[12], "scores.prefix_lens", true);
+    const at::Tensor* docs = c.tensor(a[13], "scores.doc_starts", true);
+    const float ks = number(a[14], "k_scale"), vs = number(a[15], "v_scale");
+    const at::Tensor* weights = c.output(a[16], "weights", true);
+    const at::Tensor* before = c.tensor(a[17], "weights_in", true);
+    const at::Tensor* ws = c.output(a[18], "workspace");
+    pkv_geometry g;
+    if (kv_pool_geometry(pool, &g) != PKV_OK) throw Bad("pool: not open");
+    const bool steps = q.dim() == 4;
+    const int64_t B = q.dim() >= 3 ? q.size(0) : 0, Q = steps ? q.size(1) : 1;
+    if ((q.dim() != 3 && !steps) || B > INT32_MAX || Q > INT32_MAX ||
+        q.size(steps + 1) != g.num_q_heads || q.size(steps + 2) != g.head_dim || !q.is_contiguous())
+      throw Bad("q: contiguous [batch, " + std::to_string(g.num_q_heads) + ", " +
+                std::to_string(g.head_dim) + "] or [batch, q_len, ...] is needed, got " +
+                shape_text(q.sizes()));
+    if (out.sizes() != q.sizes() || !out.is_contiguous())
+      throw Bad("out: contiguous " + shape_text(q.sizes()) + " is needed, got " +
+                shape_text(out.sizes()));
+    if (tables->dim() != 2 || tables->size(1) > INT32_MAX)
+      throw Bad("tables: [batch, max_blocks] is needed, got " + shape_text(tables->sizes()));
+    const int W = static_cast<int>(tables->size(1));
+    const int32_t* tab = c.flat<int32_t>(tables, "tables", at::kInt, B, W);
+    const int32_t* len = c.flat<int32_t>(lens, "seq_lens", at::kInt, B);
+    sc.d_slopes = c.flat<float>(slopes, "scores.slopes", at::kFloat, g.num_q_heads);
+    sc.d_prefix_lens = c.flat<int32_t>(prefix, "scores.prefix_lens", at::kInt, B);
+    // one query token: [batch] will do
+    sc.d_doc_starts = docs && docs->dim() == 1 && Q == 1
+                          ? c.flat<int32_t>(docs, "scores.doc_starts", at::kInt, B)
+                          : c.flat<int32_t>(docs, "scores.doc_starts", at::kInt, B, Q);
+    pkv_weights w{}, w0{};
+    if (weights) w = c.weights(*weights, "weights", B, g.num_kv_heads, most);
+    if (before) w0 = c.weights(*before, "weights_in", B, g.num_kv_heads, most);
+    if (ws->scalar_type() != at::kByte || !ws->is_contiguous())
+      throw Bad("workspace: contiguous uint8 is needed");
+    const pkv_dtype qt = act_code(q.scalar_type()), ot = act_code(out.scalar_type());
+    return c.run(a[19], [&](cudaStream_t s) {
+      return paged_decode_attention_scored(
+          out.data_ptr(), ot, q.data_ptr(), qt, static_cast<int>(Q), pool, layer, tab, W, len,
+          static_cast<int>(B), most, scale, ks, vs, &sc, weights ? &w : nullptr,
+          before ? &w0 : nullptr, ws->data_ptr(), static_cast<size_t>(ws->numel()), s);
+    });
+  });
+}
+
 #define PKV_METHOD(name, f) \
   {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     PKV_METHOD("rope_apply", rope_apply_py),
     PKV_METHOD("append_rope", append_rope_py),
     PKV_METHOD("verify_drafts", verify_drafts_py),
+    PKV_METHOD("attend_scored", attend_scored_py),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "pkv_tensors", nullptr, -1, methods,

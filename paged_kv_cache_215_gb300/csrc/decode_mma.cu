@@ -8,6 +8,9 @@ namespace pkv {
 cudaError_t launch_decode_mma_bf16(const CUtensorMap*, const DecodeArgs&, int, int, cudaStream_t);
 cudaError_t launch_decode_mma_f16(const CUtensorMap*, const DecodeArgs&, int, int, cudaStream_t);
 cudaError_t launch_decode_mma_fp8(const CUtensorMap*, const DecodeArgs&, int, int, cudaStream_t);
+cudaError_t launch_decode_score_bf16(const CUtensorMap*, const DecodeArgs&, int, cudaStream_t);
+cudaError_t launch_decode_score_f16(const CUtensorMap*, const DecodeArgs&, int, cudaStream_t);
+cudaError_t launch_decode_score_fp8(const CUtensorMap*, const DecodeArgs&, int, cudaStream_t);
 
 using mma::kD;
 using mma::kLineBytes;
@@ -38,6 +41,18 @@ cudaError_t launch_decode_mma(const CUtensorMap* map, const DecodeArgs& a, int g
     case PKV_BF16: return launch_decode_mma_bf16(map, a, gx, gy, stream);
     case PKV_F16: return launch_decode_mma_f16(map, a, gx, gy, stream);
     case PKV_FP8_E4M3: return launch_decode_mma_fp8(map, a, gx, gy, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_decode_mma_scored(const CUtensorMap* map, const DecodeArgs& a, int gx,
+                                     cudaStream_t stream) {
+  if (a.stages < 2 || a.stages > 16 || a.HG < 1 || a.HG > kMaxHG) return cudaErrorInvalidValue;
+  if (a.R < 1 || a.R > 16 || (a.R > 8 && a.BS == 64)) return cudaErrorInvalidValue;
+  switch (a.kv_dtype) {
+    case PKV_BF16: return launch_decode_score_bf16(map, a, gx, stream);
+    case PKV_F16: return launch_decode_score_f16(map, a, gx, stream);
+    case PKV_FP8_E4M3: return launch_decode_score_fp8(map, a, gx, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -39,9 +39,14 @@
 
 #include "device.cuh"
 #include "launch.h"
+#include "score.cuh"
 
 namespace pkv {
 namespace mma {
+
+// What an instance reads of a sequence: all of it; from the end of its shared prefix
+// on (a.len_off set); or what its queries see under the rules of score.cuh.
+enum Mode { kPlain = 0, kSuffix = 1, kScored = 2 };
 
 constexpr int kD = 128;            // head_dim of this kernel
 constexpr int kMaxHG = 8;          // consumer warps per CTA
@@ -65,7 +70,7 @@ struct KvTraits<PKV_FP8_E4M3> {
   static constexpr int kRegions = 1;   // 128 one-byte columns fill one line
 };
 
-// First token of sequence s that a shared-prefix launch (kOff, a.len_off set)
+// First token of sequence s that a shared-prefix launch (kSuffix, a.len_off set)
 // reads: the end of the sequence's shared prefix, whole blocks; a prefix the
 // check before the launch reported bad reads the sequence from token 0.
 __device__ __forceinline__ int first_token(const DecodeArgs& a, int s, int n) {
@@ -81,22 +86,26 @@ struct Cursor {
   long long remaining;     // blocks left in this CTA's run
 };
 
-template <bool kOff>
+template <int kMode>
 __device__ __forceinline__ int clamp_len(const DecodeArgs& a, int s) {
+  if constexpr (kMode == kScored) {
+    const int n = scored_len(a, s);
+    return n - first_read(a, s, n);
+  }
   int n = __ldg(a.seq_lens + s);
   int cap = a.max_blocks * a.BS;
   if (n < 0 || n > cap) {
     record_error(a.status, PKV_EBOUNDS);
     n = n < 0 ? 0 : cap;
   }
-  if constexpr (kOff) n -= first_token(a, s, n);
+  if constexpr (kMode == kSuffix) n -= first_token(a, s, n);
   return n;
 }
 
 __device__ __forceinline__ int blocks_of(int n, int BS) { return (n + BS - 1) / BS; }
 
 // Move to the next block; crosses into the next non-empty unit when needed.
-template <bool kOff>
+template <int kMode>
 __device__ __forceinline__ void cursor_next(Cursor& c, const DecodeArgs& a) {
   ++c.j;
   ++c.gb;
@@ -108,7 +117,7 @@ __device__ __forceinline__ void cursor_next(Cursor& c, const DecodeArgs& a) {
       c.hg = 0;
       do {
         ++c.s;
-        c.n = clamp_len<kOff>(a, c.s);
+        c.n = clamp_len<kMode>(a, c.s);
         c.nb = blocks_of(c.n, a.BS);
       } while (c.nb == 0);
     }
@@ -138,7 +147,7 @@ struct SmemHeader {
 // sees keys 0 .. that position (causal within the chunk; q_len = 1 is plain
 // decode).
 
-template <int KVT, int BS, int NT, bool kCausal>
+template <int KVT, int BS, int NT, bool kCausal, bool kScore = false>
 struct Consumer {
   using T = KvTraits<KVT>;
   static constexpr int kTiles = BS / 16;
@@ -153,6 +162,14 @@ struct Consumer {
   float acc[8][NT][4];     // O^T fragments: 8 tiles of 16 d x 8 rows, per n-tile
   float m[NT][2], l[NT][2];// running max (log2 units) and per-thread partial sums
   int lim[NT][2];          // last key position each of the thread's columns may see
+  // scored calls (positions count from the first token read): the first key of each
+  // column, its query's position and slope (log2 units), and over all columns the
+  // smallest and largest first and last keys
+  int from[kScore ? NT : 1][2], at[kScore ? NT : 1][2];
+  float slope[kScore ? NT : 1][2];
+  int from_min, from_max, lim_min, lim_max;
+  float cap_in_;
+  float* score_rows;       // the unit's rows in a.scores, or nullptr
   // E4M3 with block-wise scales: acc is held in units of 2^ev_ref_, the largest
   // power-of-two exponent of the V block scales seen in the current piece, and
   // each block's P carries its scale's remaining factor (at most 2), so that
@@ -222,7 +239,9 @@ struct Consumer {
       const int e = f16_fit_exponent(warp_max(amax));
       qscale = pow2i(e);
       qk_scale_log2_ = a.qk_scale_log2 * pow2i(-e);
+      if constexpr (kScore) cap_in_ = a.cap_in * pow2i(-e);
     }
+    if constexpr (kScore) load_rules(a, s, n, hkv, lane);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const long long qr = q_row(a, s, hkv, nt * 8 + (lane >> 2));
@@ -249,8 +268,99 @@ struct Consumer {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = nt * 8 + 2 * c + h;           // the thread's accumulator columns
-        if constexpr (kCausal) lim[nt][h] = r < a.R ? n - a.q_len + r / a.G : n - 1;
+        if constexpr (kCausal && !kScore) lim[nt][h] = r < a.R ? n - a.q_len + r / a.G : n - 1;
       }
+    }
+  }
+
+  // The columns' keys, positions and slopes in a unit that reads n tokens.
+  __device__ __forceinline__ void load_rules(const DecodeArgs& a, int s, int n, int hkv, int lane) {
+    const int c = lane & 3, len = scored_len(a, s), off = len - n;
+    from_min = lim_min = 0x7fffffff;
+    from_max = lim_max = -1;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = nt * 8 + 2 * c + h;
+        from[nt][h] = 0x7fffffff;              // a padding column sees no key
+        lim[nt][h] = -1;
+        at[nt][h] = 0;
+        slope[nt][h] = 0.f;
+        if (r >= a.R) continue;
+        const int i = r / a.G, g = r - i * a.G;
+        const KeyRange k = key_range(a, s, len, i);
+        if (k.lo < k.hi) {
+          from[nt][h] = k.lo - off;
+          lim[nt][h] = k.hi - 1 - off;
+        }
+        at[nt][h] = len - a.q_len + i - off;
+        if (a.slopes) slope[nt][h] = __ldg(a.slopes + hkv * a.G + g) * kLog2e;
+        from_min = min(from_min, from[nt][h]);
+        from_max = max(from_max, from[nt][h]);
+        lim_min = min(lim_min, lim[nt][h]);
+        lim_max = max(lim_max, lim[nt][h]);
+      }
+    from_min = __reduce_min_sync(0xffffffffu, from_min);
+    from_max = __reduce_max_sync(0xffffffffu, from_max);
+    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+    lim_max = __reduce_max_sync(0xffffffffu, lim_max);
+    score_rows = a.scores ? a.scores + (((int64_t)s * a.Hkv + hkv) * a.max_len + off) * a.score_row
+                          : nullptr;
+  }
+
+  // Scores of a block into log2 units: cap, distance, mask, record (score.cuh).
+  __device__ __forceinline__ void apply_rules(const DecodeArgs& a, float (&s)[kTiles][NT][4],
+                                              float ks_b, int jbase, int valid, bool full,
+                                              int lane) {
+    const int t0 = jbase + (lane >> 2);
+    const float qs = qk_scale_log2_ * ks_b, ci = cap_in_ * ks_b;
+#pragma unroll
+    for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float& x = s[mt][nt][k];
+          x = a.cap_in != 0.f ? a.cap_out * tanh_score(x * ci) : x * qs;
+        }
+    if (a.slopes) {
+#pragma unroll
+      for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int t = t0 + mt * 16 + ((k >> 1) << 3);
+            s[mt][nt][k] = fmaf(-slope[nt][k & 1], (float)abs(at[nt][k & 1] - t), s[mt][nt][k]);
+          }
+    }
+    if (!full) {
+#pragma unroll
+      for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int t = t0 + mt * 16 + ((k >> 1) << 3);
+            if (t < from[nt][k & 1] || t > lim[nt][k & 1]) s[mt][nt][k] = -INFINITY;
+          }
+    }
+    if (score_rows) {
+      const int c = lane & 3;
+#pragma unroll
+      for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          const int t = mt * 16 + (lane >> 2) + ((k >> 1) << 3);
+          if (t >= valid) continue;
+          float* row = score_rows + (int64_t)(jbase + t) * a.score_row;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            if (nt * 8 + 2 * c < a.score_row)
+              *reinterpret_cast<float2*>(row + nt * 8 + 2 * c) =
+                  make_float2(s[mt][nt][k], s[mt][nt][k + 1]);
+        }
     }
   }
 
@@ -513,9 +623,9 @@ struct Consumer {
   // the first region of K / V in the stage; `row0` is the warp's first row;
   // `jbase` the block's first token position; `valid` its tokens inside the
   // sequence; `full`: no key of the block is hidden from any query row.
-  __device__ __forceinline__ void block(uint32_t kbase, uint32_t vbase, uint32_t region_bytes,
-                                        int row0, int jbase, int valid, bool full, int lane,
-                                        float ks_b, float vs_b) {
+  __device__ __forceinline__ void block(const DecodeArgs& a, uint32_t kbase, uint32_t vbase,
+                                        uint32_t region_bytes, int row0, int jbase, int valid,
+                                        bool full, int lane, float ks_b, float vs_b) {
     if constexpr (NT == 1 && !kCausal) {
       block_decode(kbase, vbase, region_bytes, row0, valid, lane, ks_b, vs_b);
       return;
@@ -577,9 +687,15 @@ struct Consumer {
     float mx[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
+    if constexpr (kScore) apply_rules(a, s, ks_b, jbase, valid, full, lane);
 #pragma unroll
     for (int mt = 0; mt < kTiles; ++mt) {
-      if constexpr (kCausal) {
+      if constexpr (kScore) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[nt][k & 1] = fmaxf(mx[nt][k & 1], s[mt][nt][k]);
+      } else if constexpr (kCausal) {
         const int t0 = jbase + mt * 16 + (lane >> 2);   // key positions of the thread's rows
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -664,17 +780,24 @@ struct Consumer {
       }
 
     // ---- O^T += V^T P^T
-    // Rows of V past the sequence's end are unwritten slots: their lanes are
-    // zeroed (only in a tail block) so that 0 * NaN never reaches the sum.
-    const bool tail = valid < BS;
+    // Rows of V past the sequence's end are unwritten slots, and in a scored call rows
+    // that no column sees may hold anything: their lanes are zeroed (only in a tail
+    // block) so that 0 * NaN never reaches the sum.
+    int v0 = 0, v1 = valid;
+    if constexpr (kScore) {
+      v0 = from_min - jbase;
+      v1 = min(valid, lim_max + 1 - jbase);
+    }
+    const bool tail = v1 < BS || (kScore && v0 > 0);
 #pragma unroll
     for (int mt = 0; mt < kTiles; ++mt) {
       // tokens of this thread in the A fragment: 2c, 2c+1 (regs 0,1) and 8+2c, 9+2c (regs 2,3)
       uint32_t mk_lo = 0xffffffffu, mk_hi = 0xffffffffu;
       if (tail) {
         const int tl = mt * 16 + 2 * c;
-        mk_lo = (tl < valid ? 0x0000ffffu : 0u) | (tl + 1 < valid ? 0xffff0000u : 0u);
-        mk_hi = (tl + 8 < valid ? 0x0000ffffu : 0u) | (tl + 9 < valid ? 0xffff0000u : 0u);
+        auto in = [&](int t) { return t < v1 && (!kScore || t >= v0); };
+        mk_lo = (in(tl) ? 0x0000ffffu : 0u) | (in(tl + 1) ? 0xffff0000u : 0u);
+        mk_hi = (in(tl + 8) ? 0x0000ffffu : 0u) | (in(tl + 9) ? 0xffff0000u : 0u);
       }
       if constexpr (!T::kFp8) {
         const int q4 = lane >> 3;
@@ -796,8 +919,7 @@ __device__ __forceinline__ size_t part_base(const DecodeArgs& a, int w, long lon
   return (size_t)p;
 }
 
-// kOff: a shared-prefix launch, each sequence read from token a.len_off[s] on.
-template <int KVT, int BS, int NT, bool kCausal, bool kOff>
+template <int KVT, int BS, int NT, bool kCausal, int kMode>
 __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
     decode_mma_kernel(const __grid_constant__ CUtensorMap tmap, const DecodeArgs a) {
   using T = KvTraits<KVT>;
@@ -830,7 +952,7 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
     long long total = 0;
     for (int base = 0; base < a.B; base += 32) {
       const int s = base + lane;
-      int nb = s < a.B ? blocks_of(clamp_len<kOff>(a, s), BS) : 0;
+      int nb = s < a.B ? blocks_of(clamp_len<kMode>(a, s), BS) : 0;
       total += (long long)__reduce_add_sync(0xffffffffu, (unsigned)nb);
       // units of a sequence with no tokens get no piece: mark them once
       if (blockIdx.x == 0 && __any_sync(0xffffffffu, s < a.B && nb == 0)) {
@@ -851,7 +973,7 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
       bool found = false;
       for (int base = 0; base < a.B && !found; base += 32) {
         const int s = base + lane;
-        const int nbs = s < a.B ? blocks_of(clamp_len<kOff>(a, s), BS) : 0;
+        const int nbs = s < a.B ? blocks_of(clamp_len<kMode>(a, s), BS) : 0;
         const int nbu = nbs * a.NHG;
         int incl = nbu;
 #pragma unroll
@@ -901,13 +1023,13 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
     cur.j = hdr->j;
     cur.gb = hdr->gb0;
     cur.remaining = hdr->gb1 - hdr->gb0;
-    cur.n = cur.remaining > 0 ? clamp_len<kOff>(a, cur.s) : 0;
+    cur.n = cur.remaining > 0 ? clamp_len<kMode>(a, cur.s) : 0;
     cur.nb = blocks_of(cur.n, BS);
   } else {
     const int u = blockIdx.y;
     cur.s = u / a.NHG;
     cur.hg = u % a.NHG;
-    cur.n = clamp_len<kOff>(a, cur.s);
+    cur.n = clamp_len<kMode>(a, cur.s);
     cur.nb = blocks_of(cur.n, BS);
     part_p = blockIdx.x;
     const int jb = (int)((long long)part_p * cur.nb / a.S);
@@ -931,12 +1053,14 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
         id_unit_s = cur.s;
         id_base = cur.j;
         const int jj = id_base + lane;
-        // shared-prefix decode: the sequence's private blocks, after its prefix
+        // shared-prefix decode: the sequence's private blocks, after its prefix; a
+        // scored call: from the first block that holds a seen key
         // (offset from the length clamp_len clamps, so jo + cur.nb <= max_blocks)
         int jo = 0;
-        if constexpr (kOff)
+        if constexpr (kMode == kSuffix)
           jo = first_token(a, cur.s, min(max(__ldg(a.seq_lens + cur.s), 0), a.max_blocks * BS)) /
                BS;
+        if constexpr (kMode == kScored) jo = (scored_len(a, cur.s) - cur.n) / BS;
         ids = jj < cur.nb ? __ldg(a.tables + (size_t)cur.s * a.max_blocks + jo + jj) : 0;
       }
       int blk = __shfl_sync(0xffffffffu, ids, cur.j - id_base);
@@ -1016,7 +1140,7 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
         stage = 0;
         ++round;
       }
-      cursor_next<kOff>(cur, a);
+      cursor_next<kMode>(cur, a);
     }
     // drain: every stage still in flight must land before the CTA may exit
     if (lane == 0) {
@@ -1038,8 +1162,10 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
   if (warp >= a.HG) return;   // no spare warps are launched; guard anyway
 
   // ---------------------------------------------------------------- consumers
-  Consumer<KVT, BS, NT, kCausal> cons;
+  constexpr bool kScore = kMode == kScored;
+  Consumer<KVT, BS, NT, kCausal, kScore> cons;
   cons.qk_scale_log2_ = a.qk_scale_log2;
+  if constexpr (kScore) cons.cap_in_ = a.cap_in;
   cons.bscaled_ = T::kFp8 && a.block_scales != nullptr;
   cons.reset();
   const int w = warp;
@@ -1051,7 +1177,7 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
   if (a.mode == 1 && cur.remaining <= 0) {
     if (a.pdl) grid_dependency_wait();
     for (int r = 0; r < a.R; ++r) {
-      const long long qr = Consumer<KVT, BS, NT, kCausal>::q_row(a, cur.s, hkv, r);
+      const long long qr = Consumer<KVT, BS, NT, kCausal, kScore>::q_row(a, cur.s, hkv, r);
       if (a.S == 1) {
         for (int d = lane; d < kD; d += 32) store_from_float(a.out, (size_t)qr * kD + d, a.out_dtype, 0.f);
       } else {
@@ -1080,13 +1206,14 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
     const uint32_t sbase = ring + (uint32_t)stage * stage_bytes;
     const int valid = min(BS, cur.n - cur.j * BS);
     const int jbase = cur.j * BS;
-    const bool full = !kCausal || jbase + BS - 1 <= cur.n - a.q_len;
+    bool full = !kCausal || jbase + BS - 1 <= cur.n - a.q_len;
+    if constexpr (kScore) full = jbase >= cons.from_max && jbase + BS - 1 <= cons.lim_min;
     float ks_b = 1.f, vs_b = 1.f;
     if (T::kFp8 && a.block_scales) {
       ks_b = hdr->bscale[stage][0][w];
       vs_b = hdr->bscale[stage][1][w];
     }
-    cons.block(sbase, sbase + T::kRegions * region_bytes, region_bytes, w * BS, jbase, valid,
+    cons.block(a, sbase, sbase + T::kRegions * region_bytes, region_bytes, w * BS, jbase, valid,
                full, lane, ks_b, vs_b);
     __syncwarp();
     if (lane == 0) mbar_arrive(&hdr->empty[stage]);
@@ -1120,7 +1247,7 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
       }
       cons.finish(a, cur.s, hkv, lane, whole, part_base(a, w, slot, part_p), a.mode == 0);
     }
-    cursor_next<kOff>(cur, a);
+    cursor_next<kMode>(cur, a);
     if (cur.remaining > 0 && cur.j == 0) {
       hkv = cur.hg * a.HG + w;
       cons.load_q(a, cur.s, cur.n, hkv, lane);
@@ -1132,13 +1259,13 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
   grid_launch_dependents();
 }
 
-template <int KVT, int BS, int NT, bool kCausal, bool kOff = false>
+template <int KVT, int BS, int NT, bool kCausal, int kMode = kPlain>
 cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, int gx, int gy,
                      cudaStream_t stream) {
   // the ring needs mma_smem_bytes; a larger request (a.smem_bytes) caps how many
   // CTAs can share an SM
   const size_t smem = std::max(mma_smem_bytes(KVT, BS, a.HG, a.stages), (size_t)a.smem_bytes);
-  auto kern = decode_mma_kernel<KVT, BS, NT, kCausal, kOff>;
+  auto kern = decode_mma_kernel<KVT, BS, NT, kCausal, kMode>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

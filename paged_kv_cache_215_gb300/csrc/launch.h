@@ -65,6 +65,17 @@ struct DecodeArgs {
   // row (split * q_len + i) * Hq + head.
   const int32_t* key_limit;
   float* out_lse;
+  // Scored attention (score.cuh).  Lengths are limited to max_len.  With a cap, scores
+  // are cap_out * tanh(cap_in * <q, k>) (log2 units; cap_in carries the softmax scale
+  // and k_scale), without one (cap_in = 0) qk_scale_log2 * <q, k>.
+  int max_len;
+  float cap_in, cap_out;
+  int window;                // 0: none
+  const float* slopes;       // [Hq] or nullptr
+  const int32_t* prefix_lens;// [B] or nullptr
+  const int32_t* doc_starts; // [B, q_len] or nullptr
+  float* scores;             // [B, Hkv, max_len, score_row] in log2 units, or nullptr
+  int score_row;             // R rounded up to an even number
 };
 
 // Shared memory the tensor-core kernel needs for one CTA.
@@ -75,6 +86,10 @@ bool mma_supported(int kv_dtype, int BS, int D, int G, int q_len);
 cudaError_t launch_decode_mma(const CUtensorMap* map, const DecodeArgs& a, int grid_x, int grid_y,
                               cudaStream_t stream);
 cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t stream);
+// The scored instances of both.
+cudaError_t launch_decode_mma_scored(const CUtensorMap* map, const DecodeArgs& a, int grid_x,
+                                     cudaStream_t stream);
+cudaError_t launch_decode_simt_scored(const DecodeArgs& a, cudaStream_t stream);
 // Chunked prefill on tcgen05 (one CTA per 128-row query tile, KV head, sequence).
 bool prefill_tc_supported(int kv_dtype, int q_dtype, int BS, int D, int G);
 cudaError_t launch_prefill_tc(const CUtensorMap* map, const DecodeArgs& a, cudaStream_t stream);
@@ -90,9 +105,20 @@ cudaError_t launch_prefix_check(const int32_t* tables, int max_blocks, const int
                                 const int32_t* prefix_table, int prefix_blocks,
                                 const int32_t* prefix_lens, int prefix_len_max, int B, int BS,
                                 int32_t* status, cudaStream_t stream);
-// Merge of [rows, S, D] partials (the public merge_partials layout).
+// Merge of [rows, S, D] partials (the public merge_partials layout); out_lse [rows] or
+// nullptr.
 cudaError_t launch_merge_rows(void* out, int out_dtype, const float* part_o, const float* part_lse,
-                              int rows, int S, int D, bool pdl, cudaStream_t stream);
+                              int rows, int S, int D, bool pdl, cudaStream_t stream,
+                              float* out_lse = nullptr);
+
+// Accumulated attention weights: rows of fp32 per (sequence, KV head).
+struct WeightRows {
+  float* data;
+  int64_t seq_stride, head_stride;
+};
+// out = in (nullptr: 0) + the softmax weights of a.scores' scores by a.out_lse
+cudaError_t launch_accumulate(const DecodeArgs& a, const WeightRows& in, const WeightRows& out,
+                              cudaStream_t stream);
 
 struct AppendArgs {
   void* pool;

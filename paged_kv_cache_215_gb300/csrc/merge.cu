@@ -228,11 +228,12 @@ __global__ void __launch_bounds__(32 * kRowsPerCta) merge_units_warp_kernel(cons
 // [rows, S, D] partials (the layout of the public merge_partials).
 __global__ void __launch_bounds__(kThreads)
     merge_rows_kernel(void* out, int out_dtype, const float* part_o, const float* part_lse, int S,
-                      int D) {
+                      int D, float* out_lse) {
   grid_launch_dependents();
   grid_dependency_wait();
   const size_t r = blockIdx.x;
-  merge_row(part_lse + r * S, 1, part_o + r * S * D, D, S, D, out, r * D, out_dtype);
+  merge_row(part_lse + r * S, 1, part_o + r * S * D, D, S, D, out, r * D, out_dtype,
+            out_lse ? out_lse + r : nullptr);
 }
 
 }  // namespace
@@ -285,10 +286,11 @@ cudaError_t launch_merge_units(const DecodeArgs& a, bool pdl, cudaStream_t strea
 }
 
 cudaError_t launch_merge_rows(void* out, int out_dtype, const float* part_o, const float* part_lse,
-                              int rows, int S, int D, bool pdl, cudaStream_t stream) {
+                              int rows, int S, int D, bool pdl, cudaStream_t stream,
+                              float* out_lse) {
   if (D > kMaxD) return cudaErrorInvalidValue;
   if (rows == 0) return cudaSuccess;
-  void* args[] = {&out, &out_dtype, &part_o, &part_lse, &S, &D};
+  void* args[] = {&out, &out_dtype, &part_o, &part_lse, &S, &D, &out_lse};
   return launch_pdl(reinterpret_cast<const void*>(merge_rows_kernel), dim3(rows), args, pdl,
                     stream);
 }

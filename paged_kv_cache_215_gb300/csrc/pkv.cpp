@@ -1314,6 +1314,194 @@ int verify_drafts(int32_t* d_tokens, int32_t* d_num_accepted, const pkv_probs* t
   return launch_verify(a, dev.sms, stream) == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
+// ---------------------------------------------------------------- scored attention
+
+// Workspace of a scored call: the partials of the kernel that runs, then (with weights)
+// every row's log-sum-exp and the scores.
+struct ScoredWs {
+  size_t part_o, part_lse, info, lse, scores, bytes;
+};
+static size_t score_row(int R) { return (size_t)(R + 1) / 2 * 2; }
+static void add_record(const pkv_geometry& g, int batch, int q_len, int max_seq_len, ScoredWs* w) {
+  w->lse = w->bytes;
+  w->scores = w->lse + align256((size_t)batch * q_len * g.num_q_heads * sizeof(float));
+  w->bytes = w->scores +
+             align256((size_t)batch * g.num_kv_heads * max_seq_len *
+                      score_row(q_len * (g.num_q_heads / g.num_kv_heads)) * sizeof(float));
+}
+static ScoredWs scored_ws_mma(const pkv_geometry& g, int batch, int q_len, int max_seq_len,
+                              const MmaPlan& plan, bool weights) {
+  const BalancedWs b = balanced_ws(g, batch, q_len, plan);
+  ScoredWs w{b.o_off, b.lse_off, b.info_off, 0, 0, b.bytes};
+  if (weights) add_record(g, batch, q_len, max_seq_len, &w);
+  return w;
+}
+static ScoredWs scored_ws_simt(const pkv_geometry& g, int batch, int max_seq_len, int S,
+                               bool weights) {
+  ScoredWs w{};
+  if (S > 1 || weights) {
+    const size_t rows = (size_t)batch * g.num_q_heads * S;
+    w.part_lse = align256(rows * g.head_dim * sizeof(float));
+    w.bytes = w.part_lse + align256(rows * sizeof(float));
+  }
+  if (weights) add_record(g, batch, 1, max_seq_len, &w);
+  return w;
+}
+
+size_t paged_decode_scored_workspace_bytes(const pkv_geometry* g, int batch, int q_len,
+                                           int max_seq_len, int with_weights) {
+  if (!geometry_ok(g) || batch < 0 || q_len < 1 || max_seq_len < 0) return 0;
+  DeviceInfo dev;
+  if (!device_info(&dev)) return 0;
+  const int G = g->num_q_heads / g->num_kv_heads;
+  size_t need = 0;
+  MmaPlan plan;
+  if (mma_supported(g->kv_dtype, g->block_size, g->head_dim, G, q_len) &&
+      plan_mma(*g, dev, nullptr, &plan))
+    need = scored_ws_mma(*g, batch, q_len, max_seq_len, plan, with_weights != 0).bytes;
+  if (q_len == 1)
+    need = std::max(need, scored_ws_simt(*g, batch, max_seq_len,
+                                         simt_auto_splits(*g, batch, max_seq_len, dev.sms),
+                                         with_weights != 0).bytes);
+  return need + 256;
+}
+
+int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* d_q,
+                                  pkv_dtype q_dtype, int q_len, const pkv_pool* pool, int layer,
+                                  const int32_t* d_block_tables, int max_blocks_per_seq,
+                                  const int32_t* d_seq_lens, int batch, int max_seq_len,
+                                  float scale, float k_scale, float v_scale,
+                                  const pkv_scores* scores, const pkv_weights* weights,
+                                  const pkv_weights* weights_in, void* d_workspace,
+                                  size_t ws_bytes, cudaStream_t stream) {
+  pkv_pool* p = const_cast<pkv_pool*>(pool);
+  if (!p || batch < 0 || max_seq_len < 0 || layer < 0 || layer >= p->g.num_layers || q_len < 1)
+    return PKV_EINVAL;
+  const pkv_geometry& g = p->g;
+  if (!act_dtype(out_dtype) || !act_dtype(q_dtype) || !std::isfinite(scale)) return PKV_EINVAL;
+  const bool fp8 = g.kv_dtype == PKV_FP8_E4M3;
+  const float* bscales = fp8 ? p->d_block_scales : nullptr;
+  if (fp8 && !bscales &&
+      (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale)))
+    return PKV_EINVAL;
+  if (!fp8 || bscales) k_scale = v_scale = 1.f;
+  const pkv_scores none{};
+  const pkv_scores& sc = scores ? *scores : none;
+  const double x_scale = (double)scale * k_scale;
+  if (!(sc.cap >= 0.f) || !std::isfinite(sc.cap) || sc.window < 0 ||
+      (sc.cap > 0.f && !std::isfinite((float)(x_scale / sc.cap))))
+    return PKV_EINVAL;
+  if (batch == 0) return PKV_OK;
+  if (!d_out || !d_q || !d_block_tables || !d_seq_lens || max_blocks_per_seq < 1 ||
+      !aligned16(d_q) || !aligned16(d_out) || (d_workspace && !aligned16(d_workspace)))
+    return PKV_EINVAL;
+  if ((long long)max_seq_len > (long long)max_blocks_per_seq * g.block_size) return PKV_EINVAL;
+  if (!weights && weights_in) return PKV_EINVAL;
+  WeightRows w_in{}, w_out{};
+  if (weights) {
+    const pkv_rows out_rows{weights->data, weights->seq_stride, weights->head_stride};
+    if (!out_rows_ok(&out_rows, PKV_F32, batch, g.num_kv_heads, std::max(max_seq_len, 1)))
+      return PKV_EINVAL;
+    w_out = {weights->data, weights->seq_stride, weights->head_stride};
+    if (weights_in) {
+      const pkv_rows in_rows{weights_in->data, weights_in->seq_stride, weights_in->head_stride};
+      if (!rows_ok(&in_rows, PKV_F32) || !same_or_apart(&out_rows, &in_rows, batch, g.num_kv_heads))
+        return PKV_EINVAL;
+      w_in = {weights_in->data, weights_in->seq_stride, weights_in->head_stride};
+    }
+  }
+  DeviceInfo dev;
+  if (!device_info(&dev)) return PKV_ECUDA;
+  const int G = g.num_q_heads / g.num_kv_heads;
+  if (batch > 65535 || g.num_kv_heads > 65535) return PKV_EUNSUPPORTED;
+  if ((int64_t)q_len * g.num_q_heads > 0x7fffffff) return PKV_EUNSUPPORTED;
+
+  DecodeArgs a{};
+  a.q = d_q;
+  a.out = d_out;
+  a.pool = p->d_pool;
+  a.tables = d_block_tables;
+  a.seq_lens = d_seq_lens;
+  a.status = p->d_status;
+  a.B = batch;
+  a.Hq = g.num_q_heads;
+  a.Hkv = g.num_kv_heads;
+  a.G = G;
+  a.D = g.head_dim;
+  a.BS = g.block_size;
+  a.L = g.num_layers;
+  a.layer = layer;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = g.num_blocks;
+  a.q_dtype = q_dtype;
+  a.out_dtype = out_dtype;
+  a.kv_dtype = g.kv_dtype;
+  a.qk_scale_log2 = (float)(x_scale * 1.4426950408889634);
+  a.v_scale = v_scale;
+  a.block_scales = bscales;
+  a.q_len = q_len;
+  a.R = G * q_len;
+  a.max_len = max_seq_len;
+  if (sc.cap > 0.f) {
+    a.cap_in = (float)(x_scale / sc.cap);
+    a.cap_out = (float)(sc.cap * 1.4426950408889634);
+  }
+  a.window = sc.window;
+  a.slopes = sc.d_slopes;
+  a.prefix_lens = sc.d_prefix_lens;
+  a.doc_starts = sc.d_doc_starts;
+  a.score_row = (int)score_row(a.R);
+  char* ws = static_cast<char*>(d_workspace);
+  auto record = [&](const ScoredWs& w) {
+    if (!weights) return;
+    a.out_lse = reinterpret_cast<float*>(ws + w.lse);
+    a.scores = reinterpret_cast<float*>(ws + w.scores);
+  };
+  auto accumulate = [&]() -> int {
+    if (!weights) return PKV_OK;
+    return launch_accumulate(a, w_in, w_out, stream) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+  };
+
+  const bool q_ok = fp8 ? (q_dtype == PKV_BF16 || q_dtype == PKV_F16) : (int)q_dtype == g.kv_dtype;
+  if (q_ok && mma_supported(g.kv_dtype, g.block_size, g.head_dim, G, q_len)) {
+    MmaPlan plan;
+    if (!plan_mma(g, dev, nullptr, &plan)) return PKV_EUNSUPPORTED;
+    const CUtensorMap* map = p->tmap(plan.HG);
+    if (!map) return PKV_ECUDA;
+    const ScoredWs w = scored_ws_mma(g, batch, q_len, max_seq_len, plan, weights != nullptr);
+    if (!ws || ws_bytes < w.bytes) return PKV_ENOMEM;
+    a.HG = plan.HG;
+    a.NHG = plan.NHG;
+    a.stages = plan.stages;
+    a.smem_bytes = (int)plan.smem;
+    a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+    a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+    a.unit_info = reinterpret_cast<int2*>(ws + w.info);
+    a.slots = plan.grid + batch * plan.NHG;
+    a.early_trigger = fp8 ? 0 : 1;
+    record(w);
+    if (launch_decode_mma_scored(map, a, plan.grid, stream) != cudaSuccess) return PKV_ECUDA;
+    if (launch_merge_units(a, true, stream) != cudaSuccess) return PKV_ECUDA;
+    return accumulate();
+  }
+  if (q_len > 1 || g.head_dim % 32 != 0 || g.head_dim > 256 || G > 16) return PKV_EUNSUPPORTED;
+  const int S = simt_auto_splits(g, batch, max_seq_len, dev.sms);
+  const ScoredWs w = scored_ws_simt(g, batch, max_seq_len, S, weights != nullptr);
+  if (w.bytes > 0 && (!ws || ws_bytes < w.bytes)) return PKV_ENOMEM;
+  a.S = S;
+  if (w.bytes > 0) {
+    a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+    a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  }
+  record(w);
+  if (launch_decode_simt_scored(a, stream) != cudaSuccess) return PKV_ECUDA;
+  if (w.bytes > 0 && launch_merge_rows(d_out, out_dtype, a.part_o, a.part_lse,
+                                       batch * g.num_q_heads, S, g.head_dim, true, stream,
+                                       a.out_lse) != cudaSuccess)
+    return PKV_ECUDA;
+  return accumulate();
+}
+
 int pkv_check_status(const pkv_pool* p, cudaStream_t stream) {
   if (!p) return PKV_EINVAL;
   if (cudaStreamSynchronize(stream) != cudaSuccess) return PKV_ECUDA;

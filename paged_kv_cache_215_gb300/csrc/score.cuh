@@ -1,0 +1,72 @@
+// score.cuh -- the rules of paged_decode_attention_scored: which keys a query token
+// sees, and what becomes of a score before the softmax.
+//
+// Query token i of a sequence of n tokens sits at p = n - q_len + i.  It sees key j if
+//   (j <= p or j < min(prefix, n)),  p - j < window (window > 0),  j >= its document's
+//   first key:
+// all of them one interval [lo, hi).  A score x (already scaled) becomes
+// cap tanh(x / cap) (cap > 0), then loses slope |p - j|.
+#pragma once
+#include "device.cuh"
+#include "launch.h"
+
+namespace pkv {
+
+// The sequence's length as the scored calls take it: limited to [0, a.max_len].
+__device__ __forceinline__ int scored_len(const DecodeArgs& a, int s) {
+  int n = __ldg(a.seq_lens + s);
+  if (n < 0 || n > a.max_len) {
+    record_error(a.status, PKV_EBOUNDS);
+    n = n < 0 ? 0 : a.max_len;
+  }
+  return n;
+}
+
+struct KeyRange {
+  int lo, hi;                // keys [lo, hi); hi <= lo: none
+};
+
+__device__ __forceinline__ KeyRange key_range(const DecodeArgs& a, int s, int n, int i) {
+  const int p = n - a.q_len + i;
+  if (p < 0) return {0, 0};
+  int lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+  if (a.doc_starts) lo = max(lo, __ldg(a.doc_starts + (size_t)s * a.q_len + i));
+  int hi = p + 1;
+  if (a.prefix_lens) hi = max(hi, min(__ldg(a.prefix_lens + s), n));
+  return {lo, hi};
+}
+
+// The first key that any query token of the sequence sees; n if none sees a key.
+__device__ __forceinline__ int first_key(const DecodeArgs& a, int s, int n) {
+  if (a.window <= 0 && !a.doc_starts) return n > 0 ? 0 : n;
+  int first = n;
+  for (int i = max(0, a.q_len - n); i < a.q_len; ++i) {
+    const KeyRange k = key_range(a, s, n, i);
+    if (k.lo < k.hi) first = min(first, k.lo);
+    if (!a.doc_starts) break;                  // the window's starts only grow
+  }
+  return first;
+}
+
+// The first token the scored decode reads of a sequence: its first seen key's block;
+// n if there is none.
+__device__ __forceinline__ int first_read(const DecodeArgs& a, int s, int n) {
+  const int f = first_key(a, s, n);
+  return f >= n ? n : f / a.BS * a.BS;
+}
+
+// tanh within 2^-22 of itself: below 0.6 an odd polynomial (fitted by weighted least
+// squares to the smallest largest relative error, 2^-28), above it 1 - 2 / (e^2x + 1).
+__device__ __forceinline__ float tanh_score(float x) {
+  const float z = x * x;
+  const float e = ex2_ftz(x * (2.f * kLog2e));
+  const float big = fmaf(-2.f, __fdividef(1.f, e + 1.f), 1.f);
+  float p = -0x1.825852p-8f;
+  p = fmaf(p, z, 0x1.54b8a0p-6f);
+  p = fmaf(p, z, -0x1.b898dep-5f);
+  p = fmaf(p, z, 0x1.1109aep-3f);
+  p = fmaf(p, z, -0x1.55553ep-2f);
+  return fabsf(x) < 0.6f ? fmaf(x * z, p, x) : big;
+}
+
+}  // namespace pkv

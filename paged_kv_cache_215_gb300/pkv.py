@@ -64,6 +64,16 @@ class Rows(ctypes.Structure):
                 ("head_stride", ctypes.c_int64)]
 
 
+class ScoreRules(ctypes.Structure):
+    _fields_ = [("cap", ctypes.c_float), ("window", ctypes.c_int32), ("d_slopes", ctypes.c_void_p),
+                ("d_prefix_lens", ctypes.c_void_p), ("d_doc_starts", ctypes.c_void_p)]
+
+
+class WeightRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("seq_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
 class Probs(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("seq_stride", ctypes.c_int64),
                 ("row_stride", ctypes.c_int64)]
@@ -79,6 +89,7 @@ def _load() -> ctypes.CDLL:
     I64 = ctypes.c_int64
     G = ctypes.POINTER(Geometry)
     R = ctypes.POINTER(Rows)
+    W = ctypes.POINTER(WeightRows)
     sig = {
         "kv_pool_bytes": (Z, [G]),
         "kv_pool_create": (I, [G, P, Z, P, ctypes.POINTER(P)]),
@@ -120,6 +131,9 @@ def _load() -> ctypes.CDLL:
                                F, F, P]),
         "verify_drafts": (I, [P, P, ctypes.POINTER(Probs), ctypes.POINTER(Probs), I, P, P, P, P,
                               I, I, I, P, P]),
+        "paged_decode_attention_scored": (I, [P, I, P, I, I, P, I, P, I, P, I, I, F, F, F,
+                                              ctypes.POINTER(ScoreRules), W, W, P, Z, P]),
+        "paged_decode_scored_workspace_bytes": (Z, [G, I, I, I, I]),
         "pkv_check_status": (I, [P, P]),
         "pkv_wait_selftest": (I, [P, P]),
         "pkv_strerror": (ctypes.c_char_p, [I]),
@@ -144,7 +158,8 @@ class _NoTensors:
 
 def _load_tensors():
     """The compiled module that checks and passes tensors of the short calls (rope_apply,
-    append_rope, verify_drafts); without it they raise, and every other call works."""
+    append_rope, verify_drafts, paged_decode_attention_scored); without it they raise, and
+    every other call works."""
     path = _build.BINDING
     if not os.path.exists(path):
         return _NoTensors(f"{path} is not built (it needs a torch for CUDA and Python's headers); "
@@ -174,6 +189,7 @@ EXPORTS = ("kv_pool_bytes", "kv_pool_create", "kv_pool_destroy", "kv_pool_geomet
            "paged_decode_attention_cascade", "paged_decode_workspace_bytes_cascade",
            "pkv_rope_freqs", "pkv_rope_freqs_from", "rope_apply", "kv_append_rope",
            "verify_drafts",
+           "paged_decode_attention_scored", "paged_decode_scored_workspace_bytes",
            "pkv_check_status", "pkv_wait_selftest", "pkv_strerror", "pkv_launch_count")
 
 
@@ -573,6 +589,56 @@ def paged_decode_attention_cascade(out, q, pool: KVPool, layer, prefix_table, pr
         max_seq_len, scale, k_scale, v_scale, _ptr(workspace), workspace.numel(),
         ctypes.byref(opts) if opts is not None else None, _stream(stream)),
         "paged_decode_attention_cascade")
+    return out
+
+
+class Scores:
+    """Rules of paged_decode_attention_scored (include/pkv.h: pkv_scores).
+
+    cap: a score x becomes cap * tanh(x / cap) (0: none).  window: a query sees that many
+    keys, its own the last (0: all).  slopes [num_q_heads] float32: slope * distance is
+    taken off.  prefix_lens [B] int32: the tokens of a sequence that are seen from ahead
+    of them too.  doc_starts [B, q_len] int32 ([B] for one query token): the first token of
+    each query's document.  A call goes by what the attributes hold when it is made."""
+
+    def __init__(self, cap: float = 0.0, window: int = 0, slopes=None, prefix_lens=None,
+                 doc_starts=None):
+        self.cap, self.window, self.slopes = cap, window, slopes
+        self.prefix_lens, self.doc_starts = prefix_lens, doc_starts
+
+
+def scored_workspace_bytes(geom: Geometry, batch: int, q_len: int, max_seq_len: int,
+                           weights: bool = False) -> int:
+    return int(_lib.paged_decode_scored_workspace_bytes(ctypes.byref(geom), batch, q_len,
+                                                        max_seq_len, int(weights)))
+
+
+_NO_RULES = Scores()
+
+
+def paged_decode_attention_scored(out, q, pool: KVPool, layer, tables, seq_lens, max_seq_len,
+                                  scale, scores: Optional[Scores] = None, k_scale=1.0, v_scale=1.0,
+                                  weights=None, weights_in=None, workspace=None, stream=None):
+    """Attention of the last query tokens of every sequence (q, out: [B, Hq, D] or
+    [B, q_len, Hq, D]) under the rules of `scores`.  weights [B, Hkv, >= max_seq_len]
+    float32 (any strides with a unit one along the tokens) receives weights_in (None: 0)
+    plus each token's softmax weights, summed over the queries and the query heads of its
+    KV head; pass one tensor as both to accumulate."""
+    if workspace is None:
+        q_len = q.shape[1] if q.dim() == 4 else 1
+        workspace = torch.empty(
+            max(16, scored_workspace_bytes(pool.geom, q.shape[0], q_len, max_seq_len,
+                                           weights is not None)),
+            dtype=torch.uint8, device=pool.storage.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    r = scores if scores is not None else _NO_RULES
+    rc = _tensors.attend_scored(out, q, pool.handle.value if pool.handle else 0, pool.storage,
+                                layer, tables, seq_lens, max_seq_len, scale, r.cap, r.window,
+                                r.slopes, r.prefix_lens, r.doc_starts, k_scale, v_scale, weights,
+                                weights_in, workspace, stream)
+    if rc:
+        raise PkvError(rc, "paged_decode_attention_scored")
     return out
 
 

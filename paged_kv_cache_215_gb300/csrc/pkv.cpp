@@ -1484,7 +1484,15 @@ int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* 
     if (launch_merge_units(a, true, stream) != cudaSuccess) return PKV_ECUDA;
     return accumulate();
   }
-  if (q_len > 1 || g.head_dim % 32 != 0 || g.head_dim > 256 || G > 16) return PKV_EUNSUPPORTED;
+  if (q_len > 1) {
+    // chunks with more query rows than the decode kernel holds
+    if (weights || !prefill_tc_supported(g.kv_dtype, q_dtype, g.block_size, g.head_dim, G))
+      return PKV_EUNSUPPORTED;
+    const CUtensorMap* map = p->tmap_tiles();
+    if (!map) return PKV_ECUDA;
+    return launch_prefill_tc_scored(map, a, stream) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+  }
+  if (g.head_dim % 32 != 0 || g.head_dim > 256 || G > 16) return PKV_EUNSUPPORTED;
   const int S = simt_auto_splits(g, batch, max_seq_len, dev.sms);
   const ScoredWs w = scored_ws_simt(g, batch, max_seq_len, S, weights != nullptr);
   if (w.bytes > 0 && (!ws || ws_bytes < w.bytes)) return PKV_ENOMEM;

@@ -42,6 +42,7 @@
 // stage is refilled once every issuer's MMAs reading it have completed.
 #include "device.cuh"
 #include "launch.h"
+#include "score.cuh"
 
 namespace pkv {
 namespace {
@@ -94,6 +95,8 @@ struct Bars {
   uint64_t s_full[kQT][2], p_full[kQT][2], p_free[kQT][2], o_done[kQT];
   uint64_t o_final[kQT];                      // query tile t's last P V has completed
   uint64_t v_zeroed;                          // the tail tile's V rows past the end are zero
+  uint64_t v_headed;                          // scored: the first tile's V rows ahead of every
+                                              // query's keys are zero
   uint64_t q_ready;                           // the Q tiles are staged
   uint64_t eref_ready;                        // E4M3 per-block scales: the reference exponent is in
   int eref[4];                                // per converter warp: largest exponent of the V scales
@@ -152,7 +155,9 @@ __device__ __forceinline__ int key_tiles(const DecodeArgs& a, int n, int qt) {
   return p_last >= 0 ? (p_last + kN) / kN : 0;
 }
 
-template <int KVT>
+// kScore: a chunk under the rules of score.cuh; each row sees its own interval of keys,
+// and the CTA reads from the first key that any of its rows sees.
+template <int KVT, bool kScore>
 __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, const DecodeArgs a) {
   using C = PfCfg<KVT>;
@@ -189,10 +194,32 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
     if (tid == 0) record_error(a.status, PKV_EBOUNDS);
     n = n < 0 ? 0 : cap;
   }
+  if constexpr (kScore) n = scored_len(a, s);
   // key tiles jt0 .. jt0 + T - 1 of the sequence; local tile j is global tile jt0 + j
   int tiles[kQT], jt0 = 0;                        // key tiles each slot computes
   int T = 0;                                      // key tiles the CTA loads
-  if (casc) {
+  int read0 = 0;                                  // scored: the first key any row sees
+  if constexpr (kScore) {
+    int hi[kQT];
+    read0 = n;
+#pragma unroll
+    for (int t = 0; t < kQT; ++t) {
+      hi[t] = 0;
+      for (int i = lane; i < QT; i += 32) {
+        const int tok = (pair * kQT + t) * QT + i;
+        if (tok >= a.q_len) break;
+        const KeyRange k = key_range(a, s, n, tok);
+        if (k.lo >= k.hi) continue;
+        read0 = min(read0, k.lo);
+        hi[t] = max(hi[t], k.hi);
+      }
+      hi[t] = __reduce_max_sync(0xffffffffu, hi[t]);
+    }
+    read0 = __reduce_min_sync(0xffffffffu, read0);
+    jt0 = read0 / kN;
+#pragma unroll
+    for (int t = 0; t < kQT; ++t) tiles[t] = hi[t] > 0 ? (hi[t] + kN - 1) / kN - jt0 : 0;
+  } else if (casc) {
     const int nt = (n + kN - 1) / kN;
     jt0 = (int)((long long)split * nt / a.S);
     const int jt1 = (int)((long long)(split + 1) * nt / a.S);
@@ -216,6 +243,9 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
   // the sequence's last key tile, if it is ragged and this CTA reads it (local index)
   const int jg_tail = (n % kN != 0) ? (n - 1) / kN : -1;
   const int j_tail = (jg_tail >= jt0 && jg_tail < jt0 + T) ? jg_tail - jt0 : -1;
+  // scored: rows of the first tile that no query sees (their block may be stale: the
+  // first seen key's is read in its place, and V is zeroed there), and that block
+  const int head = kScore ? read0 - jt0 * kN : 0, blk0 = kScore ? read0 / a.BS : 0;
 
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
@@ -234,6 +264,7 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
       mbar_init(&bars->o_final[t], 1);
     }
     mbar_init(&bars->v_zeroed, 1);
+    mbar_init(&bars->v_headed, 1);
     mbar_init(&bars->q_ready, 32 * kSoftmaxWarps);
     mbar_init(&bars->eref_ready, kFp8 ? C::kConvWarps : 1);
     bars->abort_flag = 0;
@@ -361,7 +392,8 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
           // both 64-column halves (bs x 256 bytes).  Blocks past the sequence's
           // last one are replaced by its last block: their keys are masked and
           // their V rows zeroed before use.
-          const int jb = min(first + (lane >> 1), nblk - 1);
+          const int jb = min(kScore ? max(first + (lane >> 1), blk0) : first + (lane >> 1),
+                             nblk - 1);
           int blk = __shfl_sync(0xffffffffu, ids, jb - id_base);
           if (leader) mbar_arrive_expect_tx(&bars->kv_full[st], kStageBytes);
           __syncwarp();
@@ -389,7 +421,8 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
               id_base = first;
               ids = id_base + lane < nblk ? __ldg(trow + id_base + lane) : 0;
             }
-            const int jb = min(first + (lane >> 1), nblk - 1);
+            const int jb = min(kScore ? max(first + (lane >> 1), blk0) : first + (lane >> 1),
+                             nblk - 1);
             int blk = __shfl_sync(0xffffffffu, ids, jb - id_base);
             if (leader) mbar_arrive_expect_tx(&bars->s8_full[st], kStage8Bytes);
             __syncwarp();
@@ -441,6 +474,20 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (leader) mbar_arrive(&bars->v_zeroed);
+          }
+        }
+        if (kScore && prod == 1 && head > 0) {
+          ok = wait(&bars->kv_full[0], 0);
+          if (ok) {
+            uint8_t* vbuf = sm + stage_off(0) + 2 * kKVHalf;
+            for (int e = lane; e < head * 16; e += 32) {
+              const int row = e / 16, c16 = e % 16;
+              *reinterpret_cast<uint4*>(vbuf + ((row >> 3) * 2 + (c16 >> 3)) * 1024 +
+                                        sw128(row & 7, c16 & 7)) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (leader) mbar_arrive(&bars->v_headed);
           }
         }
         // every TMA load issued must land before the CTA may exit.  A stage's key
@@ -505,7 +552,7 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
           const int bpt = kN / a.BS;
           const int b1 = min((jt0 + T) * bpt, nblk);
           int ev = -100000;
-          for (int b = jt0 * bpt + c * 32 + lane; b < b1; b += W * 32) {
+          for (int b = max(jt0 * bpt, blk0) + c * 32 + lane; b < b1; b += W * 32) {
             int blk = __ldg(trow + b);
             blk = (blk < 0 || blk >= a.num_blocks) ? 0 : blk;
             const float vs =
@@ -529,6 +576,7 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
           uint8_t* dst = sm + stage_off(st);
           const uint8_t* src = dst + 2 * kKVHalf;              // E4M3 K rows, then V rows
           const int valid = n - (jt0 + j) * kN;                // keys of the tile in the sequence
+          const int skip = j == 0 ? head : 0;                  // keys ahead of every query's
           // two groups a step (eight loads in flight a lane before the warp syncs)
 #pragma unroll 1
           for (int gr = g0; gr < g1; gr += 2) {
@@ -547,7 +595,8 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
             if (scaled) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const int jb = min((jt0 + j) * (kN / a.BS) + (row0 + 4 * h) / a.BS, nblk - 1);
+                int jb = min((jt0 + j) * (kN / a.BS) + (row0 + 4 * h) / a.BS, nblk - 1);
+                if (kScore) jb = max(jb, blk0);
                 int blk = __ldg(trow + jb);
                 blk = (blk < 0 || blk >= a.num_blocks) ? 0 : blk;
                 sv[h] = ldexpf(
@@ -560,7 +609,7 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
             convert(xk0, 1.f, false, o);
             store(dst, 0, row0, o);
             convert(xv0, sv[0], scaled, o);
-            if (row0 >= valid) {
+            if (row0 >= valid || (kScore && row0 < skip)) {
               // keys past the sequence end: zero V, so that P = 0 never meets NaN
 #pragma unroll
               for (int e = 0; e < 8; ++e) o[e] = 0u;
@@ -570,7 +619,7 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
               convert(xk1, 1.f, false, o);
               store(dst, 0, row1, o);
               convert(xv1, sv[1], scaled, o);
-              if (row1 >= valid) {
+              if (row1 >= valid || (kScore && row1 < skip)) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) o[e] = 0u;
               }
@@ -619,6 +668,7 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
             const int b = jl & 1;
             ok = wait(&bars->p_full[t][b], (jl >> 1) & 1);
             if (!kFp8 && ok && j == j_tail) ok = wait(&bars->v_zeroed, 0);
+            if (!kFp8 && kScore && ok && j == 0 && head > 0) ok = wait(&bars->v_headed, 0);
             if (!ok) break;
             tc_fence_after();
             if (leader) {
@@ -654,6 +704,14 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
     const bool live = tok < a.q_len;
     // this query's last visible key: causal within the chunk, or its prefix length
     const int pos = casc ? (live ? __ldg(a.key_limit + tok) : 0) - 1 : n - a.q_len + tok;
+    // scored: the row's keys, its slope and cap in log2 units
+    KeyRange keys{0, 0};
+    float slope = 0.f, cap_in = 0.f;
+    if constexpr (kScore) {
+      if (live) keys = key_range(a, s, n, tok);
+      if (a.slopes) slope = __ldg(a.slopes + hkv * G + g) * kLog2e;
+      cap_in = fabsf(a.cap_in) * pow2i(-q_e);
+    }
     const int my_tiles = tiles[t];
     // Q carries the sign; 2^-q_e undoes the row's f16 prescale (E4M3 pools)
     float qs = fabsf(a.qk_scale_log2) * pow2i(-q_e);
@@ -687,9 +745,10 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
         // issued before the wait for S, so the loads overlap it
 #pragma unroll
         for (int g4 = 0; g4 < 4; ++g4) {
-          int blk = __ldg(trow + min((kpos0 + 16 * g4) / a.BS, nblk - 1));
+          const int jb = min((kpos0 + 16 * g4) / a.BS, nblk - 1);
+          int blk = __ldg(trow + (kScore ? max(jb, blk0) : jb));
           blk = (blk < 0 || blk >= a.num_blocks) ? 0 : blk;
-          qsb[g4] = qs * __ldg(a.block_scales + ((size_t)blk * 2 * a.L + a.layer) * a.Hkv + hkv);
+          qsb[g4] = (kScore && a.cap_in != 0.f ? cap_in : qs) * __ldg(a.block_scales + ((size_t)blk * 2 * a.L + a.layer) * a.Hkv + hkv);
         }
       }
       if (!wait(&bars->s_full[t][b], (jl >> 1) & 1)) {
@@ -705,7 +764,34 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
       float mp[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) mp[e] = -INFINITY;
-      if (__all_sync(0xffffffffu, live && kpos0 + kN - 1 <= pos)) {
+      if constexpr (kScore) {
+        // to log2 units: scale or cap, distance, mask
+        if (a.cap_in != 0.f) {
+#pragma unroll
+          for (int c = 0; c < kN; ++c)
+            sv[c] = a.cap_out * tanh_score(sv[c] * (bscaled ? qsb[c >> 4] : cap_in));
+        } else {
+#pragma unroll
+          for (int c = 0; c < kN; ++c) sv[c] *= qsb[c >> 4];
+        }
+        if (a.slopes) {
+          const float d0 = (float)(pos - kpos0);
+#pragma unroll
+          for (int c = 0; c < kN; ++c) sv[c] = fmaf(-slope, fabsf(d0 - (float)c), sv[c]);
+        }
+        if (!__all_sync(0xffffffffu, kpos0 >= keys.lo && kpos0 + kN <= keys.hi)) {
+          const int c0 = keys.lo - kpos0, c1 = keys.hi - kpos0;
+#pragma unroll
+          for (int c = 0; c < kN; ++c) sv[c] = c >= c0 && c < c1 ? sv[c] : -INFINITY;
+        }
+#pragma unroll
+        for (int c = 0; c < kN; c += 2) {
+          const int e = 2 * (c >> 4) + ((c >> 1) & 1);
+          mp[e] = fmax3(mp[e], sv[c], sv[c + 1]);
+        }
+#pragma unroll
+        for (int g4 = 0; g4 < 4; ++g4) qsb[g4] = 1.f;
+      } else if (__all_sync(0xffffffffu, live && kpos0 + kN - 1 <= pos)) {
         // the warp's rows see every key of the tile: no mask
 #pragma unroll
         for (int c = 0; c < kN; c += 2) {
@@ -768,7 +854,8 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
           const int c = q4 * 16 + 2 * c2;
           // p = 2^(s * scale - ref): one FMA per two keys and the SFU per key
           float x0, x1;
-          f2_unpack(ffma2(f2_pack(sv[c], sv[c + 1]), qs2, nref2), x0, x1);
+          const uint64_t sv2 = f2_pack(sv[c], sv[c + 1]);
+          f2_unpack(kScore ? fadd2(sv2, nref2) : ffma2(sv2, qs2, nref2), x0, x1);
           const float p0 = ex2_ftz(x0), p1 = ex2_ftz(x1);
           const uint64_t p2 = f2_pack(p0, p1);
           pp[c2 & 3] = fadd2(pp[c2 & 3], p2);
@@ -863,10 +950,10 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
 template <int KVT>
 size_t smem_bytes_t() { return PfCfg<KVT>::kSmemBytes + sizeof(Bars) + kAlignSlack; }
 
-template <int KVT>
+template <int KVT, bool kScore>
 cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, dim3 grid, cudaStream_t stream) {
   const size_t smem = smem_bytes_t<KVT>();
-  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<KVT>,
+  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<KVT, kScore>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -879,7 +966,7 @@ cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, dim3 grid, cud
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<KVT>, *map, a);
+  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<KVT, kScore>, *map, a);
 }
 
 bool prefill_tc_supported(int kv_dtype, int q_dtype, int BS, int D, int G) {
@@ -890,7 +977,8 @@ bool prefill_tc_supported(int kv_dtype, int q_dtype, int BS, int D, int G) {
          kM % G == 0;
 }
 
-cudaError_t launch_prefill_tc(const CUtensorMap* map, const DecodeArgs& a, cudaStream_t stream) {
+template <bool kScore>
+static cudaError_t launch_chunk(const CUtensorMap* map, const DecodeArgs& a, cudaStream_t stream) {
   const int QT = kM / a.G;
   const int qtiles = (a.q_len + QT - 1) / QT;
   if (qtiles == 0 || a.B == 0) return cudaSuccess;
@@ -900,15 +988,25 @@ cudaError_t launch_prefill_tc(const CUtensorMap* map, const DecodeArgs& a, cudaS
   dim3 grid(a.Hkv, a.key_limit ? a.S : a.B, pairs);
   cudaError_t e;
   switch (a.kv_dtype) {
-    case PKV_BF16: e = launch_t<PKV_BF16>(map, a, grid, stream); break;
-    case PKV_F16: e = launch_t<PKV_F16>(map, a, grid, stream); break;
-    case PKV_FP8_E4M3: e = launch_t<PKV_FP8_E4M3>(map, a, grid, stream); break;
+    case PKV_BF16: e = launch_t<PKV_BF16, kScore>(map, a, grid, stream); break;
+    case PKV_F16: e = launch_t<PKV_F16, kScore>(map, a, grid, stream); break;
+    case PKV_FP8_E4M3: e = launch_t<PKV_FP8_E4M3, kScore>(map, a, grid, stream); break;
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;
   e = cudaGetLastError();
   if (e == cudaSuccess) count_launch();
   return e;
+}
+
+cudaError_t launch_prefill_tc(const CUtensorMap* map, const DecodeArgs& a, cudaStream_t stream) {
+  return launch_chunk<false>(map, a, stream);
+}
+
+cudaError_t launch_prefill_tc_scored(const CUtensorMap* map, const DecodeArgs& a,
+                                     cudaStream_t stream) {
+  if (a.key_limit) return cudaErrorInvalidValue;
+  return launch_chunk<true>(map, a, stream);
 }
 
 }  // namespace pkv

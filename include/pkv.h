@@ -577,6 +577,41 @@ PKV_API int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, cons
 PKV_API size_t paged_decode_scored_workspace_bytes(const pkv_geometry* geom, int batch, int q_len,
                                                    int max_seq_len, int with_weights);
 
+/* ---------------------------------------------------------------- eviction */
+
+/* Keep a long cache in a budget: of every sequence's n = d_seq_lens[s] tokens each KV
+ * head of `layer` keeps k = min(n, d_keep[s]): the last r = min(recent, k), and of the
+ * n - r others the k - r with the largest accumulated weight (NaN and values below 0
+ * count as 0; the lowest slots first among equals).  The kept tokens' K and V are copied
+ * into the blocks of d_new_tables, slot t taking the t-th kept token in the order of
+ * their slots, so each head may keep other tokens under one table.  With w = weights:
+ *   new_weights[s, h, t] = w[s, h, j_t] for t < k, 0 for k <= t < new_width
+ *   d_index[s, h, t] = j_t, the slot it had (int32 [batch, num_kv_heads, index_width];
+ *   NULL: not wanted; columns from k on are left as they were)
+ *   d_new_lens[s] = k
+ * The old blocks are only read: afterwards free them (kv_pool_free) and go on with the
+ * new table and length.  Every layer is evicted by a call of its own, into the same new
+ * blocks.  The new blocks are taken from the pool (kv_pool_alloc) and must not be blocks
+ * of d_tables (of any sequence) or twice in d_new_tables; new_weights must not overlap
+ * weights.  Keys keep the rotation of their old positions, and the calls that go by
+ * distance (window, slopes, prefixes, documents) then count slots.
+ * new_width columns of new_weights and index_width of d_index must hold what is kept: a
+ * sequence that would keep more than they or max_new_blocks * block_size tokens keeps
+ * that many and records PKV_EBOUNDS, as does a length outside [0, max_seq_len] (limited
+ * to it), a d_keep below 0 (taken as 0) or a block id outside the pool (the token is not
+ * copied).  weights have rows of max_seq_len columns or more.  d_workspace:
+ * kv_evict_workspace_bytes bytes (0 with d_index), 16-byte aligned.  E4M3 pools with
+ * block scales attached: PKV_EUNSUPPORTED (a token cannot leave its block's scale).
+ * PKV_EINVAL for NULL pointers, sizes below 0 and overlapping rows of new_weights. */
+PKV_API int kv_evict(pkv_pool* pool, int layer, const int32_t* d_new_tables, int max_new_blocks,
+                     const int32_t* d_tables, int max_blocks_per_seq, const int32_t* d_seq_lens,
+                     int batch, int max_seq_len, const int32_t* d_keep, int recent,
+                     const pkv_weights* weights, const pkv_weights* new_weights, int new_width,
+                     int32_t* d_new_lens, int32_t* d_index, int index_width, void* d_workspace,
+                     size_t ws_bytes, cudaStream_t stream);
+/* Workspace bytes of kv_evict without d_index. */
+PKV_API size_t kv_evict_workspace_bytes(const pkv_geometry* geom, int batch, int max_seq_len);
+
 /* Log-sum-exp merge of partial results ([SEQPAR] incremental softmax,
  * [ENG26] 3.1): for each row r = (s, h) of batch x num_q_heads,
  *   M = max_p lse[r,p],  w_p = exp(lse[r,p] - M),

@@ -1,5 +1,6 @@
 // pkv_tensors.cpp -- torch tensors checked and handed to the rotary, append,
-// verification and scored attention calls of include/pkv.h, as a CPython module.
+// verification, scored attention and eviction calls of include/pkv.h, as a CPython
+// module.
 //
 // These calls run a few microseconds on the device, so the host's share is what a
 // decode step waits for.  Reading a tensor's device, type, sizes, strides and
@@ -406,6 +407,61 @@ PyObject* attend_scored_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// evict(pool handle, pool storage, layer, new_tables, tables, seq_lens, max_seq_len, keep,
+//       recent, weights, new_weights, new_lens, index, workspace, stream)
+PyObject* evict_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 15, [&]() -> PyObject* {
+    pkv_pool* pool = address<pkv_pool>(a[0], "pool");
+    Call c;
+    c.output(a[1], "pool");
+    const int layer = small(a[2], "layer");
+    const at::Tensor* fresh = c.tensor(a[3], "new_tables");
+    const at::Tensor* tables = c.tensor(a[4], "tables");
+    const at::Tensor* lens = c.tensor(a[5], "seq_lens");
+    const int most = small(a[6], "max_seq_len");
+    const at::Tensor* keep = c.tensor(a[7], "keep");
+    const int recent = small(a[8], "recent");
+    const at::Tensor& weights = *c.tensor(a[9], "weights");
+    const at::Tensor& kept = *c.output(a[10], "new_weights");
+    const at::Tensor* new_lens = c.output(a[11], "new_lens");
+    const at::Tensor* index = c.output(a[12], "index", true);
+    const at::Tensor* ws = c.tensor(a[13], "workspace", true);
+    pkv_geometry g;
+    if (kv_pool_geometry(pool, &g) != PKV_OK) throw Bad("pool: not open");
+    for (const at::Tensor* t : {tables, fresh})
+      if (t->dim() != 2 || t->size(0) > INT32_MAX || t->size(1) > INT32_MAX)
+        throw Bad("tables and new_tables: [batch, blocks] are needed, got " +
+                  shape_text(t->sizes()));
+    const int64_t B = tables->size(0);
+    const int W = static_cast<int>(tables->size(1)), F = static_cast<int>(fresh->size(1));
+    const int32_t* tab = c.flat<int32_t>(tables, "tables", at::kInt, B, W);
+    const int32_t* to = c.flat<int32_t>(fresh, "new_tables", at::kInt, B, F);
+    const int32_t* len = c.flat<int32_t>(lens, "seq_lens", at::kInt, B);
+    const int32_t* budget = c.flat<int32_t>(keep, "keep", at::kInt, B);
+    int32_t* out_len = c.flat<int32_t>(new_lens, "new_lens", at::kInt, B);
+    const pkv_weights w = c.weights(weights, "weights", B, g.num_kv_heads, most);
+    const pkv_weights o = c.weights(kept, "new_weights", B, g.num_kv_heads, 0);
+    int64_t I = 0;
+    if (index) {
+      I = index->dim() == 3 ? index->size(2) : 0;
+      if (index->dim() != 3 || index->size(0) != B || index->size(1) != g.num_kv_heads ||
+          index->scalar_type() != at::kInt || !index->is_contiguous())
+        throw Bad("index: contiguous int32 " + shape_text({B, g.num_kv_heads}) +
+                  " rows are needed, got " + shape_text(index->sizes()));
+    }
+    if (I > INT32_MAX || kept.size(2) > INT32_MAX) throw Bad("new_weights, index: out of range");
+    if (ws && (ws->scalar_type() != at::kByte || !ws->is_contiguous()))
+      throw Bad("workspace: contiguous uint8 is needed");
+    return c.run(a[14], [&](cudaStream_t s) {
+      return kv_evict(pool, layer, to, F, tab, W, len, static_cast<int>(B), most, budget, recent,
+                      &w, &o, static_cast<int>(kept.size(2)), out_len,
+                      index ? static_cast<int32_t*>(index->data_ptr()) : nullptr,
+                      static_cast<int>(I), ws ? ws->data_ptr() : nullptr,
+                      ws ? static_cast<size_t>(ws->numel()) : 0, s);
+    });
+  });
+}
+
 #define PKV_METHOD(name, f) \
   {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
@@ -413,6 +469,7 @@ PyMethodDef methods[] = {
     PKV_METHOD("append_rope", append_rope_py),
     PKV_METHOD("verify_drafts", verify_drafts_py),
     PKV_METHOD("attend_scored", attend_scored_py),
+    PKV_METHOD("evict", evict_py),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "pkv_tensors", nullptr, -1, methods,

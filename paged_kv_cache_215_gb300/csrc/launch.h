@@ -189,6 +189,24 @@ struct VerifyArgs {
 };
 cudaError_t launch_verify(const VerifyArgs& a, int sms, cudaStream_t stream);
 
+struct EvictArgs {
+  uint8_t* pool;
+  const int32_t* tables;
+  const int32_t* new_tables;
+  const int32_t* seq_lens;
+  const int32_t* keep;
+  int32_t* new_lens;
+  int32_t* index;            // [B, Hkv, index_row]
+  int64_t index_row;
+  WeightRows w_in, w_out;
+  int width;                 // columns of w_out
+  int32_t* status;
+  int B, Hkv, BS, L, layer, max_blocks, max_new_blocks, num_blocks, row_bytes;
+  int max_len, recent;
+  int capacity;              // tokens the new tables, weights and index hold
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
+
 // Launch counter shared by every launcher.
 void count_launch();
 

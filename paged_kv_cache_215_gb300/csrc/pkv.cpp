@@ -1510,6 +1510,72 @@ int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* 
   return accumulate();
 }
 
+// ---------------------------------------------------------------- eviction
+
+size_t kv_evict_workspace_bytes(const pkv_geometry* g, int batch, int max_seq_len) {
+  if (!geometry_ok(g) || batch < 0 || max_seq_len < 0) return 0;
+  return align256((size_t)batch * g->num_kv_heads * max_seq_len * sizeof(int32_t));
+}
+
+int kv_evict(pkv_pool* p, int layer, const int32_t* d_new_tables, int max_new_blocks,
+             const int32_t* d_tables, int max_blocks_per_seq, const int32_t* d_seq_lens, int batch,
+             int max_seq_len, const int32_t* d_keep, int recent, const pkv_weights* weights,
+             const pkv_weights* new_weights, int new_width, int32_t* d_new_lens, int32_t* d_index,
+             int index_width, void* d_workspace, size_t ws_bytes, cudaStream_t stream) {
+  if (!p || layer < 0 || layer >= p->g.num_layers || batch < 0 || max_seq_len < 0 || recent < 0 ||
+      max_new_blocks < 0 || new_width < 0 || (d_index && index_width < 0))
+    return PKV_EINVAL;
+  const pkv_geometry& g = p->g;
+  if (batch == 0) return PKV_OK;
+  if (!d_tables || max_blocks_per_seq < 1 || !d_seq_lens || !d_keep || !d_new_lens ||
+      (max_new_blocks > 0 && !d_new_tables) || !weights || !new_weights ||
+      (long long)max_seq_len > (long long)max_blocks_per_seq * g.block_size)
+    return PKV_EINVAL;
+  const pkv_rows in{weights->data, weights->seq_stride, weights->head_stride};
+  const pkv_rows out{new_weights->data, new_weights->seq_stride, new_weights->head_stride};
+  if (!rows_ok(&in, PKV_F32) ||
+      !out_rows_ok(&out, PKV_F32, batch, g.num_kv_heads, std::max(new_width, 1)) ||
+      in.data == out.data)
+    return PKV_EINVAL;
+  if (p->d_block_scales || batch > 65535 || g.num_kv_heads > 65535) return PKV_EUNSUPPORTED;
+  EvictArgs a{};
+  const long long slots = (long long)max_new_blocks * g.block_size;
+  a.capacity = (int)std::min<long long>(std::min(slots, (long long)new_width),
+                                        d_index ? index_width : max_seq_len);
+  if (d_index) {
+    a.index = d_index;
+    a.index_row = index_width;
+  } else {
+    if (max_seq_len > 0 && (!d_workspace || !aligned16(d_workspace) ||
+                            ws_bytes < (size_t)batch * g.num_kv_heads * max_seq_len * 4))
+      return d_workspace && !aligned16(d_workspace) ? PKV_EINVAL : PKV_ENOMEM;
+    a.index = static_cast<int32_t*>(d_workspace);
+    a.index_row = max_seq_len;
+  }
+  a.pool = static_cast<uint8_t*>(p->d_pool);
+  a.tables = d_tables;
+  a.new_tables = d_new_tables;
+  a.seq_lens = d_seq_lens;
+  a.keep = d_keep;
+  a.new_lens = d_new_lens;
+  a.w_in = {weights->data, weights->seq_stride, weights->head_stride};
+  a.w_out = {new_weights->data, new_weights->seq_stride, new_weights->head_stride};
+  a.width = new_width;
+  a.status = p->d_status;
+  a.B = batch;
+  a.Hkv = g.num_kv_heads;
+  a.BS = g.block_size;
+  a.L = g.num_layers;
+  a.layer = layer;
+  a.max_blocks = max_blocks_per_seq;
+  a.max_new_blocks = max_new_blocks;
+  a.num_blocks = g.num_blocks;
+  a.row_bytes = g.head_dim * elem_bytes(g.kv_dtype);
+  a.max_len = max_seq_len;
+  a.recent = recent;
+  return launch_evict(a, stream) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
 int pkv_check_status(const pkv_pool* p, cudaStream_t stream) {
   if (!p) return PKV_EINVAL;
   if (cudaStreamSynchronize(stream) != cudaSuccess) return PKV_ECUDA;

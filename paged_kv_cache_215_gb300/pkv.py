@@ -134,6 +134,8 @@ def _load() -> ctypes.CDLL:
         "paged_decode_attention_scored": (I, [P, I, P, I, I, P, I, P, I, P, I, I, F, F, F,
                                               ctypes.POINTER(ScoreRules), W, W, P, Z, P]),
         "paged_decode_scored_workspace_bytes": (Z, [G, I, I, I, I]),
+        "kv_evict": (I, [P, I, P, I, P, I, P, I, I, P, I, W, W, I, P, P, I, P, Z, P]),
+        "kv_evict_workspace_bytes": (Z, [G, I, I]),
         "pkv_check_status": (I, [P, P]),
         "pkv_wait_selftest": (I, [P, P]),
         "pkv_strerror": (ctypes.c_char_p, [I]),
@@ -158,8 +160,8 @@ class _NoTensors:
 
 def _load_tensors():
     """The compiled module that checks and passes tensors of the short calls (rope_apply,
-    append_rope, verify_drafts, paged_decode_attention_scored); without it they raise, and
-    every other call works."""
+    append_rope, verify_drafts, paged_decode_attention_scored, evict); without it they
+    raise, and every other call works."""
     path = _build.BINDING
     if not os.path.exists(path):
         return _NoTensors(f"{path} is not built (it needs a torch for CUDA and Python's headers); "
@@ -190,6 +192,7 @@ EXPORTS = ("kv_pool_bytes", "kv_pool_create", "kv_pool_destroy", "kv_pool_geomet
            "pkv_rope_freqs", "pkv_rope_freqs_from", "rope_apply", "kv_append_rope",
            "verify_drafts",
            "paged_decode_attention_scored", "paged_decode_scored_workspace_bytes",
+           "kv_evict", "kv_evict_workspace_bytes",
            "pkv_check_status", "pkv_wait_selftest", "pkv_strerror", "pkv_launch_count")
 
 
@@ -427,6 +430,27 @@ class KVPool:
             raise PkvError(rc, "kv_append_rope")
         return q_out
 
+    def evict(self, layer, new_tables, tables, seq_lens, max_seq_len, keep, recent, weights,
+              new_weights, new_lens, index=None, workspace=None, stream=None):
+        """Each sequence's keep[s] (int32 [B]) tokens, the last `recent` and the heaviest by
+        weights [B, Hkv, >= max_seq_len] float32 of the others, per KV head, copied into
+        the blocks of new_tables [B, blocks] int32 (taken with alloc), in order.
+        new_weights [B, Hkv, any] takes their weights and zeros behind, new_lens [B] int32
+        the new lengths, index [B, Hkv, any] int32 the slots they had.  The old blocks are
+        only read; free them afterwards.  One call a layer, all into the same blocks."""
+        if workspace is None and index is None:
+            workspace = torch.empty(max(16, evict_workspace_bytes(self.geom, tables.shape[0],
+                                                                  max_seq_len)),
+                                    dtype=torch.uint8, device=self.storage.device)
+            if stream is not None:
+                workspace.record_stream(stream)
+        rc = _tensors.evict(self.handle.value if self.handle else 0, self.storage, layer,
+                            new_tables, tables, seq_lens, max_seq_len, keep, recent, weights,
+                            new_weights, new_lens, index, workspace, stream)
+        if rc:
+            raise PkvError(rc, "kv_evict")
+        return new_lens
+
     def set_block_scales(self, scales: Optional[torch.Tensor]):
         """Attach a [NB, 2, L, Hkv] float32 device tensor of per-tile E4M3 scales."""
         self.block_scales = scales
@@ -611,6 +635,10 @@ def scored_workspace_bytes(geom: Geometry, batch: int, q_len: int, max_seq_len: 
                            weights: bool = False) -> int:
     return int(_lib.paged_decode_scored_workspace_bytes(ctypes.byref(geom), batch, q_len,
                                                         max_seq_len, int(weights)))
+
+
+def evict_workspace_bytes(geom: Geometry, batch: int, max_seq_len: int) -> int:
+    return int(_lib.kv_evict_workspace_bytes(ctypes.byref(geom), batch, max_seq_len))
 
 
 _NO_RULES = Scores()

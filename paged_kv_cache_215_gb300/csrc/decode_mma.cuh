@@ -139,6 +139,14 @@ struct SmemHeader {
   volatile int abort_flag;
 };
 
+// A column of a scored call: its keys [from, lim], its query's position and slope (log2
+// units).
+struct ColumnRule {
+  int from, lim, at;
+  float slope;
+};
+constexpr int kMaxColumns = 16;
+
 // ---------------------------------------------------------------- consumer math
 //
 // A warp owns one KV head.  Its query rows are R = q_len * G (query token i,
@@ -162,11 +170,10 @@ struct Consumer {
   float acc[8][NT][4];     // O^T fragments: 8 tiles of 16 d x 8 rows, per n-tile
   float m[NT][2], l[NT][2];// running max (log2 units) and per-thread partial sums
   int lim[NT][2];          // last key position each of the thread's columns may see
-  // scored calls (positions count from the first token read): the first key of each
-  // column, its query's position and slope (log2 units), and over all columns the
-  // smallest and largest first and last keys
-  int from[kScore ? NT : 1][2], at[kScore ? NT : 1][2];
-  float slope[kScore ? NT : 1][2];
+  // scored calls (positions count from the first token read): the columns' rules (of
+  // this warp, in shared memory: registers are short and most blocks need none of them),
+  // and over all columns the smallest and largest first and last keys
+  ColumnRule* rules;
   int from_min, from_max, lim_min, lim_max;
   float cap_in_;
   float* score_rows;       // the unit's rows in a.scores, or nullptr
@@ -273,38 +280,28 @@ struct Consumer {
     }
   }
 
-  // The columns' keys, positions and slopes in a unit that reads n tokens.
+  // The columns' rules in a unit that reads n tokens.
   __device__ __forceinline__ void load_rules(const DecodeArgs& a, int s, int n, int hkv, int lane) {
-    const int c = lane & 3, len = scored_len(a, s), off = len - n;
-    from_min = lim_min = 0x7fffffff;
-    from_max = lim_max = -1;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = nt * 8 + 2 * c + h;
-        from[nt][h] = 0x7fffffff;              // a padding column sees no key
-        lim[nt][h] = -1;
-        at[nt][h] = 0;
-        slope[nt][h] = 0.f;
-        if (r >= a.R) continue;
-        const int i = r / a.G, g = r - i * a.G;
-        const KeyRange k = key_range(a, s, len, i);
-        if (k.lo < k.hi) {
-          from[nt][h] = k.lo - off;
-          lim[nt][h] = k.hi - 1 - off;
-        }
-        at[nt][h] = len - a.q_len + i - off;
-        if (a.slopes) slope[nt][h] = __ldg(a.slopes + hkv * a.G + g) * kLog2e;
-        from_min = min(from_min, from[nt][h]);
-        from_max = max(from_max, from[nt][h]);
-        lim_min = min(lim_min, lim[nt][h]);
-        lim_max = max(lim_max, lim[nt][h]);
+    const int len = scored_len(a, s), off = len - n;
+    ColumnRule r{0x7fffffff, -1, 0, 0.f};           // a column that sees no key
+    __syncwarp();                                   // the unit before has read its rules
+    if (lane < a.R) {
+      const int i = lane / a.G, g = lane - i * a.G;
+      const KeyRange k = key_range(a, s, len, i);
+      if (k.lo < k.hi) {
+        r.from = k.lo - off;
+        r.lim = k.hi - 1 - off;
       }
-    from_min = __reduce_min_sync(0xffffffffu, from_min);
-    from_max = __reduce_max_sync(0xffffffffu, from_max);
-    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
-    lim_max = __reduce_max_sync(0xffffffffu, lim_max);
+      r.at = len - a.q_len + i - off;
+      if (a.slopes) r.slope = __ldg(a.slopes + hkv * a.G + g) * kLog2e;
+    }
+    if (lane < kMaxColumns) rules[lane] = r;
+    const bool live = lane < a.R;
+    from_min = __reduce_min_sync(0xffffffffu, r.from);
+    from_max = __reduce_max_sync(0xffffffffu, live ? r.from : -1);
+    lim_min = __reduce_min_sync(0xffffffffu, live ? r.lim : 0x7fffffff);
+    lim_max = __reduce_max_sync(0xffffffffu, r.lim);
+    __syncwarp();
     score_rows = a.scores ? a.scores + (((int64_t)s * a.Hkv + hkv) * a.max_len + off) * a.score_row
                           : nullptr;
   }
@@ -313,41 +310,31 @@ struct Consumer {
   __device__ __forceinline__ void apply_rules(const DecodeArgs& a, float (&s)[kTiles][NT][4],
                                               float ks_b, int jbase, int valid, bool full,
                                               int lane) {
-    const int t0 = jbase + (lane >> 2);
-    const float qs = qk_scale_log2_ * ks_b, ci = cap_in_ * ks_b;
-#pragma unroll
-    for (int mt = 0; mt < kTiles; ++mt)
+    const int c = lane & 3, t0 = jbase + (lane >> 2);
+    float* flat = &s[0][0][0];
+    if (a.cap_in != 0.f) {
+      scale_scores<kTiles * NT * 4>(flat, cap_in_ * ks_b);
+      cap_scores<kTiles * NT * 4>(flat, a.cap_out);
+    } else {
+      scale_scores<kTiles * NT * 4>(flat, qk_scale_log2_ * ks_b);
+    }
+    if (a.slopes || !full) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float& x = s[mt][nt][k];
-          x = a.cap_in != 0.f ? a.cap_out * tanh_score(x * ci) : x * qs;
+        for (int h = 0; h < 2; ++h) {
+          const ColumnRule r = rules[nt * 8 + 2 * c + h];
+#pragma unroll
+          for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+            for (int k = h; k < 4; k += 2) {
+              const int t = t0 + mt * 16 + ((k >> 1) << 3);
+              s[mt][nt][k] = fmaf(-r.slope, (float)abs(r.at - t), s[mt][nt][k]);
+              if (t < r.from || t > r.lim) s[mt][nt][k] = -INFINITY;
+            }
         }
-    if (a.slopes) {
-#pragma unroll
-      for (int mt = 0; mt < kTiles; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int t = t0 + mt * 16 + ((k >> 1) << 3);
-            s[mt][nt][k] = fmaf(-slope[nt][k & 1], (float)abs(at[nt][k & 1] - t), s[mt][nt][k]);
-          }
-    }
-    if (!full) {
-#pragma unroll
-      for (int mt = 0; mt < kTiles; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int t = t0 + mt * 16 + ((k >> 1) << 3);
-            if (t < from[nt][k & 1] || t > lim[nt][k & 1]) s[mt][nt][k] = -INFINITY;
-          }
     }
     if (score_rows) {
-      const int c = lane & 3;
 #pragma unroll
       for (int mt = 0; mt < kTiles; ++mt)
 #pragma unroll
@@ -1165,7 +1152,10 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
   constexpr bool kScore = kMode == kScored;
   Consumer<KVT, BS, NT, kCausal, kScore> cons;
   cons.qk_scale_log2_ = a.qk_scale_log2;
-  if constexpr (kScore) cons.cap_in_ = a.cap_in;
+  if constexpr (kScore) {
+    cons.cap_in_ = a.cap_in;
+    cons.rules = reinterpret_cast<ColumnRule*>(hdr + 1) + warp * kMaxColumns;
+  }
   cons.bscaled_ = T::kFp8 && a.block_scales != nullptr;
   cons.reset();
   const int w = warp;
@@ -1264,7 +1254,9 @@ cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, int gx, int gy
                      cudaStream_t stream) {
   // the ring needs mma_smem_bytes; a larger request (a.smem_bytes) caps how many
   // CTAs can share an SM
-  const size_t smem = std::max(mma_smem_bytes(KVT, BS, a.HG, a.stages), (size_t)a.smem_bytes);
+  const size_t rules = kMode == kScored ? a.HG * kMaxColumns * sizeof(ColumnRule) : 0;
+  const size_t smem = std::max(mma_smem_bytes(KVT, BS, a.HG, a.stages) + rules,
+                               (size_t)a.smem_bytes);
   auto kern = decode_mma_kernel<KVT, BS, NT, kCausal, kMode>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;

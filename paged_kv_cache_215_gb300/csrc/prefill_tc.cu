@@ -110,38 +110,6 @@ static_assert(PfCfg<PKV_FP8_E4M3>::kSmemBytes + sizeof(Bars) + kAlignSlack <= 22
 static_assert(PfCfg<PKV_FP8_E4M3>::kThreads <= 512, "threads");
 static_assert(PfCfg<PKV_BF16>::kThreads <= 512, "threads");
 
-// Two FP32 lanes in one 64-bit register, for the f32x2 instructions (each lane
-// rounds exactly as the scalar instruction does).
-__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t fsub2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-// max of three (one instruction)
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 __device__ __forceinline__ uint32_t sw128(int row, int chunk) {
   return (uint32_t)row * 128u + ((uint32_t)(chunk ^ (row & 7)) << 4);
 }
@@ -766,14 +734,10 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
       for (int e = 0; e < 8; ++e) mp[e] = -INFINITY;
       if constexpr (kScore) {
         // to log2 units: scale or cap, distance, mask
-        if (a.cap_in != 0.f) {
 #pragma unroll
-          for (int c = 0; c < kN; ++c)
-            sv[c] = a.cap_out * tanh_score(sv[c] * (bscaled ? qsb[c >> 4] : cap_in));
-        } else {
-#pragma unroll
-          for (int c = 0; c < kN; ++c) sv[c] *= qsb[c >> 4];
-        }
+        for (int g4 = 0; g4 < 4; ++g4)
+          scale_scores<16>(sv + 16 * g4, bscaled || a.cap_in == 0.f ? qsb[g4] : cap_in);
+        if (a.cap_in != 0.f) cap_scores<kN>(sv, a.cap_out);
         if (a.slopes) {
           const float d0 = (float)(pos - kpos0);
 #pragma unroll

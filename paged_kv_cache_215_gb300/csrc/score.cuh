@@ -69,4 +69,42 @@ __device__ __forceinline__ float tanh_score(float x) {
   return fabsf(x) < 0.6f ? fmaf(x * z, p, x) : big;
 }
 
+// x[i] = cap_out tanh(x[i]) of N scores a thread (N even); whole warps.  While no score
+// of the warp is above 1 in magnitude (scores within the cap) one polynomial in x^2, two
+// scores an instruction, serves them all (2^-24 before rounding, 2^-22.5 with it): 4.5
+// instructions a score, none of them on the special-function unit that the softmax's
+// exponentials need, against 15 for tanh_score.
+template <int N>
+__device__ __forceinline__ void cap_scores(float* x, float cap_out) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) top = fmax3(top, fabsf(x[i]), fabsf(x[i + 1]));
+  if (__all_sync(0xffffffffu, top <= 1.f)) {
+    const float c[7] = {1.f, -0x1.55546cp-2f, 0x1.10ecc4p-3f, -0x1.b642ecp-5f,
+                        0x1.4d9306p-6f, -0x1.9a364ap-8f, 0x1.156af0p-10f};
+    uint64_t c2[7];
+#pragma unroll
+    for (int k = 0; k < 7; ++k) c2[k] = f2_pack(c[k] * cap_out, c[k] * cap_out);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint64_t v = f2_pack(x[i], x[i + 1]), z = fmul2(v, v);
+      uint64_t p = c2[6];
+#pragma unroll
+      for (int k = 5; k >= 0; --k) p = ffma2(p, z, c2[k]);
+      f2_unpack(fmul2(v, p), x[i], x[i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = cap_out * tanh_score(x[i]);
+  }
+}
+
+// x[i] *= f, two a time.
+template <int N>
+__device__ __forceinline__ void scale_scores(float* x, float f) {
+  const uint64_t f2 = f2_pack(f, f);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) f2_unpack(fmul2(f2_pack(x[i], x[i + 1]), f2), x[i], x[i + 1]);
+}
+
 }  // namespace pkv

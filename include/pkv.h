@@ -287,7 +287,8 @@ typedef struct {
  * head_dim <= 512, rotary_dim <= head_dim.  Asynchronous on `stream`;
  * PKV_EINVAL for NULL or misaligned pointers (to the element size), negative counts or
  * strides, overlapping output rows, a bad rotation, or more than 65535 heads.
- * rope_apply, kv_append_rope and verify_drafts are launched with programmatic dependent
+ * rope_apply, kv_append_rope, verify_drafts, paged_decode_attention_scored (up to 16
+ * query rows per KV head) and kv_evict are launched with programmatic dependent
  * launch: a call is scheduled while the launch before it finishes and waits for it (and
  * all before) ahead of any access, so it runs as any call in the stream does. */
 PKV_API int rope_apply(const pkv_rows* q_out, const pkv_rows* q, int num_q_heads,
@@ -561,8 +562,7 @@ typedef struct {
  * d_workspace: paged_decode_scored_workspace_bytes bytes, 16-byte aligned; with weights
  * it holds every score of the call (4 bytes for each query row and token).
  * Kernels, types and shapes as in paged_decode_attention_mq with num_splits = 0;
- * weights take up to 16 query rows per KV head (8 at block size 64), else
- * PKV_EUNSUPPORTED.  PKV_EINVAL also for a cap or window below 0, a cap that is not
+ * weights take up to 16 query rows per KV head, else PKV_EUNSUPPORTED.  PKV_EINVAL also for a cap or window below 0, a cap that is not
  * finite, and scale / cap not finite in fp32. */
 PKV_API int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* d_q,
                                           pkv_dtype q_dtype, int q_len, const pkv_pool* pool,

@@ -33,6 +33,11 @@ bool mma_supported(int kv_dtype, int BS, int D, int G, int q_len) {
          (R <= 8 || BS <= 32);
 }
 
+bool mma_scored_supported(int kv_dtype, int BS, int D, int G, int q_len) {
+  return (kv_dtype == PKV_BF16 || kv_dtype == PKV_F16 || kv_dtype == PKV_FP8_E4M3) &&
+         (BS == 16 || BS == 32 || BS == 64) && D == kD && G >= 1 && (long long)G * q_len <= 16;
+}
+
 cudaError_t launch_decode_mma(const CUtensorMap* map, const DecodeArgs& a, int gx, int gy,
                               cudaStream_t stream) {
   if (a.stages < 2 || a.stages > 16 || a.HG < 1 || a.HG > kMaxHG) return cudaErrorInvalidValue;
@@ -48,7 +53,7 @@ cudaError_t launch_decode_mma(const CUtensorMap* map, const DecodeArgs& a, int g
 cudaError_t launch_decode_mma_scored(const CUtensorMap* map, const DecodeArgs& a, int gx,
                                      cudaStream_t stream) {
   if (a.stages < 2 || a.stages > 16 || a.HG < 1 || a.HG > kMaxHG) return cudaErrorInvalidValue;
-  if (a.R < 1 || a.R > 16 || (a.R > 8 && a.BS == 64)) return cudaErrorInvalidValue;
+  if (a.R < 1 || a.R > 16) return cudaErrorInvalidValue;
   switch (a.kv_dtype) {
     case PKV_BF16: return launch_decode_score_bf16(map, a, gx, stream);
     case PKV_F16: return launch_decode_score_f16(map, a, gx, stream);

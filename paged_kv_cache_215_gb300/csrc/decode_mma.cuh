@@ -145,7 +145,7 @@ struct ColumnRule {
   int from, lim, at;
   float slope;
 };
-constexpr int kMaxColumns = 16;
+constexpr int kWarpColumns = 8;
 
 // ---------------------------------------------------------------- consumer math
 //
@@ -174,6 +174,7 @@ struct Consumer {
   // this warp, in shared memory: registers are short and most blocks need none of them),
   // and over all columns the smallest and largest first and last keys
   ColumnRule* rules;
+  int col0;                // the first of the warp's 8 columns (a warp for each 8 rows)
   int from_min, from_max, lim_min, lim_max;
   float cap_in_;
   float* score_rows;       // the unit's rows in a.scores, or nullptr
@@ -214,6 +215,12 @@ struct Consumer {
   }
 
 
+  // The query row of one of the warp's columns.
+  __device__ __forceinline__ int column(int r) const {
+    if constexpr (kScore) return col0 + r;
+    return r;
+  }
+
   // q row of column r (query token r / G, head r % G of this KV head), -1 if padding.
   __device__ __forceinline__ static long long q_row(const DecodeArgs& a, int s, int hkv, int r) {
     if (r >= a.R) return -1;
@@ -234,7 +241,7 @@ struct Consumer {
       float amax = 0.f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const long long qr = q_row(a, s, hkv, nt * 8 + (lane >> 2));
+        const long long qr = q_row(a, s, hkv, column(nt * 8 + (lane >> 2)));
         if (qr < 0) continue;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
@@ -251,7 +258,7 @@ struct Consumer {
     if constexpr (kScore) load_rules(a, s, n, hkv, lane);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const long long qr = q_row(a, s, hkv, nt * 8 + (lane >> 2));
+      const long long qr = q_row(a, s, hkv, column(nt * 8 + (lane >> 2)));
       const bool live = qr >= 0;
       const size_t row = (size_t)(live ? qr : 0) * kD;
 #pragma unroll
@@ -268,13 +275,14 @@ struct Consumer {
         } else {
           const uint32_t* qp = reinterpret_cast<const uint32_t*>(
               static_cast<const uint16_t*>(a.q) + row + 16 * kk + 2 * c);
-          qf[nt][kk][0] = live ? __ldg(qp) : 0u;
-          qf[nt][kk][1] = live ? __ldg(qp + 4) : 0u;
+          // (scored launches may be scheduled before q is written: plain loads)
+          qf[nt][kk][0] = !live ? 0u : kScore ? qp[0] : __ldg(qp);
+          qf[nt][kk][1] = !live ? 0u : kScore ? qp[4] : __ldg(qp + 4);
         }
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = nt * 8 + 2 * c + h;           // the thread's accumulator columns
+        const int r = column(nt * 8 + 2 * c + h);   // the thread's accumulator columns
         if constexpr (kCausal && !kScore) lim[nt][h] = r < a.R ? n - a.q_len + r / a.G : n - 1;
       }
     }
@@ -285,25 +293,27 @@ struct Consumer {
     const int len = scored_len(a, s), off = len - n;
     ColumnRule r{0x7fffffff, -1, 0, 0.f};           // a column that sees no key
     __syncwarp();                                   // the unit before has read its rules
-    if (lane < a.R) {
-      const int i = lane / a.G, g = lane - i * a.G;
+    const int row = col0 + lane;
+    const bool live = lane < 8 && row < a.R;
+    if (live) {
+      const int i = row / a.G, g = row - i * a.G;
       const KeyRange k = key_range(a, s, len, i);
       if (k.lo < k.hi) {
         r.from = k.lo - off;
         r.lim = k.hi - 1 - off;
       }
       r.at = len - a.q_len + i - off;
-      if (a.slopes) r.slope = __ldg(a.slopes + hkv * a.G + g) * kLog2e;
+      if (a.slopes) r.slope = a.slopes[hkv * a.G + g] * kLog2e;
     }
-    if (lane < kMaxColumns) rules[lane] = r;
-    const bool live = lane < a.R;
+    if (lane < 8) rules[lane] = r;
     from_min = __reduce_min_sync(0xffffffffu, r.from);
     from_max = __reduce_max_sync(0xffffffffu, live ? r.from : -1);
     lim_min = __reduce_min_sync(0xffffffffu, live ? r.lim : 0x7fffffff);
     lim_max = __reduce_max_sync(0xffffffffu, r.lim);
     __syncwarp();
-    score_rows = a.scores ? a.scores + (((int64_t)s * a.Hkv + hkv) * a.max_len + off) * a.score_row
-                          : nullptr;
+    score_rows = nullptr;
+    if (a.scores)
+      score_rows = a.scores + (((int64_t)s * a.Hkv + hkv) * a.max_len + off) * a.score_row + col0;
   }
 
   // Scores of a block into log2 units: cap, distance, mask, record (score.cuh).
@@ -344,9 +354,12 @@ struct Consumer {
           float* row = score_rows + (int64_t)(jbase + t) * a.score_row;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            if (nt * 8 + 2 * c < a.score_row)
+            if (a.score_row == 1) {
+              if (c == 0) row[0] = s[mt][nt][k];
+            } else if (col0 + nt * 8 + 2 * c < a.score_row) {
               *reinterpret_cast<float2*>(row + nt * 8 + 2 * c) =
                   make_float2(s[mt][nt][k], s[mt][nt][k + 1]);
+            }
         }
     }
   }
@@ -871,7 +884,7 @@ struct Consumer {
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = nt * 8 + 2 * c + h;
+        const int r = column(nt * 8 + 2 * c + h);
         const long long qr = q_row(a, s, hkv, r);
         if (qr < 0) continue;
         // a column that saw no key (a query before the sequence start) is empty
@@ -934,6 +947,12 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
     fence_mbar_init();
   }
   if (warp == producer && lane == 0) prefetch_tensormap(&tmap);
+  if constexpr (kMode == kScored) {
+    // scheduled while the launches ahead finish; the fence puts their writes to the pool
+    // ahead of this grid's TMA reads
+    grid_dependency_wait();
+    fence_proxy_async_global();
+  }
 
   if (a.mode == 0 && warp == 0) {
     long long total = 0;
@@ -1048,7 +1067,8 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
           jo = first_token(a, cur.s, min(max(__ldg(a.seq_lens + cur.s), 0), a.max_blocks * BS)) /
                BS;
         if constexpr (kMode == kScored) jo = (scored_len(a, cur.s) - cur.n) / BS;
-        ids = jj < cur.nb ? __ldg(a.tables + (size_t)cur.s * a.max_blocks + jo + jj) : 0;
+        const int32_t* entry = a.tables + (size_t)cur.s * a.max_blocks + jo + jj;
+        ids = jj >= cur.nb ? 0 : kMode == kScored ? *entry : __ldg(entry);
       }
       int blk = __shfl_sync(0xffffffffu, ids, cur.j - id_base);
       const bool blk_ok = blk >= 0 && blk < a.num_blocks;
@@ -1146,7 +1166,9 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
     return;
   }
 
-  if (warp >= a.HG) return;   // no spare warps are launched; guard anyway
+  // a scored call has a consumer warp for every 8 query rows of a KV head, else one
+  const int row_warps = kMode == kScored ? (a.R + kWarpColumns - 1) / kWarpColumns : 1;
+  if (warp >= a.HG * row_warps) return;   // no spare warps are launched; guard anyway
 
   // ---------------------------------------------------------------- consumers
   constexpr bool kScore = kMode == kScored;
@@ -1154,11 +1176,12 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
   cons.qk_scale_log2_ = a.qk_scale_log2;
   if constexpr (kScore) {
     cons.cap_in_ = a.cap_in;
-    cons.rules = reinterpret_cast<ColumnRule*>(hdr + 1) + warp * kMaxColumns;
+    cons.rules = reinterpret_cast<ColumnRule*>(hdr + 1) + warp * kWarpColumns;
+    cons.col0 = warp % row_warps * kWarpColumns;
   }
   cons.bscaled_ = T::kFp8 && a.block_scales != nullptr;
   cons.reset();
-  const int w = warp;
+  const int w = warp / row_warps;          // KV head of the group
   bool waited = false;
   int hkv = cur.hg * a.HG + w;
   if (cur.remaining > 0) cons.load_q(a, cur.s, cur.n, hkv, lane);
@@ -1181,8 +1204,9 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
   }
 
   // a shared-prefix decode merges every row with its prefix partials, and a call
-  // that returns each row's log-sum-exp has the merge write every row
-  const bool whole_ok = a.ext_lse == nullptr && a.out_lse == nullptr;
+  // that returns each row's log-sum-exp, or records weights by it, has the merge write
+  // every row
+  const bool whole_ok = a.ext_lse == nullptr && a.out_lse == nullptr && a.scores == nullptr;
   int stage = 0;
   uint32_t round = 0;
   while (cur.remaining > 0) {
@@ -1226,7 +1250,7 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
       if (a.mode == 0) {
         whole = first && unit_end && whole_ok;
         slot = (long long)blockIdx.x + u;
-        if (first && w == 0 && lane == 0) {
+        if (first && warp == 0 && lane == 0) {
           const long long unit_first_gb = cur.gb - cur.j;
           const long long parts = hdr->total < (long long)gridDim.x ? hdr->total : (long long)gridDim.x;
           const long long c_last = owner_of(unit_first_gb + cur.nb - 1, hdr->total, parts);
@@ -1254,7 +1278,10 @@ cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, int gx, int gy
                      cudaStream_t stream) {
   // the ring needs mma_smem_bytes; a larger request (a.smem_bytes) caps how many
   // CTAs can share an SM
-  const size_t rules = kMode == kScored ? a.HG * kMaxColumns * sizeof(ColumnRule) : 0;
+  const int consumers =
+      kMode == kScored ? a.HG * ((a.R + kWarpColumns - 1) / kWarpColumns) : a.HG;
+  if (consumers > kMaxHG) return cudaErrorInvalidValue;
+  const size_t rules = kMode == kScored ? consumers * kWarpColumns * sizeof(ColumnRule) : 0;
   const size_t smem = std::max(mma_smem_bytes(KVT, BS, a.HG, a.stages) + rules,
                                (size_t)a.smem_bytes);
   auto kern = decode_mma_kernel<KVT, BS, NT, kCausal, kMode>;
@@ -1262,14 +1289,15 @@ cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, int gx, int gy
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(gx, gy);
-  cfg.blockDim = dim3(32 * (a.HG + 1));
+  cfg.blockDim = dim3(32 * (consumers + 1));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = a.pdl ? 1 : 0;
+  // (a scored launch waits for the launches ahead before it reads or writes anything)
+  cfg.numAttrs = a.pdl || kMode == kScored ? 1 : 0;
   e = cudaLaunchKernelEx(&cfg, kern, *map, a);
   if (e == cudaSuccess) count_launch();
   return e;

@@ -75,13 +75,14 @@ struct DecodeArgs {
   const int32_t* prefix_lens;// [B] or nullptr
   const int32_t* doc_starts; // [B, q_len] or nullptr
   float* scores;             // [B, Hkv, max_len, score_row] in log2 units, or nullptr
-  int score_row;             // R rounded up to an even number
+  int score_row;             // floats a token (score_row(R))
 };
 
 // Shared memory the tensor-core kernel needs for one CTA.
 size_t mma_stage_bytes(int kv_dtype, int BS, int HG);
 size_t mma_smem_bytes(int kv_dtype, int BS, int HG, int stages);
 bool mma_supported(int kv_dtype, int BS, int D, int G, int q_len);
+bool mma_scored_supported(int kv_dtype, int BS, int D, int G, int q_len);
 
 cudaError_t launch_decode_mma(const CUtensorMap* map, const DecodeArgs& a, int grid_x, int grid_y,
                               cudaStream_t stream);
@@ -107,20 +108,25 @@ cudaError_t launch_prefix_check(const int32_t* tables, int max_blocks, const int
                                 const int32_t* prefix_table, int prefix_blocks,
                                 const int32_t* prefix_lens, int prefix_len_max, int B, int BS,
                                 int32_t* status, cudaStream_t stream);
-// Merge of [rows, S, D] partials (the public merge_partials layout); out_lse [rows] or
-// nullptr.
+// Merge of [rows, S, D] partials (the public merge_partials layout).
 cudaError_t launch_merge_rows(void* out, int out_dtype, const float* part_o, const float* part_lse,
-                              int rows, int S, int D, bool pdl, cudaStream_t stream,
-                              float* out_lse = nullptr);
+                              int rows, int S, int D, bool pdl, cudaStream_t stream);
 
 // Accumulated attention weights: rows of fp32 per (sequence, KV head).
 struct WeightRows {
   float* data;
   int64_t seq_stride, head_stride;
 };
-// out = in (nullptr: 0) + the softmax weights of a.scores' scores by a.out_lse
-cudaError_t launch_accumulate(const DecodeArgs& a, const WeightRows& in, const WeightRows& out,
-                              cudaStream_t stream);
+// Floats of a token's scores in a.scores, for R query rows (a power of two).
+inline int score_row(int R) {
+  int w = 1;
+  while (w < R) w *= 2;
+  return w;
+}
+// Merge of a scored call's partials (balanced or fixed) and, beside it, out = in
+// (nullptr: 0) + the softmax weights of the scores in a.scores.
+cudaError_t launch_merge_accumulate(const DecodeArgs& a, const WeightRows& in,
+                                    const WeightRows& out, cudaStream_t stream);
 
 struct AppendArgs {
   void* pool;
@@ -205,7 +211,7 @@ struct EvictArgs {
   int max_len, recent;
   int capacity;              // tokens the new tables, weights and index hold
 };
-cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
+cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t stream);
 
 // Launch counter shared by every launcher.
 void count_launch();

@@ -15,8 +15,11 @@
 // each of the sixteen warps takes every sixteenth partial with four rows in
 // flight, lanes split the head dimension, and the warps' sums meet in shared
 // memory.  For many rows with few partials each, one warp merges one row.
+#include <algorithm>
+
 #include "device.cuh"
 #include "launch.h"
+#include "score.cuh"
 
 namespace pkv {
 namespace {
@@ -228,15 +231,186 @@ __global__ void __launch_bounds__(32 * kRowsPerCta) merge_units_warp_kernel(cons
 // [rows, S, D] partials (the layout of the public merge_partials).
 __global__ void __launch_bounds__(kThreads)
     merge_rows_kernel(void* out, int out_dtype, const float* part_o, const float* part_lse, int S,
-                      int D, float* out_lse) {
+                      int D) {
   grid_launch_dependents();
   grid_dependency_wait();
   const size_t r = blockIdx.x;
-  merge_row(part_lse + r * S, 1, part_o + r * S * D, D, S, D, out, r * D, out_dtype,
-            out_lse ? out_lse + r : nullptr);
+  merge_row(part_lse + r * S, 1, part_o + r * S * D, D, S, D, out, r * D, out_dtype);
+}
+
+// ---------------------------------------------------------------- scored calls with a record
+
+// The partials of a row: (s, KV head h, row r = i * G + g).
+struct RowPartials {
+  size_t first, stride;      // rows of part_o and part_lse
+  int count;
+  size_t q_row;
+  bool ok;
+};
+__device__ __forceinline__ RowPartials row_partials(const DecodeArgs& a, int s, int h, int r) {
+  RowPartials p;
+  const int i = r / a.G, g = r % a.G;
+  p.q_row = ((size_t)s * a.q_len + i) * a.Hq + (size_t)h * a.G + g;
+  if (a.mode == 1) {                              // fixed splits
+    p.first = p.q_row * a.S;
+    p.stride = 1;
+    p.count = a.S;
+    p.ok = true;
+    return p;
+  }
+  const int hg = h / a.HG, w = h % a.HG, HGR = a.HG * a.R;
+  const int2 info = a.unit_info[s * a.NHG + hg];
+  p.ok = info_ok(a, info);
+  p.first = (size_t)info.x * HGR + (size_t)w * a.R + r;
+  p.stride = HGR;
+  p.count = p.ok ? info.y : 0;
+  return p;
+}
+
+// A token's weight is the sum over its rows of 2^(y - lse), y its scores in log2 units
+// (-inf where the row does not see it) and lse the rows' log-sum-exp, in one fixed order.
+// Every CTA of tokens finds its rows' log-sum-exp from the partials itself, with its
+// scores already in flight, so that it runs beside the merge instead of behind it.
+// ROW floats of scores a token, TOKENS a thread.
+template <int ROW>
+__device__ __forceinline__ void accumulate_tokens(const DecodeArgs& a, const WeightRows& in,
+                                                  const WeightRows& out, int s, int h, int j0) {
+  constexpr int TOKENS = ROW <= 4 ? 4 : ROW == 8 ? 2 : 1;
+  __shared__ float lse[16];
+  const int n = scored_len(a, s);
+  if (j0 >= n) return;
+  const int from = first_read(a, s, n);
+  const float* scores = a.scores + ((int64_t)s * a.Hkv + h) * a.max_len * ROW;
+  const float* win = in.data ? in.data + s * in.seq_stride + h * in.head_stride : nullptr;
+  float y[TOKENS][ROW], w[TOKENS];
+#pragma unroll
+  for (int k = 0; k < TOKENS; ++k) {
+    const int j = j0 + k * kThreads + threadIdx.x;
+    w[k] = win && j < n ? win[j] : 0.f;
+    const float* row = scores + (int64_t)j * ROW;
+    if (j >= from && j < n) {
+      if constexpr (ROW >= 4) {
+#pragma unroll
+        for (int r = 0; r < ROW; r += 4)
+          *reinterpret_cast<float4*>(&y[k][r]) = *reinterpret_cast<const float4*>(row + r);
+      } else if constexpr (ROW == 2) {
+        *reinterpret_cast<float2*>(&y[k][0]) = *reinterpret_cast<const float2*>(row);
+      } else {
+        y[k][0] = row[0];
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < ROW; ++r) y[k][r] = -INFINITY;
+    }
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < a.R) {
+    const RowPartials p = row_partials(a, s, h, warp);
+    float M = -INFINITY, W = 0.f;
+    for (int i = lane; i < p.count; i += 32)
+      M = fmaxf(M, a.part_lse[p.first + (size_t)i * p.stride]);
+    M = warp_max(M);
+    if (M != -INFINITY)
+      for (int i = lane; i < p.count; i += 32)
+        W += exp2f((a.part_lse[p.first + (size_t)i * p.stride] - M) * kLog2e);
+    W = warp_sum(W);
+    // a row that sees no key: its scores are all -inf, 2^(-inf - 0) adds nothing
+    if (lane == 0) lse[warp] = M == -INFINITY ? 0.f : fmaf(M, kLog2e, log2f(W));
+  }
+  __syncthreads();
+  float* wout = out.data + s * out.seq_stride + h * out.head_stride;
+#pragma unroll
+  for (int k = 0; k < TOKENS; ++k) {
+    const int j = j0 + k * kThreads + threadIdx.x;
+    float sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < ROW; ++r)
+      if (r < a.R) sum += exp2f(y[k][r] - lse[r]);
+    if (j < n) wout[j] = w[k] + sum;
+  }
+}
+
+__host__ __device__ constexpr int tokens_per_cta(int row) {
+  return kThreads * (row <= 4 ? 4 : row == 8 ? 2 : 1);
+}
+
+// CTAs [0, row_ctas) merge rows (one each, or with kWarpRows one a warp), the others
+// take tokens.
+template <bool kWarpRows>
+__global__ void __launch_bounds__(kThreads)
+    merge_accumulate_kernel(const DecodeArgs a, const WeightRows in, const WeightRows out,
+                            int row_ctas, int token_ctas) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  if (blockIdx.x >= row_ctas) {
+    const unsigned u = (blockIdx.x - row_ctas) / token_ctas;
+    const int tile = (blockIdx.x - row_ctas) % token_ctas, h = u % a.Hkv, s = u / a.Hkv;
+    const int j0 = tile * tokens_per_cta(a.score_row);
+    switch (a.score_row) {
+      case 1: accumulate_tokens<1>(a, in, out, s, h, j0); break;
+      case 2: accumulate_tokens<2>(a, in, out, s, h, j0); break;
+      case 4: accumulate_tokens<4>(a, in, out, s, h, j0); break;
+      case 8: accumulate_tokens<8>(a, in, out, s, h, j0); break;
+      default: accumulate_tokens<16>(a, in, out, s, h, j0); break;
+    }
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  const long long row =
+      kWarpRows ? (long long)blockIdx.x * kWarps + (threadIdx.x >> 5) : (long long)blockIdx.x;
+  if (row >= (long long)a.B * a.Hkv * a.R) return;
+  const int r = (int)(row % a.R), h = (int)(row / a.R % a.Hkv), s = (int)(row / a.R / a.Hkv);
+  const RowPartials p = row_partials(a, s, h, r);
+  if (!p.ok && threadIdx.x == 0) record_error(a.status, PKV_EBOUNDS);
+  if constexpr (kWarpRows) {
+    float M = -INFINITY;
+    for (int i = lane; i < p.count; i += 32)
+      M = fmaxf(M, a.part_lse[p.first + (size_t)i * p.stride]);
+    M = warp_max(M);
+    for (int d0 = 4 * lane; d0 < a.D; d0 += 128) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float W = 0.f;
+      for (int i = 0; i < p.count && M != -INFINITY; ++i) {
+        const size_t pr = p.first + (size_t)i * p.stride;
+        const float wt = exp2f((a.part_lse[pr] - M) * kLog2e);
+        const float4 v = *reinterpret_cast<const float4*>(a.part_o + pr * a.D + d0);
+        W += wt;
+        acc.x = fmaf(wt, v.x, acc.x);
+        acc.y = fmaf(wt, v.y, acc.y);
+        acc.z = fmaf(wt, v.z, acc.z);
+        acc.w = fmaf(wt, v.w, acc.w);
+      }
+      const float inv = W > 0.f ? 1.f / W : 0.f;
+      store_from_float(a.out, p.q_row * a.D + d0 + 0, a.out_dtype, acc.x * inv);
+      store_from_float(a.out, p.q_row * a.D + d0 + 1, a.out_dtype, acc.y * inv);
+      store_from_float(a.out, p.q_row * a.D + d0 + 2, a.out_dtype, acc.z * inv);
+      store_from_float(a.out, p.q_row * a.D + d0 + 3, a.out_dtype, acc.w * inv);
+    }
+  } else {
+    merge_row(a.part_lse + p.first, p.stride, a.part_o + p.first * a.D, p.stride * a.D, p.count,
+              a.D, a.out, p.q_row * a.D, a.out_dtype);
+  }
 }
 
 }  // namespace
+
+cudaError_t launch_merge_accumulate(const DecodeArgs& a, const WeightRows& in,
+                                    const WeightRows& out, cudaStream_t stream) {
+  if (a.D > kMaxD || a.R > kWarps || a.score_row > 16) return cudaErrorInvalidValue;
+  const long long rows = (long long)a.B * a.Hkv * a.R;
+  const bool warp_rows = rows >= 512 && a.D % 4 == 0;   // as launch_merge_units
+  const long long row_ctas = warp_rows ? (rows + kWarps - 1) / kWarps : rows;
+  const long long token_ctas =
+      ((long long)a.max_len + tokens_per_cta(a.score_row) - 1) / tokens_per_cta(a.score_row);
+  const long long grid = row_ctas + token_ctas * a.B * a.Hkv;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const cudaError_t e =
+      launch_chained(warp_rows ? merge_accumulate_kernel<true> : merge_accumulate_kernel<false>,
+                     dim3((unsigned)grid), dim3(kThreads), 1, stream, a, in, out, (int)row_ctas,
+                     (int)std::max(token_ctas, 1LL));
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
 
 static cudaError_t launch_pdl(const void* func, dim3 grid, void** args, bool pdl,
                               cudaStream_t stream) {
@@ -286,11 +460,10 @@ cudaError_t launch_merge_units(const DecodeArgs& a, bool pdl, cudaStream_t strea
 }
 
 cudaError_t launch_merge_rows(void* out, int out_dtype, const float* part_o, const float* part_lse,
-                              int rows, int S, int D, bool pdl, cudaStream_t stream,
-                              float* out_lse) {
+                              int rows, int S, int D, bool pdl, cudaStream_t stream) {
   if (D > kMaxD) return cudaErrorInvalidValue;
   if (rows == 0) return cudaSuccess;
-  void* args[] = {&out, &out_dtype, &part_o, &part_lse, &S, &D, &out_lse};
+  void* args[] = {&out, &out_dtype, &part_o, &part_lse, &S, &D};
   return launch_pdl(reinterpret_cast<const void*>(merge_rows_kernel), dim3(rows), args, pdl,
                     stream);
 }

@@ -1317,14 +1317,24 @@ int verify_drafts(int32_t* d_tokens, int32_t* d_num_accepted, const pkv_probs* t
 // ---------------------------------------------------------------- scored attention
 
 // Workspace of a scored call: the partials of the kernel that runs, then (with weights)
-// every row's log-sum-exp and the scores.
+// the scores.
 struct ScoredWs {
-  size_t part_o, part_lse, info, lse, scores, bytes;
+  size_t part_o, part_lse, info, scores, bytes;
 };
-static size_t score_row(int R) { return (size_t)(R + 1) / 2 * 2; }
+// The decode kernel's plan of a scored call: with more than 8 query rows per KV head two
+// warps take a head's tile, so a CTA takes half as many heads (its warps then still run
+// two CTAs to an SM).
+static bool plan_scored(const pkv_geometry& g, const DeviceInfo& dev, int R, MmaPlan* p) {
+  if (R <= 8) return plan_mma(g, dev, nullptr, p);
+  pkv_launch_opts o{};
+  for (o.kv_heads_per_cta = 2; o.kv_heads_per_cta >= 1; --o.kv_heads_per_cta)
+    if (hg_ok(g, o.kv_heads_per_cta) &&
+        mma_stage_bytes(g.kv_dtype, g.block_size, o.kv_heads_per_cta) <= 32 * 1024)
+      return plan_mma(g, dev, &o, p);
+  return false;
+}
 static void add_record(const pkv_geometry& g, int batch, int q_len, int max_seq_len, ScoredWs* w) {
-  w->lse = w->bytes;
-  w->scores = w->lse + align256((size_t)batch * q_len * g.num_q_heads * sizeof(float));
+  w->scores = w->bytes;
   w->bytes = w->scores +
              align256((size_t)batch * g.num_kv_heads * max_seq_len *
                       score_row(q_len * (g.num_q_heads / g.num_kv_heads)) * sizeof(float));
@@ -1332,7 +1342,7 @@ static void add_record(const pkv_geometry& g, int batch, int q_len, int max_seq_
 static ScoredWs scored_ws_mma(const pkv_geometry& g, int batch, int q_len, int max_seq_len,
                               const MmaPlan& plan, bool weights) {
   const BalancedWs b = balanced_ws(g, batch, q_len, plan);
-  ScoredWs w{b.o_off, b.lse_off, b.info_off, 0, 0, b.bytes};
+  ScoredWs w{b.o_off, b.lse_off, b.info_off, 0, b.bytes};
   if (weights) add_record(g, batch, q_len, max_seq_len, &w);
   return w;
 }
@@ -1356,8 +1366,8 @@ size_t paged_decode_scored_workspace_bytes(const pkv_geometry* g, int batch, int
   const int G = g->num_q_heads / g->num_kv_heads;
   size_t need = 0;
   MmaPlan plan;
-  if (mma_supported(g->kv_dtype, g->block_size, g->head_dim, G, q_len) &&
-      plan_mma(*g, dev, nullptr, &plan))
+  if (mma_scored_supported(g->kv_dtype, g->block_size, g->head_dim, G, q_len) &&
+      plan_scored(*g, dev, G * q_len, &plan))
     need = scored_ws_mma(*g, batch, q_len, max_seq_len, plan, with_weights != 0).bytes;
   if (q_len == 1)
     need = std::max(need, scored_ws_simt(*g, batch, max_seq_len,
@@ -1450,22 +1460,12 @@ int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* 
   a.slopes = sc.d_slopes;
   a.prefix_lens = sc.d_prefix_lens;
   a.doc_starts = sc.d_doc_starts;
-  a.score_row = (int)score_row(a.R);
+  a.score_row = score_row(a.R);
   char* ws = static_cast<char*>(d_workspace);
-  auto record = [&](const ScoredWs& w) {
-    if (!weights) return;
-    a.out_lse = reinterpret_cast<float*>(ws + w.lse);
-    a.scores = reinterpret_cast<float*>(ws + w.scores);
-  };
-  auto accumulate = [&]() -> int {
-    if (!weights) return PKV_OK;
-    return launch_accumulate(a, w_in, w_out, stream) == cudaSuccess ? PKV_OK : PKV_ECUDA;
-  };
-
   const bool q_ok = fp8 ? (q_dtype == PKV_BF16 || q_dtype == PKV_F16) : (int)q_dtype == g.kv_dtype;
-  if (q_ok && mma_supported(g.kv_dtype, g.block_size, g.head_dim, G, q_len)) {
+  if (q_ok && mma_scored_supported(g.kv_dtype, g.block_size, g.head_dim, G, q_len)) {
     MmaPlan plan;
-    if (!plan_mma(g, dev, nullptr, &plan)) return PKV_EUNSUPPORTED;
+    if (!plan_scored(g, dev, a.R, &plan)) return PKV_EUNSUPPORTED;
     const CUtensorMap* map = p->tmap(plan.HG);
     if (!map) return PKV_ECUDA;
     const ScoredWs w = scored_ws_mma(g, batch, q_len, max_seq_len, plan, weights != nullptr);
@@ -1479,10 +1479,11 @@ int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* 
     a.unit_info = reinterpret_cast<int2*>(ws + w.info);
     a.slots = plan.grid + batch * plan.NHG;
     a.early_trigger = fp8 ? 0 : 1;
-    record(w);
+    if (weights) a.scores = reinterpret_cast<float*>(ws + w.scores);
     if (launch_decode_mma_scored(map, a, plan.grid, stream) != cudaSuccess) return PKV_ECUDA;
-    if (launch_merge_units(a, true, stream) != cudaSuccess) return PKV_ECUDA;
-    return accumulate();
+    const cudaError_t e = weights ? launch_merge_accumulate(a, w_in, w_out, stream)
+                                  : launch_merge_units(a, true, stream);
+    return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
   }
   if (q_len > 1) {
     // chunks with more query rows than the decode kernel holds
@@ -1501,13 +1502,15 @@ int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* 
     a.part_o = reinterpret_cast<float*>(ws + w.part_o);
     a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
   }
-  record(w);
+  if (weights) a.scores = reinterpret_cast<float*>(ws + w.scores);
+  a.mode = 1;
   if (launch_decode_simt_scored(a, stream) != cudaSuccess) return PKV_ECUDA;
-  if (w.bytes > 0 && launch_merge_rows(d_out, out_dtype, a.part_o, a.part_lse,
-                                       batch * g.num_q_heads, S, g.head_dim, true, stream,
-                                       a.out_lse) != cudaSuccess)
-    return PKV_ECUDA;
-  return accumulate();
+  if (w.bytes == 0) return PKV_OK;                 // one split: out is written
+  const cudaError_t e =
+      weights ? launch_merge_accumulate(a, w_in, w_out, stream)
+              : launch_merge_rows(d_out, out_dtype, a.part_o, a.part_lse, batch * g.num_q_heads, S,
+                                  g.head_dim, true, stream);
+  return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
 // ---------------------------------------------------------------- eviction
@@ -1573,7 +1576,9 @@ int kv_evict(pkv_pool* p, int layer, const int32_t* d_new_tables, int max_new_bl
   a.row_bytes = g.head_dim * elem_bytes(g.kv_dtype);
   a.max_len = max_seq_len;
   a.recent = recent;
-  return launch_evict(a, stream) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+  DeviceInfo dev;
+  if (!device_info(&dev)) return PKV_ECUDA;
+  return launch_evict(a, dev.sms, stream) == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
 int pkv_check_status(const pkv_pool* p, cudaStream_t stream) {

@@ -6,6 +6,9 @@
 //   first key:
 // all of them one interval [lo, hi).  A score x (already scaled) becomes
 // cap tanh(x / cap) (cap > 0), then loses slope |p - j|.
+//
+// Plain loads: scored kernels are scheduled while the launches before them, which may
+// write what is read here, still run.
 #pragma once
 #include "device.cuh"
 #include "launch.h"
@@ -14,7 +17,7 @@ namespace pkv {
 
 // The sequence's length as the scored calls take it: limited to [0, a.max_len].
 __device__ __forceinline__ int scored_len(const DecodeArgs& a, int s) {
-  int n = __ldg(a.seq_lens + s);
+  int n = a.seq_lens[s];
   if (n < 0 || n > a.max_len) {
     record_error(a.status, PKV_EBOUNDS);
     n = n < 0 ? 0 : a.max_len;
@@ -30,9 +33,9 @@ __device__ __forceinline__ KeyRange key_range(const DecodeArgs& a, int s, int n,
   const int p = n - a.q_len + i;
   if (p < 0) return {0, 0};
   int lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
-  if (a.doc_starts) lo = max(lo, __ldg(a.doc_starts + (size_t)s * a.q_len + i));
+  if (a.doc_starts) lo = max(lo, a.doc_starts[(size_t)s * a.q_len + i]);
   int hi = p + 1;
-  if (a.prefix_lens) hi = max(hi, min(__ldg(a.prefix_lens + s), n));
+  if (a.prefix_lens) hi = max(hi, min(a.prefix_lens[s], n));
   return {lo, hi};
 }
 

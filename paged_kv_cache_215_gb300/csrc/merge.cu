@@ -277,17 +277,24 @@ __device__ __forceinline__ void accumulate_tokens(const DecodeArgs& a, const Wei
                                                   const WeightRows& out, int s, int h, int j0) {
   constexpr int TOKENS = ROW <= 4 ? 4 : ROW == 8 ? 2 : 1;
   __shared__ float lse[16];
+  // the attention ahead has waited for everything before it, and writes none of these
   const int n = scored_len(a, s);
-  if (j0 >= n) return;
   const int from = first_read(a, s, n);
-  const float* scores = a.scores + ((int64_t)s * a.Hkv + h) * a.max_len * ROW;
-  const float* win = in.data ? in.data + s * in.seq_stride + h * in.head_stride : nullptr;
+  const float* win =
+      in.data ? in.data + s * in.seq_stride + h * in.head_stride + j0 + threadIdx.x : nullptr;
   float y[TOKENS][ROW], w[TOKENS];
 #pragma unroll
   for (int k = 0; k < TOKENS; ++k) {
+    w[k] = win && j0 + k * kThreads + (int)threadIdx.x < n ? win[k * kThreads] : 0.f;
+  }
+  grid_dependency_wait();
+  if (j0 >= n) return;
+  const float* scores =
+      a.scores + (((int64_t)s * a.Hkv + h) * a.max_len + j0 + threadIdx.x) * ROW;
+#pragma unroll
+  for (int k = 0; k < TOKENS; ++k) {
     const int j = j0 + k * kThreads + threadIdx.x;
-    w[k] = win && j < n ? win[j] : 0.f;
-    const float* row = scores + (int64_t)j * ROW;
+    const float* row = scores + k * kThreads * ROW;
     if (j >= from && j < n) {
       if constexpr (ROW >= 4) {
 #pragma unroll
@@ -306,27 +313,32 @@ __device__ __forceinline__ void accumulate_tokens(const DecodeArgs& a, const Wei
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp < a.R) {
     const RowPartials p = row_partials(a, s, h, warp);
-    float M = -INFINITY, W = 0.f;
-    for (int i = lane; i < p.count; i += 32)
+    const float first = lane < p.count ? a.part_lse[p.first + (size_t)lane * p.stride] : -INFINITY;
+    float M = first;
+    for (int i = lane + 32; i < p.count; i += 32)
       M = fmaxf(M, a.part_lse[p.first + (size_t)i * p.stride]);
     M = warp_max(M);
-    if (M != -INFINITY)
-      for (int i = lane; i < p.count; i += 32)
-        W += exp2f((a.part_lse[p.first + (size_t)i * p.stride] - M) * kLog2e);
-    W = warp_sum(W);
     // a row that sees no key: its scores are all -inf, 2^(-inf - 0) adds nothing
-    if (lane == 0) lse[warp] = M == -INFINITY ? 0.f : fmaf(M, kLog2e, log2f(W));
+    float sum = 0.f;
+    if (M != -INFINITY) {
+      float W = exp2f((first - M) * kLog2e);
+      for (int i = lane + 32; i < p.count; i += 32)
+        W += exp2f((a.part_lse[p.first + (size_t)i * p.stride] - M) * kLog2e);
+      sum = fmaf(M, kLog2e, log2f(warp_sum(W)));
+    }
+    if (lane == 0) lse[warp] = sum;
   }
   __syncthreads();
-  float* wout = out.data + s * out.seq_stride + h * out.head_stride;
+  float l[ROW];                                   // (rows behind the last add 2^-inf)
+#pragma unroll
+  for (int r = 0; r < ROW; ++r) l[r] = r < a.R ? lse[r] : 0.f;
+  float* wout = out.data + s * out.seq_stride + h * out.head_stride + j0 + threadIdx.x;
 #pragma unroll
   for (int k = 0; k < TOKENS; ++k) {
-    const int j = j0 + k * kThreads + threadIdx.x;
-    float sum = 0.f;
+    float sum = 0.f;                              // (a weight below 2^-126 counts as 0)
 #pragma unroll
-    for (int r = 0; r < ROW; ++r)
-      if (r < a.R) sum += exp2f(y[k][r] - lse[r]);
-    if (j < n) wout[j] = w[k] + sum;
+    for (int r = 0; r < ROW; ++r) sum += ex2_ftz((r < a.R ? y[k][r] : -INFINITY) - l[r]);
+    if (j0 + k * kThreads + (int)threadIdx.x < n) wout[k * kThreads] = w[k] + sum;
   }
 }
 
@@ -334,18 +346,15 @@ __host__ __device__ constexpr int tokens_per_cta(int row) {
   return kThreads * (row <= 4 ? 4 : row == 8 ? 2 : 1);
 }
 
-// CTAs [0, row_ctas) merge rows (one each, or with kWarpRows one a warp), the others
-// take tokens.
+// CTA (x, h, s): the first CTAs along x merge the rows of (s, h) (one each, or with
+// kWarpRows a warp each), the others take its tokens.
 template <bool kWarpRows>
-__global__ void __launch_bounds__(kThreads)
-    merge_accumulate_kernel(const DecodeArgs a, const WeightRows in, const WeightRows out,
-                            int row_ctas, int token_ctas) {
+__global__ void __launch_bounds__(kThreads, 2)
+    merge_accumulate_kernel(const DecodeArgs a, const WeightRows in, const WeightRows out) {
   grid_launch_dependents();
-  grid_dependency_wait();
-  if (blockIdx.x >= row_ctas) {
-    const unsigned u = (blockIdx.x - row_ctas) / token_ctas;
-    const int tile = (blockIdx.x - row_ctas) % token_ctas, h = u % a.Hkv, s = u / a.Hkv;
-    const int j0 = tile * tokens_per_cta(a.score_row);
+  const int row_ctas = kWarpRows ? 1 : a.R, h = blockIdx.y, s = blockIdx.z;
+  if ((int)blockIdx.x >= row_ctas) {
+    const int j0 = (blockIdx.x - row_ctas) * tokens_per_cta(a.score_row);
     switch (a.score_row) {
       case 1: accumulate_tokens<1>(a, in, out, s, h, j0); break;
       case 2: accumulate_tokens<2>(a, in, out, s, h, j0); break;
@@ -355,11 +364,9 @@ __global__ void __launch_bounds__(kThreads)
     }
     return;
   }
-  const int lane = threadIdx.x & 31;
-  const long long row =
-      kWarpRows ? (long long)blockIdx.x * kWarps + (threadIdx.x >> 5) : (long long)blockIdx.x;
-  if (row >= (long long)a.B * a.Hkv * a.R) return;
-  const int r = (int)(row % a.R), h = (int)(row / a.R % a.Hkv), s = (int)(row / a.R / a.Hkv);
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31, r = kWarpRows ? threadIdx.x >> 5 : blockIdx.x;
+  if (r >= a.R) return;
   const RowPartials p = row_partials(a, s, h, r);
   if (!p.ok && threadIdx.x == 0) record_error(a.status, PKV_EBOUNDS);
   if constexpr (kWarpRows) {
@@ -397,17 +404,15 @@ __global__ void __launch_bounds__(kThreads)
 cudaError_t launch_merge_accumulate(const DecodeArgs& a, const WeightRows& in,
                                     const WeightRows& out, cudaStream_t stream) {
   if (a.D > kMaxD || a.R > kWarps || a.score_row > 16) return cudaErrorInvalidValue;
-  const long long rows = (long long)a.B * a.Hkv * a.R;
-  const bool warp_rows = rows >= 512 && a.D % 4 == 0;   // as launch_merge_units
-  const long long row_ctas = warp_rows ? (rows + kWarps - 1) / kWarps : rows;
+  if (a.B > 65535 || a.Hkv > 65535) return cudaErrorInvalidValue;
+  // as launch_merge_units
+  const bool warp_rows = (long long)a.B * a.Hkv * a.R >= 512 && a.D % 4 == 0;
   const long long token_ctas =
       ((long long)a.max_len + tokens_per_cta(a.score_row) - 1) / tokens_per_cta(a.score_row);
-  const long long grid = row_ctas + token_ctas * a.B * a.Hkv;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)(token_ctas + (warp_rows ? 1 : a.R)), a.Hkv, a.B);
   const cudaError_t e =
       launch_chained(warp_rows ? merge_accumulate_kernel<true> : merge_accumulate_kernel<false>,
-                     dim3((unsigned)grid), dim3(kThreads), 1, stream, a, in, out, (int)row_ctas,
-                     (int)std::max(token_ctas, 1LL));
+                     grid, dim3(kThreads), 1, stream, a, in, out);
   if (e == cudaSuccess) count_launch();
   return e;
 }

@@ -324,7 +324,7 @@ struct Consumer {
     float* flat = &s[0][0][0];
     if (a.cap_in != 0.f) {
       scale_scores<kTiles * NT * 4>(flat, cap_in_ * ks_b);
-      cap_scores<kTiles * NT * 4>(flat, a.cap_out);
+      cap_scores_fine<kTiles * NT * 4>(flat, a.cap_out);
     } else {
       scale_scores<kTiles * NT * 4>(flat, qk_scale_log2_ * ks_b);
     }

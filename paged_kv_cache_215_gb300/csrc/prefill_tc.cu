@@ -67,6 +67,7 @@ constexpr uint32_t kSmemKV = kSmemQ + kQT * 2 * kHalf;
 constexpr uint32_t kTmemCols = 512;          // query tile t: S/P0 [256t, +64) S/P1 [+64, +128) O [+128, +256)
 constexpr uint32_t kAlignSlack = 1024;       // the tiles start on a 1024-byte boundary
 constexpr int kMaxStages = 6;
+constexpr float kTiny = 0x1p-126f;           // in the place of a scale of 0: -inf times it is -inf
 
 // Per pool dtype.  bf16 / f16: TMA fills kStages tiles the MMAs read directly.
 // E4M3: TMA lands the E4M3 tile (one 128-byte line per key: half the boxes) in
@@ -123,13 +124,15 @@ __device__ __forceinline__ int key_tiles(const DecodeArgs& a, int n, int qt) {
   return p_last >= 0 ? (p_last + kN) / kN : 0;
 }
 
-// kScore: a chunk under the rules of score.cuh; each row sees its own interval of keys,
-// and the CTA reads from the first key that any of its rows sees.
-template <int KVT, bool kScore>
+// kRules: a chunk under the rules of score.cuh (windows, prefixes and documents alone, with
+// a cap, or with distances and perhaps a cap); each row sees its own interval of keys, and
+// the CTA reads from the first key that any of its rows sees.
+enum Rules { kNone = 0, kMasks = 1, kCap = 2, kDistance = 3 };
+template <int KVT, int kRules>
 __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, const DecodeArgs a) {
   using C = PfCfg<KVT>;
-  constexpr bool kBf16 = C::kBf16, kFp8 = C::kFp8;
+  constexpr bool kBf16 = C::kBf16, kFp8 = C::kFp8, kScore = kRules != kNone;
   constexpr int kStages = C::kStages;
   constexpr bool kSplitP = kBf16;            // f16 P (11 bits) needs no low term
   // f16 P is 2^(s - ref + kPOff) <= 2^15: weights down to 2^-21 of the row's
@@ -677,12 +680,13 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
     float slope = 0.f, cap_in = 0.f;
     if constexpr (kScore) {
       if (live) keys = key_range(a, s, n, tok);
-      if (a.slopes) slope = __ldg(a.slopes + hkv * G + g) * kLog2e;
-      cap_in = fabsf(a.cap_in) * pow2i(-q_e);
     }
+    if constexpr (kRules >= kCap) cap_in = fabsf(a.cap_in) * pow2i(-q_e);
+    if constexpr (kRules == kDistance) slope = a.slopes[hkv * G + g] * kLog2e;
     const int my_tiles = tiles[t];
     // Q carries the sign; 2^-q_e undoes the row's f16 prescale (E4M3 pools)
     float qs = fabsf(a.qk_scale_log2) * pow2i(-q_e);
+    if (kScore) qs = fmaxf(qs, kTiny);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tcol = tmem + lane_base + t * 256;
     float mref = -INFINITY, lsum = 0.f;
@@ -708,7 +712,9 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
       const int b = jl & 1;
       const int j = jl;
       const int kpos0 = (jt0 + j) * kN;
-      float qsb[4] = {qs, qs, qs, qs};
+      float qsb[4];                 // of 16 keys each: the scale, or with a cap the scale over it
+#pragma unroll
+      for (int g4 = 0; g4 < 4; ++g4) qsb[g4] = kRules >= kCap && a.cap_in != 0.f ? cap_in : qs;
       if (bscaled) {
         // issued before the wait for S, so the loads overlap it
 #pragma unroll
@@ -716,7 +722,8 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
           const int jb = min((kpos0 + 16 * g4) / a.BS, nblk - 1);
           int blk = __ldg(trow + (kScore ? max(jb, blk0) : jb));
           blk = (blk < 0 || blk >= a.num_blocks) ? 0 : blk;
-          qsb[g4] = (kScore && a.cap_in != 0.f ? cap_in : qs) * __ldg(a.block_scales + ((size_t)blk * 2 * a.L + a.layer) * a.Hkv + hkv);
+          qsb[g4] = (kRules >= kCap && a.cap_in != 0.f ? cap_in : qs) * __ldg(a.block_scales + ((size_t)blk * 2 * a.L + a.layer) * a.Hkv + hkv);
+          if (kScore && qsb[g4] == 0.f) qsb[g4] = kTiny;
         }
       }
       if (!wait(&bars->s_full[t][b], (jl >> 1) & 1)) {
@@ -733,18 +740,32 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 8; ++e) mp[e] = -INFINITY;
       if constexpr (kScore) {
-        // to log2 units: scale or cap, distance, mask
+        if constexpr (kRules >= kCap) {
+          // to log2 units here (the cap is no factor of the largest score)
 #pragma unroll
-        for (int g4 = 0; g4 < 4; ++g4)
-          scale_scores<16>(sv + 16 * g4, bscaled || a.cap_in == 0.f ? qsb[g4] : cap_in);
-        if (a.cap_in != 0.f) cap_scores<kN>(sv, a.cap_out);
-        if (a.slopes) {
-          const float d0 = (float)(pos - kpos0);
-#pragma unroll
-          for (int c = 0; c < kN; ++c) sv[c] = fmaf(-slope, fabsf(d0 - (float)c), sv[c]);
+          for (int g4 = 0; g4 < 4; ++g4) {
+            scale_scores<16>(sv + 16 * g4, qsb[g4]);
+            qsb[g4] = 1.f;
+          }
+          if (kRules == kCap || a.cap_in != 0.f) cap_scores<kN>(sv, a.cap_out);
         }
-        if (!__all_sync(0xffffffffu, kpos0 >= keys.lo && kpos0 + kN <= keys.hi)) {
-          const int c0 = keys.lo - kpos0, c1 = keys.hi - kpos0;
+        if constexpr (kRules == kDistance) {
+          const float d0 = (float)(pos - kpos0);
+          if (__all_sync(0xffffffffu, pos >= kpos0 + kN - 1)) {
+            // every key lies behind its query: - slope (d0 - c), two keys an instruction
+            const uint64_t s2 = f2_pack(slope, slope);
+#pragma unroll
+            for (int c = 0; c < kN; c += 2) {
+              const uint64_t d2 = f2_pack((float)c - d0, (float)(c + 1) - d0);
+              f2_unpack(ffma2(s2, d2, f2_pack(sv[c], sv[c + 1])), sv[c], sv[c + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kN; ++c) sv[c] = fmaf(-slope, fabsf(d0 - (float)c), sv[c]);
+          }
+        }
+        const int c0 = keys.lo - kpos0, c1 = keys.hi - kpos0;
+        if (!__all_sync(0xffffffffu, c0 <= 0 && c1 >= kN)) {
 #pragma unroll
           for (int c = 0; c < kN; ++c) sv[c] = c >= c0 && c < c1 ? sv[c] : -INFINITY;
         }
@@ -753,8 +774,6 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
           const int e = 2 * (c >> 4) + ((c >> 1) & 1);
           mp[e] = fmax3(mp[e], sv[c], sv[c + 1]);
         }
-#pragma unroll
-        for (int g4 = 0; g4 < 4; ++g4) qsb[g4] = 1.f;
       } else if (__all_sync(0xffffffffu, live && kpos0 + kN - 1 <= pos)) {
         // the warp's rows see every key of the tile: no mask
 #pragma unroll
@@ -819,7 +838,7 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
           // p = 2^(s * scale - ref): one FMA per two keys and the SFU per key
           float x0, x1;
           const uint64_t sv2 = f2_pack(sv[c], sv[c + 1]);
-          f2_unpack(kScore ? fadd2(sv2, nref2) : ffma2(sv2, qs2, nref2), x0, x1);
+          f2_unpack(kRules >= kCap ? fadd2(sv2, nref2) : ffma2(sv2, qs2, nref2), x0, x1);
           const float p0 = ex2_ftz(x0), p1 = ex2_ftz(x1);
           const uint64_t p2 = f2_pack(p0, p1);
           pp[c2 & 3] = fadd2(pp[c2 & 3], p2);
@@ -914,10 +933,10 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
 template <int KVT>
 size_t smem_bytes_t() { return PfCfg<KVT>::kSmemBytes + sizeof(Bars) + kAlignSlack; }
 
-template <int KVT, bool kScore>
+template <int KVT, int kRules>
 cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, dim3 grid, cudaStream_t stream) {
   const size_t smem = smem_bytes_t<KVT>();
-  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<KVT, kScore>,
+  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<KVT, kRules>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -930,7 +949,7 @@ cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, dim3 grid, cud
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<KVT, kScore>, *map, a);
+  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<KVT, kRules>, *map, a);
 }
 
 bool prefill_tc_supported(int kv_dtype, int q_dtype, int BS, int D, int G) {
@@ -941,7 +960,7 @@ bool prefill_tc_supported(int kv_dtype, int q_dtype, int BS, int D, int G) {
          kM % G == 0;
 }
 
-template <bool kScore>
+template <int kRules>
 static cudaError_t launch_chunk(const CUtensorMap* map, const DecodeArgs& a, cudaStream_t stream) {
   const int QT = kM / a.G;
   const int qtiles = (a.q_len + QT - 1) / QT;
@@ -952,9 +971,9 @@ static cudaError_t launch_chunk(const CUtensorMap* map, const DecodeArgs& a, cud
   dim3 grid(a.Hkv, a.key_limit ? a.S : a.B, pairs);
   cudaError_t e;
   switch (a.kv_dtype) {
-    case PKV_BF16: e = launch_t<PKV_BF16, kScore>(map, a, grid, stream); break;
-    case PKV_F16: e = launch_t<PKV_F16, kScore>(map, a, grid, stream); break;
-    case PKV_FP8_E4M3: e = launch_t<PKV_FP8_E4M3, kScore>(map, a, grid, stream); break;
+    case PKV_BF16: e = launch_t<PKV_BF16, kRules>(map, a, grid, stream); break;
+    case PKV_F16: e = launch_t<PKV_F16, kRules>(map, a, grid, stream); break;
+    case PKV_FP8_E4M3: e = launch_t<PKV_FP8_E4M3, kRules>(map, a, grid, stream); break;
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;
@@ -964,13 +983,15 @@ static cudaError_t launch_chunk(const CUtensorMap* map, const DecodeArgs& a, cud
 }
 
 cudaError_t launch_prefill_tc(const CUtensorMap* map, const DecodeArgs& a, cudaStream_t stream) {
-  return launch_chunk<false>(map, a, stream);
+  return launch_chunk<kNone>(map, a, stream);
 }
 
 cudaError_t launch_prefill_tc_scored(const CUtensorMap* map, const DecodeArgs& a,
                                      cudaStream_t stream) {
   if (a.key_limit) return cudaErrorInvalidValue;
-  return launch_chunk<true>(map, a, stream);
+  return a.slopes           ? launch_chunk<kDistance>(map, a, stream)
+         : a.cap_in != 0.f ? launch_chunk<kCap>(map, a, stream)
+                           : launch_chunk<kMasks>(map, a, stream);
 }
 
 }  // namespace pkv

@@ -72,30 +72,77 @@ __device__ __forceinline__ float tanh_score(float x) {
   return fabsf(x) < 0.6f ? fmaf(x * z, p, x) : big;
 }
 
-// x[i] = cap_out tanh(x[i]) of N scores a thread (N even); whole warps.  While no score
-// of the warp is above 1 in magnitude (scores within the cap) one polynomial in x^2, two
-// scores an instruction, serves them all (2^-24 before rounding, 2^-22.5 with it): 4.5
-// instructions a score, none of them on the special-function unit that the softmax's
-// exponentials need, against 15 for tanh_score.
+// x[i] = cap_out x[i] (1 + z (c[0] + z (c[1] + ...))), z = x[i]^2: an odd polynomial on
+// two scores an instruction.
+template <int N, int K>
+__device__ __forceinline__ void odd_polynomial(float* x, float cap_out, const float (&c)[K]) {
+  uint64_t c2[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) c2[k] = f2_pack(c[k] * cap_out, c[k] * cap_out);
+  const uint64_t one = f2_pack(cap_out, cap_out);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const uint64_t v = f2_pack(x[i], x[i + 1]), z = fmul2(v, v);
+    uint64_t p = c2[K - 1];
+#pragma unroll
+    for (int k = K - 2; k >= 0; --k) p = ffma2(p, z, c2[k]);
+    f2_unpack(fmul2(v, ffma2(p, z, one)), x[i], x[i + 1]);
+  }
+}
+
+// cap_out tanh(x) of many scores: while no score of the warp is above 1 in magnitude
+// (scores within the cap) a polynomial serves them all, without the special-function unit
+// that the softmax's exponentials need.  The polynomials are fitted by weighted least
+// squares to the smallest largest relative error.
+
+// In a chunk, whose softmax is bound by these instructions and rounds its weights to 2^-16
+// or less ahead of the values: within 2^-20.5, by the shortest polynomial (4 to 7
+// instructions for two scores) that the warp's largest score `top` allows.
+__device__ __forceinline__ int cap_tier(float top) {
+  return __all_sync(0xffffffffu, top <= 0.25f)  ? 0
+         : __all_sync(0xffffffffu, top <= 0.5f) ? 1
+         : __all_sync(0xffffffffu, top <= 1.f)  ? 2
+                                                : 3;
+}
+// x[i] = cap_out tanh(x[i])
 template <int N>
 __device__ __forceinline__ void cap_scores(float* x, float cap_out) {
+  float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < N; i += 2)
+    top[i / 2 % 4] = fmax3(top[i / 2 % 4], fabsf(x[i]), fabsf(x[i + 1]));
+  const int tier = cap_tier(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+  if (tier == 0) {
+    const float c[2] = {-0x1.553e5ep-2f, 0x1.07b588p-3f};
+    odd_polynomial<N>(x, cap_out, c);
+  } else if (tier == 1) {
+    const float c[3] = {-0x1.5547c6p-2f, 0x1.0e721ep-3f, -0x1.6e98e6p-5f};
+    odd_polynomial<N>(x, cap_out, c);
+  } else if (tier == 2) {
+    const float c[5] = {-0x1.554d54p-2f, 0x1.1025f6p-3f, -0x1.a815f6p-5f, 0x1.14fe9cp-6f,
+                        -0x1.99ce86p-9f};
+    odd_polynomial<N>(x, cap_out, c);
+  } else {
+    // 1 - 2 / (e^2x + 1), within 2^-22 of 1
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float e = ex2_ftz(x[i] * (2.f * kLog2e));
+      x[i] = fmaf(-2.f * cap_out, __fdividef(1.f, e + 1.f), cap_out);
+    }
+  }
+}
+
+// In a decode, whose weights may be recorded in fp32: 2^-24 before rounding, 2^-22.5 with
+// it.  x[i] = cap_out tanh(x[i]).
+template <int N>
+__device__ __forceinline__ void cap_scores_fine(float* x, float cap_out) {
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < N; i += 2) top = fmax3(top, fabsf(x[i]), fabsf(x[i + 1]));
   if (__all_sync(0xffffffffu, top <= 1.f)) {
-    const float c[7] = {1.f, -0x1.55546cp-2f, 0x1.10ecc4p-3f, -0x1.b642ecp-5f,
-                        0x1.4d9306p-6f, -0x1.9a364ap-8f, 0x1.156af0p-10f};
-    uint64_t c2[7];
-#pragma unroll
-    for (int k = 0; k < 7; ++k) c2[k] = f2_pack(c[k] * cap_out, c[k] * cap_out);
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const uint64_t v = f2_pack(x[i], x[i + 1]), z = fmul2(v, v);
-      uint64_t p = c2[6];
-#pragma unroll
-      for (int k = 5; k >= 0; --k) p = ffma2(p, z, c2[k]);
-      f2_unpack(fmul2(v, p), x[i], x[i + 1]);
-    }
+    const float c[6] = {-0x1.55546cp-2f, 0x1.10ecc4p-3f,  -0x1.b642ecp-5f,
+                        0x1.4d9306p-6f,  -0x1.9a364ap-8f, 0x1.156af0p-10f};
+    odd_polynomial<N>(x, cap_out, c);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = cap_out * tanh_score(x[i]);

@@ -99,10 +99,12 @@ __device__ __forceinline__ void odd_polynomial(float* x, float cap_out, const fl
 // or less ahead of the values: within 2^-20.5, by the shortest polynomial (4 to 7
 // instructions for two scores) that the warp's largest score `top` allows.
 __device__ __forceinline__ int cap_tier(float top) {
-  return __all_sync(0xffffffffu, top <= 0.25f)  ? 0
-         : __all_sync(0xffffffffu, top <= 0.5f) ? 1
-         : __all_sync(0xffffffffu, top <= 1.f)  ? 2
-                                                : 3;
+  // (magnitudes are in the order of their bits, NaN above all)
+  const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+  return most <= __float_as_uint(0.25f)  ? 0
+         : most <= __float_as_uint(0.5f) ? 1
+         : most <= __float_as_uint(1.f)  ? 2
+                                         : 3;
 }
 // x[i] = cap_out tanh(x[i])
 template <int N>

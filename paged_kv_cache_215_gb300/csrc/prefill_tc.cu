@@ -128,8 +128,17 @@ __device__ __forceinline__ int key_tiles(const DecodeArgs& a, int n, int qt) {
 // a cap, or with distances and perhaps a cap); each row sees its own interval of keys, and
 // the CTA reads from the first key that any of its rows sees.
 enum Rules { kNone = 0, kMasks = 1, kCap = 2, kDistance = 3 };
+// Threads of an instance.  The softmax warps of the scored ones hold a row of 64 scores
+// beside their rules: they take registers that the issuing and loading warps do not need
+// (setmaxnreg, by warpgroups of four warps, so two idle warps fill the last one up), at
+// launch 128 a thread.
 template <int KVT, int kRules>
-__global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
+constexpr int threads_of() { return kRules == kNone ? PfCfg<KVT>::kThreads : 512; }
+constexpr int kSoftmaxRegs = 160, kOtherRegs = 96;
+static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= 512 * 128, "registers");
+
+template <int KVT, int kRules>
+__global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, const DecodeArgs a) {
   using C = PfCfg<KVT>;
   constexpr bool kBf16 = C::kBf16, kFp8 = C::kFp8, kScore = kRules != kNone;
@@ -366,10 +375,12 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
   }
 
   if (warp >= kSoftmaxWarps) {
+    if constexpr (kScore)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // ------------------------------------------------------------ issuers
     // Each issuer warp walks its loop and waits as a whole (so it stays
     // converged); its lane 0 issues the MMAs and the commits.
-    if (T > 0) {
+    if (T > 0 && warp < PfCfg<KVT>::kThreads / 32) {
       const bool leader = lane == 0;
       // every lane waits; the warp agrees on the outcome
       auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -722,6 +733,8 @@ __global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
       __syncwarp();
     }
   } else {
+    if constexpr (kScore)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ------------------------------------------------------------ softmax, one row per thread
     const int t = warp / 4, r = tid - 128 * t, i = r / G, g = r % G;
     const int tok = (pair * kQT + t) * QT + i;
@@ -992,9 +1005,18 @@ cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, dim3 grid, cud
   cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<KVT, kRules>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
+  if (kRules != kNone) {
+    // the softmax warps wait for registers that only a launch with 128 a thread can give
+    static const bool enough = [] {
+      cudaFuncAttributes at{};
+      return cudaFuncGetAttributes(&at, prefill_tc_kernel<KVT, kRules>) == cudaSuccess &&
+             at.numRegs >= 128;
+    }();
+    if (!enough) return cudaErrorInvalidConfiguration;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(PfCfg<KVT>::kThreads);
+  cfg.blockDim = dim3(threads_of<KVT, kRules>());
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -130,6 +130,14 @@ __device__ __forceinline__ long long owner_of(long long b, long long T, long lon
   return ((b + 1) * P - 1) / T;
 }
 
+// a * b / c, in 32 bits where that is enough (a 64-bit division takes some 100
+// instructions, and a short call's prologue is a chain of them).
+__device__ __forceinline__ long long muldiv(long long a, long long b, long long c) {
+  const unsigned long long n = (unsigned long long)a * b;
+  if ((n | (unsigned long long)c) >> 32) return (long long)(n / c);
+  return (unsigned)n / (unsigned)c;
+}
+
 struct SmemHeader {
   uint64_t full[16];
   uint64_t empty[16];
@@ -863,10 +871,56 @@ struct Consumer {
     else return 16 * dt + (lane >> 2) + ((k >> 1) << 3);
   }
 
+  // The scored form of finish (balanced mode): the thread's two columns, rows 2c and
+  // 2c + 1 of the warp's eight.
+  __device__ __forceinline__ void finish_scored(const DecodeArgs& a, int s, int hkv, int lane,
+                                                bool whole, size_t part_base) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float L = l[0][h];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      const int r = column(2 * (lane & 3) + h);
+      if (r >= a.R) continue;
+      // a column that saw no key is empty
+      const bool empty = m[0][h] == -INFINITY;
+      float inv = empty ? 0.f : a.v_scale / L;
+      if (T::kFp8 && bscaled_) inv = ldexpf(inv, ev_ref_);
+      if (whole) {
+        const size_t row = (size_t)q_row(a, s, hkv, r) * kD;
+#pragma unroll
+        for (int dt = 0; dt < 8; ++dt)
+#pragma unroll
+          for (int k = h; k < 4; k += 2)
+            store_from_float(a.out, row + d_of(dt, k, lane), a.out_dtype, acc[dt][0][k] * inv);
+      } else {
+        float* row = a.part_o + (part_base + (size_t)r) * kD + d_of(0, 0, lane);
+#pragma unroll
+        for (int dt = 0; dt < 8; ++dt) {
+          const float x = acc[dt][0][h] * inv, y = acc[dt][0][h + 2] * inv;
+          if constexpr (T::kFp8) {
+            *reinterpret_cast<float2*>(row + 16 * dt) = make_float2(x, y);
+          } else {
+            row[16 * dt] = x;
+            row[16 * dt + 8] = y;
+          }
+        }
+        if ((lane >> 2) == 0)
+          a.part_lse[part_base + (size_t)r] =
+              empty ? -INFINITY : (m[0][h] + __log2f(L) - kPOff) * kLn2;
+      }
+    }
+    reset();
+  }
+
   // Write the piece's result: directly to out (whole = true) or as a partial
   // (balanced: rows part_base + column; fixed: part_base + q_row * S).
   __device__ __forceinline__ void finish(const DecodeArgs& a, int s, int hkv, int lane, bool whole,
                                          size_t part_base, bool balanced) {
+    if constexpr (kScore) {
+      finish_scored(a, s, hkv, lane, whole, part_base);
+      return;
+    }
     if constexpr (NT == 1 && !kCausal) {
       if (balanced) finish_decode(a, s, hkv, lane, whole, part_base, 1);
       else finish_decode(a, s, hkv, lane, whole,
@@ -919,6 +973,38 @@ __device__ __forceinline__ size_t part_base(const DecodeArgs& a, int w, long lon
   return (size_t)p;
 }
 
+// The CTA's run of the balanced stream of at most 32 sequences, a lane each (one warp;
+// the general form is in the kernel).
+template <int kMode, int BS>
+__device__ __forceinline__ void find_run_of_few(const DecodeArgs& a, SmemHeader* hdr, int lane) {
+  const int nb = lane < a.B ? blocks_of(clamp_len<kMode>(a, lane), BS) : 0;
+  if (blockIdx.x == 0 && lane < a.B && nb == 0)
+    for (int hg = 0; hg < a.NHG; ++hg) a.unit_info[(size_t)lane * a.NHG + hg] = make_int2(0, 0);
+  long long upto = (long long)nb * a.NHG;
+  const long long mine = upto;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const long long total = __shfl_sync(0xffffffffu, upto, 31);
+  const long long P = min(total, (long long)gridDim.x);
+  const bool takes_part = blockIdx.x < P;
+  const long long gb0 = takes_part ? muldiv(blockIdx.x, total, P) : 0;
+  const long long gb1 = takes_part ? muldiv(blockIdx.x + 1, total, P) : 0;
+  if (lane == 0) {
+    hdr->total = total;
+    hdr->gb0 = gb0;
+    hdr->gb1 = gb1;
+  }
+  if (takes_part && upto - mine <= gb0 && gb0 < upto) {   // one lane's
+    const int off = (int)(gb0 - (upto - mine));           // below 2^31: nb * NHG of one sequence
+    hdr->s = lane;
+    hdr->hg = off / nb;
+    hdr->j = off % nb;
+  }
+}
+
 template <int KVT, int BS, int NT, bool kCausal, int kMode>
 __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
     decode_mma_kernel(const __grid_constant__ CUtensorMap tmap, const DecodeArgs a) {
@@ -954,7 +1040,10 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
     fence_proxy_async_global();
   }
 
-  if (a.mode == 0 && warp == 0) {
+  if constexpr (kMode == kScored) {
+    if (warp == 0 && a.B <= 32) find_run_of_few<kMode, BS>(a, hdr, lane);
+  }
+  if (a.mode == 0 && warp == 0 && (kMode != kScored || a.B > 32)) {
     long long total = 0;
     for (int base = 0; base < a.B; base += 32) {
       const int s = base + lane;
@@ -1253,7 +1342,12 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
         if (first && warp == 0 && lane == 0) {
           const long long unit_first_gb = cur.gb - cur.j;
           const long long parts = hdr->total < (long long)gridDim.x ? hdr->total : (long long)gridDim.x;
-          const long long c_last = owner_of(unit_first_gb + cur.nb - 1, hdr->total, parts);
+          const long long last = unit_first_gb + cur.nb - 1;
+          const long long c_last = kMode == kScored
+                                       ? ((last + 1) * parts >> 32 ? owner_of(last, hdr->total, parts)
+                                                                   : (unsigned)((last + 1) * parts - 1) /
+                                                                         (unsigned)hdr->total)
+                                       : owner_of(last, hdr->total, parts);
           a.unit_info[u] = make_int2((int)slot, (int)(c_last - blockIdx.x + 1));
         }
       } else {

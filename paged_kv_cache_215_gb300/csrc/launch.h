@@ -123,10 +123,10 @@ inline int score_row(int R) {
   while (w < R) w *= 2;
   return w;
 }
-// Merge of a scored call's partials (balanced or fixed) and, beside it, out = in
-// (nullptr: 0) + the softmax weights of the scores in a.scores.
-cudaError_t launch_merge_accumulate(const DecodeArgs& a, const WeightRows& in,
-                                    const WeightRows& out, cudaStream_t stream);
+// Merge of a scored call's partials (balanced or fixed) and, beside it (out not nullptr),
+// *out = *in (nullptr data: 0) + the softmax weights of the scores in a.scores.
+cudaError_t launch_merge_scored(const DecodeArgs& a, const WeightRows* in, const WeightRows* out,
+                                cudaStream_t stream);
 
 struct AppendArgs {
   void* pool;

@@ -346,73 +346,147 @@ __host__ __device__ constexpr int tokens_per_cta(int row) {
   return kThreads * (row <= 4 ? 4 : row == 8 ? 2 : 1);
 }
 
+// One row of D = 128, by kGroup warps (of the whole CTA, or one alone).  A lane holds four
+// columns; the first partials are loaded together with their log-sum-exps, before the
+// largest of those is known, so that a row of few partials takes two trips to memory (its
+// place, its partials).
+template <int kGroup>
+__device__ __forceinline__ void merge_row128(const DecodeArgs& a, const RowPartials& p, int w,
+                                             int lane) {
+  constexpr int kFirst = kGroup == 1 ? 8 : 4;
+  __shared__ float tops[kGroup];
+  __shared__ float sums[kGroup];
+  __shared__ float4 cols[kGroup][32];
+  const float* lse = a.part_lse + p.first;
+  const float4* o = reinterpret_cast<const float4*>(a.part_o + p.first * 128) + lane;
+  const size_t step = p.stride * 32;               // float4s from a partial to the next
+  float4 v[kFirst];
+  float l[kFirst], M = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < kFirst; ++u) {
+    const int i = w + u * kGroup;
+    const bool in = i < p.count;
+    l[u] = in ? lse[(size_t)i * p.stride] : -INFINITY;
+    v[u] = in ? o[(size_t)i * step] : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int u = 0; u < kFirst; ++u) M = fmaxf(M, l[u]);
+  if (p.count > kFirst * kGroup) {
+    for (int i = kFirst * kGroup + w * 32 + lane; i < p.count; i += 32 * kGroup)
+      M = fmaxf(M, lse[(size_t)i * p.stride]);
+    M = warp_max(M);
+  }
+  if (kGroup > 1) {
+    if (lane == 0) tops[w] = M;
+    __syncthreads();
+    M = warp_max(lane < kGroup ? tops[lane] : -INFINITY);
+  }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float W = 0.f;
+  auto add = [&](float lse_i, const float4& x) {
+    const float f = lse_i == -INFINITY ? 0.f : exp2f((lse_i - M) * kLog2e);
+    W += f;
+    acc.x = fmaf(f, x.x, acc.x);
+    acc.y = fmaf(f, x.y, acc.y);
+    acc.z = fmaf(f, x.z, acc.z);
+    acc.w = fmaf(f, x.w, acc.w);
+  };
+#pragma unroll
+  for (int u = 0; u < kFirst; ++u) add(l[u], v[u]);
+  for (int i0 = w + kFirst * kGroup; i0 < p.count; i0 += kFirst * kGroup) {
+#pragma unroll
+    for (int u = 0; u < kFirst; ++u) {
+      const int i = i0 + u * kGroup;
+      const bool in = i < p.count;
+      l[u] = in ? lse[(size_t)i * p.stride] : -INFINITY;
+      v[u] = in ? o[(size_t)i * step] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < kFirst; ++u) add(l[u], v[u]);
+  }
+  if (kGroup > 1) {
+    cols[w][lane] = acc;
+    if (lane == 0) sums[w] = W;
+    __syncthreads();
+    if (w > 0) return;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      const float4 x = cols[g][lane];
+      acc.x += x.x;
+      acc.y += x.y;
+      acc.z += x.z;
+      acc.w += x.w;
+    }
+    W = warp_sum(lane < kGroup ? sums[lane] : 0.f);
+  }
+  const float inv = W > 0.f ? 1.f / W : 0.f;
+  const size_t at = p.q_row * 128 + 4 * lane;
+  acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  if (a.out_dtype == PKV_F32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = acc;
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+        a.out_dtype == PKV_BF16
+            ? make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w))
+            : make_uint2(pack_f16(acc.x, acc.y), pack_f16(acc.z, acc.w));
+}
+
 // CTA (x, h, s): the first CTAs along x merge the rows of (s, h) (one each, or with
-// kWarpRows a warp each), the others take its tokens.
-template <bool kWarpRows>
+// kWarpRows a warp each), the others (with a record) take its tokens.
+template <bool kWarpRows, bool kRecord>
 __global__ void __launch_bounds__(kThreads, 2)
-    merge_accumulate_kernel(const DecodeArgs a, const WeightRows in, const WeightRows out) {
+    merge_scored_kernel(const DecodeArgs a, const WeightRows in, const WeightRows out) {
   grid_launch_dependents();
   const int row_ctas = kWarpRows ? 1 : a.R, h = blockIdx.y, s = blockIdx.z;
-  if ((int)blockIdx.x >= row_ctas) {
-    const int j0 = (blockIdx.x - row_ctas) * tokens_per_cta(a.score_row);
-    switch (a.score_row) {
-      case 1: accumulate_tokens<1>(a, in, out, s, h, j0); break;
-      case 2: accumulate_tokens<2>(a, in, out, s, h, j0); break;
-      case 4: accumulate_tokens<4>(a, in, out, s, h, j0); break;
-      case 8: accumulate_tokens<8>(a, in, out, s, h, j0); break;
-      default: accumulate_tokens<16>(a, in, out, s, h, j0); break;
+  if constexpr (kRecord) {
+    if ((int)blockIdx.x >= row_ctas) {
+      const int j0 = (blockIdx.x - row_ctas) * tokens_per_cta(a.score_row);
+      switch (a.score_row) {
+        case 1: accumulate_tokens<1>(a, in, out, s, h, j0); break;
+        case 2: accumulate_tokens<2>(a, in, out, s, h, j0); break;
+        case 4: accumulate_tokens<4>(a, in, out, s, h, j0); break;
+        case 8: accumulate_tokens<8>(a, in, out, s, h, j0); break;
+        default: accumulate_tokens<16>(a, in, out, s, h, j0); break;
+      }
+      return;
     }
-    return;
   }
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31, r = kWarpRows ? threadIdx.x >> 5 : blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = kWarpRows ? warp : blockIdx.x;
   if (r >= a.R) return;
   const RowPartials p = row_partials(a, s, h, r);
+  if (!kRecord && a.mode == 0 && p.count == 1) return;     // the attention wrote this row
   if (!p.ok && threadIdx.x == 0) record_error(a.status, PKV_EBOUNDS);
-  if constexpr (kWarpRows) {
-    float M = -INFINITY;
-    for (int i = lane; i < p.count; i += 32)
-      M = fmaxf(M, a.part_lse[p.first + (size_t)i * p.stride]);
-    M = warp_max(M);
-    for (int d0 = 4 * lane; d0 < a.D; d0 += 128) {
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float W = 0.f;
-      for (int i = 0; i < p.count && M != -INFINITY; ++i) {
-        const size_t pr = p.first + (size_t)i * p.stride;
-        const float wt = exp2f((a.part_lse[pr] - M) * kLog2e);
-        const float4 v = *reinterpret_cast<const float4*>(a.part_o + pr * a.D + d0);
-        W += wt;
-        acc.x = fmaf(wt, v.x, acc.x);
-        acc.y = fmaf(wt, v.y, acc.y);
-        acc.z = fmaf(wt, v.z, acc.z);
-        acc.w = fmaf(wt, v.w, acc.w);
-      }
-      const float inv = W > 0.f ? 1.f / W : 0.f;
-      store_from_float(a.out, p.q_row * a.D + d0 + 0, a.out_dtype, acc.x * inv);
-      store_from_float(a.out, p.q_row * a.D + d0 + 1, a.out_dtype, acc.y * inv);
-      store_from_float(a.out, p.q_row * a.D + d0 + 2, a.out_dtype, acc.z * inv);
-      store_from_float(a.out, p.q_row * a.D + d0 + 3, a.out_dtype, acc.w * inv);
-    }
+  if (a.D == 128) {
+    merge_row128<kWarpRows ? 1 : kWarps>(a, p, kWarpRows ? 0 : warp, lane);
   } else {
-    merge_row(a.part_lse + p.first, p.stride, a.part_o + p.first * a.D, p.stride * a.D, p.count,
-              a.D, a.out, p.q_row * a.D, a.out_dtype);
+    // (CUDA-core shapes: a CTA each)
+    if constexpr (!kWarpRows)
+      merge_row(a.part_lse + p.first, p.stride, a.part_o + p.first * a.D, p.stride * a.D, p.count,
+                a.D, a.out, p.q_row * a.D, a.out_dtype);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_merge_accumulate(const DecodeArgs& a, const WeightRows& in,
-                                    const WeightRows& out, cudaStream_t stream) {
-  if (a.D > kMaxD || a.R > kWarps || a.score_row > 16) return cudaErrorInvalidValue;
-  if (a.B > 65535 || a.Hkv > 65535) return cudaErrorInvalidValue;
-  // as launch_merge_units
-  const bool warp_rows = (long long)a.B * a.Hkv * a.R >= 512 && a.D % 4 == 0;
+cudaError_t launch_merge_scored(const DecodeArgs& a, const WeightRows* in, const WeightRows* out,
+                                cudaStream_t stream) {
+  if (a.D > kMaxD || a.R > kWarps || a.score_row > 16 || a.B > 65535 || a.Hkv > 65535)
+    return cudaErrorInvalidValue;
+  // few rows (each of many partials): a CTA a row; else a warp
+  const bool warp_rows = (long long)a.B * a.Hkv * a.R >= 512 && a.D == 128;
   const long long token_ctas =
-      ((long long)a.max_len + tokens_per_cta(a.score_row) - 1) / tokens_per_cta(a.score_row);
+      out ? ((long long)a.max_len + tokens_per_cta(a.score_row) - 1) / tokens_per_cta(a.score_row)
+          : 0;
   const dim3 grid((unsigned)(token_ctas + (warp_rows ? 1 : a.R)), a.Hkv, a.B);
-  const cudaError_t e =
-      launch_chained(warp_rows ? merge_accumulate_kernel<true> : merge_accumulate_kernel<false>,
-                     grid, dim3(kThreads), 1, stream, a, in, out);
+  const WeightRows none{};
+  auto kernel = out ? (warp_rows ? merge_scored_kernel<true, true> : merge_scored_kernel<false, true>)
+                    : (warp_rows ? merge_scored_kernel<true, false>
+                                 : merge_scored_kernel<false, false>);
+  const cudaError_t e = launch_chained(kernel, grid, dim3(kThreads), 1, stream, a, in ? *in : none,
+                                       out ? *out : none);
   if (e == cudaSuccess) count_launch();
   return e;
 }

@@ -1462,6 +1462,13 @@ int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* 
   a.doc_starts = sc.d_doc_starts;
   a.score_row = score_row(a.R);
   char* ws = static_cast<char*>(d_workspace);
+  auto merge = [&]() -> int {
+    return launch_merge_scored(a, weights ? &w_in : nullptr, weights ? &w_out : nullptr, stream) ==
+                   cudaSuccess
+               ? PKV_OK
+               : PKV_ECUDA;
+  };
+
   const bool q_ok = fp8 ? (q_dtype == PKV_BF16 || q_dtype == PKV_F16) : (int)q_dtype == g.kv_dtype;
   if (q_ok && mma_scored_supported(g.kv_dtype, g.block_size, g.head_dim, G, q_len)) {
     MmaPlan plan;
@@ -1481,9 +1488,7 @@ int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* 
     a.early_trigger = fp8 ? 0 : 1;
     if (weights) a.scores = reinterpret_cast<float*>(ws + w.scores);
     if (launch_decode_mma_scored(map, a, plan.grid, stream) != cudaSuccess) return PKV_ECUDA;
-    const cudaError_t e = weights ? launch_merge_accumulate(a, w_in, w_out, stream)
-                                  : launch_merge_units(a, true, stream);
-    return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
+    return merge();
   }
   if (q_len > 1) {
     // chunks with more query rows than the decode kernel holds
@@ -1506,11 +1511,7 @@ int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* 
   a.mode = 1;
   if (launch_decode_simt_scored(a, stream) != cudaSuccess) return PKV_ECUDA;
   if (w.bytes == 0) return PKV_OK;                 // one split: out is written
-  const cudaError_t e =
-      weights ? launch_merge_accumulate(a, w_in, w_out, stream)
-              : launch_merge_rows(d_out, out_dtype, a.part_o, a.part_lse, batch * g.num_q_heads, S,
-                                  g.head_dim, true, stream);
-  return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
+  return merge();
 }
 
 // ---------------------------------------------------------------- eviction

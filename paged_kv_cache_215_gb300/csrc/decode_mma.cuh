@@ -46,7 +46,15 @@ namespace mma {
 
 // What an instance reads of a sequence: all of it; from the end of its shared prefix
 // on (a.len_off set); or what its queries see under the rules of score.cuh.
-enum Mode { kPlain = 0, kSuffix = 1, kScored = 2 };
+// (The scored instances for one query token, up to 8 rows and no slopes have the plain
+// decode's inner loop: with the general form's branches in it the compiler keeps less of a
+// block's work in flight, 64 us against 56 for 128K tokens on an E4M3 pool.)
+enum Mode { kPlain = 0, kSuffix = 1, kScored = 2, kOne = 4, kOneCap = 5, kOneRecord = 6,
+            kOneCapRecord = 7 };
+__host__ __device__ constexpr bool is_scored(int mode) { return mode >= kScored; }
+__host__ __device__ constexpr bool is_one(int mode) { return mode >= kOne; }
+__host__ __device__ constexpr bool one_cap(int mode) { return is_one(mode) && (mode & 1); }
+__host__ __device__ constexpr bool one_record(int mode) { return is_one(mode) && (mode & 2); }
 
 constexpr int kD = 128;            // head_dim of this kernel
 constexpr int kMaxHG = 8;          // consumer warps per CTA
@@ -88,7 +96,7 @@ struct Cursor {
 
 template <int kMode>
 __device__ __forceinline__ int clamp_len(const DecodeArgs& a, int s) {
-  if constexpr (kMode == kScored) {
+  if constexpr (is_scored(kMode)) {
     const int n = scored_len(a, s);
     return n - first_read(a, s, n);
   }
@@ -163,9 +171,12 @@ constexpr int kWarpColumns = 8;
 // sees keys 0 .. that position (causal within the chunk; q_len = 1 is plain
 // decode).
 
-template <int KVT, int BS, int NT, bool kCausal, bool kScore = false>
+template <int KVT, int BS, int NT, bool kCausal, int kMode = kPlain>
 struct Consumer {
   using T = KvTraits<KVT>;
+  static constexpr bool kScore = is_scored(kMode);
+  // the single-token forms of the inner loop
+  static constexpr bool kSingle = NT == 1 && (!kCausal || is_one(kMode));
   static constexpr int kTiles = BS / 16;
   static constexpr bool kSplitP = T::kBf16Mma;   // bf16 P is split into hi + lo parts
   // f16 P (f16 and E4M3 pools) is computed as 2^(s - m + kPOff): the largest
@@ -237,8 +248,9 @@ struct Consumer {
   }
 
   __device__ __forceinline__ void load_q(const DecodeArgs& a, int s, int n, int hkv, int lane) {
-    if constexpr (NT == 1 && !kCausal) {
+    if constexpr (kSingle) {
       load_q_decode(a, s, hkv, lane);
+      if constexpr (kScore) load_rules_one(a, s, n, hkv);
       return;
     }
     const int c = lane & 3;
@@ -294,6 +306,16 @@ struct Consumer {
         if constexpr (kCausal && !kScore) lim[nt][h] = r < a.R ? n - a.q_len + r / a.G : n - 1;
       }
     }
+  }
+
+  // One query token: its first and last key of the n tokens that the unit reads.
+  __device__ __forceinline__ void load_rules_one(const DecodeArgs& a, int s, int n, int hkv) {
+    const int len = scored_len(a, s), off = len - n;
+    const KeyRange k = key_range(a, s, len, 0);
+    from_min = k.lo - off;
+    lim_max = k.hi - 1 - off;
+    if constexpr (one_record(kMode))
+      score_rows = a.scores + (((int64_t)s * a.Hkv + hkv) * a.max_len + off) * a.score_row;
   }
 
   // The columns' rules in a unit that reads n tokens.
@@ -352,30 +374,60 @@ struct Consumer {
             }
         }
     }
-    if (score_rows) {
+    if (score_rows) record(a, s, jbase, valid, lane);
+  }
+
+  __device__ __forceinline__ void record_one(const DecodeArgs& a, const float (&s)[kTiles][4],
+                                             int jbase, int valid, int lane) {
+    const int c = lane & 3;
+    float* row = score_rows + (int64_t)(jbase + (lane >> 2)) * a.score_row + 2 * c;
 #pragma unroll
-      for (int mt = 0; mt < kTiles; ++mt)
+    for (int mt = 0; mt < kTiles; ++mt)
 #pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-          const int t = mt * 16 + (lane >> 2) + ((k >> 1) << 3);
-          if (t >= valid) continue;
-          float* row = score_rows + (int64_t)(jbase + t) * a.score_row;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            if (a.score_row == 1) {
-              if (c == 0) row[0] = s[mt][nt][k];
-            } else if (col0 + nt * 8 + 2 * c < a.score_row) {
-              *reinterpret_cast<float2*>(row + nt * 8 + 2 * c) =
-                  make_float2(s[mt][nt][k], s[mt][nt][k + 1]);
-            }
+      for (int k = 0; k < 4; k += 2) {
+        const int t = mt * 16 + ((k >> 1) << 3);
+        if (t + (lane >> 2) >= valid) continue;
+        if (a.score_row == 1) {
+          if (c == 0) row[t] = s[mt][k];
+        } else if (2 * c < a.score_row) {
+          *reinterpret_cast<float2*>(row + t * a.score_row) = make_float2(s[mt][k], s[mt][k + 1]);
         }
-    }
+      }
+  }
+
+  // The block's scores of the tokens before `valid` into the record.
+  __device__ __forceinline__ void record(const DecodeArgs& a, const float (&s)[kTiles][NT][4],
+                                         int jbase, int valid, int lane) {
+    const int c = lane & 3;
+#pragma unroll
+    for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        const int t = mt * 16 + (lane >> 2) + ((k >> 1) << 3);
+        if (t >= valid) continue;
+        float* row = score_rows + (int64_t)(jbase + t) * a.score_row;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          if (a.score_row == 1) {
+            if (c == 0) row[0] = s[mt][nt][k];
+          } else if (col0 + nt * 8 + 2 * c < a.score_row) {
+            *reinterpret_cast<float2*>(row + nt * 8 + 2 * c) =
+                make_float2(s[mt][nt][k], s[mt][nt][k + 1]);
+          }
+      }
   }
 
   // The single-token path (one query token, G <= 8 heads as the 8 columns).
   // ks_b / vs_b: the block's own E4M3 scales (block-wise scaling), else 1.
-  __device__ __forceinline__ void block_decode(uint32_t kbase, uint32_t vbase, uint32_t region_bytes,
-                                        int row0, int valid, int lane, float ks_b, float vs_b) {
+  __device__ __forceinline__ void block_decode(const DecodeArgs& a, uint32_t kbase, uint32_t vbase,
+                                        uint32_t region_bytes, int row0, int jbase, int valid,
+                                        int lane, float ks_b, float vs_b) {
+    // scored: keys [first, valid) of the block are seen
+    int first = 0;
+    if constexpr (kScore) {
+      first = from_min - jbase;
+      valid = min(valid, lim_max + 1 - jbase);
+    }
     const int c = lane & 3;
     const uint32_t sw = lane & 7;   // every ldmatrix row index is congruent to lane mod 8
     float s[kTiles][4];
@@ -417,12 +469,21 @@ struct Consumer {
     }
 
     // ---- online softmax (log2 domain); thread holds tokens lane/4 (+8), heads 2c, 2c+1
-    const float qs = T::kFp8 ? qk_scale_log2_ * ks_b : qk_scale_log2_;
+    float qs = T::kFp8 ? qk_scale_log2_ * ks_b : qk_scale_log2_;
+    if constexpr (one_cap(kMode)) {
+      scale_scores<kTiles * 4>(&s[0][0], T::kFp8 ? cap_in_ * ks_b : cap_in_);
+      cap_scores_fine<kTiles * 4>(&s[0][0], a.cap_out);
+      qs = 1.f;
+    }
     float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
     for (int mt = 0; mt < kTiles; ++mt) {
       const int t0 = mt * 16 + (lane >> 2);
-      const bool v0 = t0 < valid, v1 = t0 + 8 < valid;
+      bool v0 = t0 < valid, v1 = t0 + 8 < valid;
+      if constexpr (kScore) {
+        v0 = v0 && t0 >= first;
+        v1 = v1 && t0 + 8 >= first;
+      }
       s[mt][0] = v0 ? s[mt][0] * qs : -INFINITY;
       s[mt][1] = v0 ? s[mt][1] * qs : -INFINITY;
       s[mt][2] = v1 ? s[mt][2] * qs : -INFINITY;
@@ -430,6 +491,7 @@ struct Consumer {
       mx0 = fmaxf(mx0, fmaxf(s[mt][0], s[mt][2]));
       mx1 = fmaxf(mx1, fmaxf(s[mt][1], s[mt][3]));
     }
+    if constexpr (one_record(kMode)) record_one(a, s, jbase, valid, lane);
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
@@ -484,15 +546,16 @@ struct Consumer {
     // ---- O^T += V^T P^T
     // Rows of V past the sequence's end are unwritten slots: their lanes are
     // zeroed (only in a tail block) so that 0 * NaN never reaches the sum.
-    const bool tail = valid < BS;
+    const bool tail = valid < BS || (kScore && first > 0);
 #pragma unroll
     for (int mt = 0; mt < kTiles; ++mt) {
       // tokens of this thread in the A fragment: 2c, 2c+1 (regs 0,1) and 8+2c, 9+2c (regs 2,3)
       uint32_t mk_lo = 0xffffffffu, mk_hi = 0xffffffffu;
       if (tail) {
         const int tl = mt * 16 + 2 * c;
-        mk_lo = (tl < valid ? 0x0000ffffu : 0u) | (tl + 1 < valid ? 0xffff0000u : 0u);
-        mk_hi = (tl + 8 < valid ? 0x0000ffffu : 0u) | (tl + 9 < valid ? 0xffff0000u : 0u);
+        auto in = [&](int t) { return t < valid && (!kScore || t >= first); };
+        mk_lo = (in(tl) ? 0x0000ffffu : 0u) | (in(tl + 1) ? 0xffff0000u : 0u);
+        mk_hi = (in(tl + 8) ? 0x0000ffffu : 0u) | (in(tl + 9) ? 0xffff0000u : 0u);
       }
       if constexpr (!T::kFp8) {
         const int q4 = lane >> 3;
@@ -566,6 +629,7 @@ struct Consumer {
       const int e = f16_fit_exponent(warp_max(amax));
       const float qscale = pow2i(e);
       qk_scale_log2_ = a.qk_scale_log2 * pow2i(-e);
+      if constexpr (kScore) cap_in_ = a.cap_in * pow2i(-e);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
         qf[0][kk][0] = pack_f16(x[kk][0] * qscale, x[kk][1] * qscale);
@@ -576,8 +640,8 @@ struct Consumer {
       for (int kk = 0; kk < 8; ++kk) {
         const uint32_t* qp = reinterpret_cast<const uint32_t*>(
             static_cast<const uint16_t*>(a.q) + row + 16 * kk + 2 * c);
-        qf[0][kk][0] = live ? __ldg(qp) : 0u;
-        qf[0][kk][1] = live ? __ldg(qp + 4) : 0u;
+        qf[0][kk][0] = !live ? 0u : kScore ? qp[0] : __ldg(qp);
+        qf[0][kk][1] = !live ? 0u : kScore ? qp[4] : __ldg(qp + 4);
       }
     }
   }
@@ -634,8 +698,8 @@ struct Consumer {
   __device__ __forceinline__ void block(const DecodeArgs& a, uint32_t kbase, uint32_t vbase,
                                         uint32_t region_bytes, int row0, int jbase, int valid,
                                         bool full, int lane, float ks_b, float vs_b) {
-    if constexpr (NT == 1 && !kCausal) {
-      block_decode(kbase, vbase, region_bytes, row0, valid, lane, ks_b, vs_b);
+    if constexpr (kSingle) {
+      block_decode(a, kbase, vbase, region_bytes, row0, jbase, valid, lane, ks_b, vs_b);
       return;
     }
     const int c = lane & 3;
@@ -921,7 +985,7 @@ struct Consumer {
       finish_scored(a, s, hkv, lane, whole, part_base);
       return;
     }
-    if constexpr (NT == 1 && !kCausal) {
+    if constexpr (kSingle) {
       if (balanced) finish_decode(a, s, hkv, lane, whole, part_base, 1);
       else finish_decode(a, s, hkv, lane, whole,
                          part_base + ((size_t)s * a.Hq + (size_t)hkv * a.G) * a.S, a.S);
@@ -1033,17 +1097,17 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
     fence_mbar_init();
   }
   if (warp == producer && lane == 0) prefetch_tensormap(&tmap);
-  if constexpr (kMode == kScored) {
+  if constexpr (is_scored(kMode)) {
     // scheduled while the launches ahead finish; the fence puts their writes to the pool
     // ahead of this grid's TMA reads
     grid_dependency_wait();
     fence_proxy_async_global();
   }
 
-  if constexpr (kMode == kScored) {
+  if constexpr (is_scored(kMode)) {
     if (warp == 0 && a.B <= 32) find_run_of_few<kMode, BS>(a, hdr, lane);
   }
-  if (a.mode == 0 && warp == 0 && (kMode != kScored || a.B > 32)) {
+  if (a.mode == 0 && warp == 0 && (!is_scored(kMode) || a.B > 32)) {
     long long total = 0;
     for (int base = 0; base < a.B; base += 32) {
       const int s = base + lane;
@@ -1155,9 +1219,9 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
         if constexpr (kMode == kSuffix)
           jo = first_token(a, cur.s, min(max(__ldg(a.seq_lens + cur.s), 0), a.max_blocks * BS)) /
                BS;
-        if constexpr (kMode == kScored) jo = (scored_len(a, cur.s) - cur.n) / BS;
+        if constexpr (is_scored(kMode)) jo = (scored_len(a, cur.s) - cur.n) / BS;
         const int32_t* entry = a.tables + (size_t)cur.s * a.max_blocks + jo + jj;
-        ids = jj >= cur.nb ? 0 : kMode == kScored ? *entry : __ldg(entry);
+        ids = jj >= cur.nb ? 0 : is_scored(kMode) ? *entry : __ldg(entry);
       }
       int blk = __shfl_sync(0xffffffffu, ids, cur.j - id_base);
       const bool blk_ok = blk >= 0 && blk < a.num_blocks;
@@ -1256,12 +1320,12 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
   }
 
   // a scored call has a consumer warp for every 8 query rows of a KV head, else one
-  const int row_warps = kMode == kScored ? (a.R + kWarpColumns - 1) / kWarpColumns : 1;
+  const int row_warps = is_scored(kMode) ? (a.R + kWarpColumns - 1) / kWarpColumns : 1;
   if (warp >= a.HG * row_warps) return;   // no spare warps are launched; guard anyway
 
   // ---------------------------------------------------------------- consumers
-  constexpr bool kScore = kMode == kScored;
-  Consumer<KVT, BS, NT, kCausal, kScore> cons;
+  constexpr bool kScore = is_scored(kMode);
+  Consumer<KVT, BS, NT, kCausal, kMode> cons;
   cons.qk_scale_log2_ = a.qk_scale_log2;
   if constexpr (kScore) {
     cons.cap_in_ = a.cap_in;
@@ -1279,7 +1343,7 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
   if (a.mode == 1 && cur.remaining <= 0) {
     if (a.pdl) grid_dependency_wait();
     for (int r = 0; r < a.R; ++r) {
-      const long long qr = Consumer<KVT, BS, NT, kCausal, kScore>::q_row(a, cur.s, hkv, r);
+      const long long qr = Consumer<KVT, BS, NT, kCausal, kMode>::q_row(a, cur.s, hkv, r);
       if (a.S == 1) {
         for (int d = lane; d < kD; d += 32) store_from_float(a.out, (size_t)qr * kD + d, a.out_dtype, 0.f);
       } else {
@@ -1310,7 +1374,7 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
     const int valid = min(BS, cur.n - cur.j * BS);
     const int jbase = cur.j * BS;
     bool full = !kCausal || jbase + BS - 1 <= cur.n - a.q_len;
-    if constexpr (kScore) full = jbase >= cons.from_max && jbase + BS - 1 <= cons.lim_min;
+    if constexpr (kMode == kScored) full = jbase >= cons.from_max && jbase + BS - 1 <= cons.lim_min;
     float ks_b = 1.f, vs_b = 1.f;
     if (T::kFp8 && a.block_scales) {
       ks_b = hdr->bscale[stage][0][w];
@@ -1343,7 +1407,7 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
           const long long unit_first_gb = cur.gb - cur.j;
           const long long parts = hdr->total < (long long)gridDim.x ? hdr->total : (long long)gridDim.x;
           const long long last = unit_first_gb + cur.nb - 1;
-          const long long c_last = kMode == kScored
+          const long long c_last = is_scored(kMode)
                                        ? ((last + 1) * parts >> 32 ? owner_of(last, hdr->total, parts)
                                                                    : (unsigned)((last + 1) * parts - 1) /
                                                                          (unsigned)hdr->total)
@@ -1373,7 +1437,7 @@ cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, int gx, int gy
   // the ring needs mma_smem_bytes; a larger request (a.smem_bytes) caps how many
   // CTAs can share an SM
   const int consumers =
-      kMode == kScored ? a.HG * ((a.R + kWarpColumns - 1) / kWarpColumns) : a.HG;
+      is_scored(kMode) ? a.HG * ((a.R + kWarpColumns - 1) / kWarpColumns) : a.HG;
   if (consumers > kMaxHG) return cudaErrorInvalidValue;
   const size_t rules = kMode == kScored ? consumers * kWarpColumns * sizeof(ColumnRule) : 0;
   const size_t smem = std::max(mma_smem_bytes(KVT, BS, a.HG, a.stages) + rules,
@@ -1391,7 +1455,7 @@ cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, int gx, int gy
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   // (a scored launch waits for the launches ahead before it reads or writes anything)
-  cfg.numAttrs = a.pdl || kMode == kScored ? 1 : 0;
+  cfg.numAttrs = a.pdl || is_scored(kMode) ? 1 : 0;
   e = cudaLaunchKernelEx(&cfg, kern, *map, a);
   if (e == cudaSuccess) count_launch();
   return e;

@@ -110,13 +110,15 @@ __device__ __forceinline__ void grid_launch_dependents() {
 }
 // Launch with programmatic dependent launch: the grid is scheduled while the launch
 // before it finishes, so `kernel` begins with grid_dependency_wait().  cluster: CTAs
-// of a cluster along x.
+// of a cluster along x; smem: dynamic shared memory.
 template <typename... P, typename... A>
-inline cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, unsigned cluster,
-                                  cudaStream_t stream, A... args) {
+inline cudaError_t launch_chained_smem(void (*kernel)(P...), dim3 grid, dim3 block,
+                                       unsigned cluster, size_t smem, cudaStream_t stream,
+                                       A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -129,6 +131,11 @@ inline cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, u
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
   if (e != cudaSuccess) cudaGetLastError();   // the caller gets e, not the next launch
   return e;
+}
+template <typename... P, typename... A>
+inline cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, unsigned cluster,
+                                  cudaStream_t stream, A... args) {
+  return launch_chained_smem(kernel, grid, block, cluster, 0, stream, args...);
 }
 
 // ---------------------------------------------------------------- ldmatrix / movmatrix / mma

@@ -27,6 +27,7 @@ constexpr int kMaxCtas = 16;                 // of a cluster
 constexpr int kDigits = 3;
 constexpr int kFlight = 8;                   // weights a thread loads at a time
 constexpr int kList = 64;                    // keys a warp remembers of its last pass
+constexpr int kStaged = 1024;                // slots a warp keeps in shared memory at most
 __device__ __forceinline__ int digit_bits(int d) { return d == 0 ? 11 : 10; }
 __device__ __forceinline__ int digit_shift(int d) { return 20 - 10 * d; }
 
@@ -110,8 +111,11 @@ __device__ __forceinline__ int2 ahead_of_warp(int2 mine, int2* warps, int2* tota
 
 // A cluster of `ctas` CTAs a row: index[t] = source slot of kept token t, the new weights
 // and the new length.  A warp takes neighbouring slots, 32 at a time, so that ballots give
-// their order; every pass reads the weights again (from L1 or L2).
-__global__ void __launch_bounds__(kThreads, 2) select_kernel(const EvictArgs a, int ctas) {
+// their order.  The first pass leaves the weights in shared memory where they fit (staged:
+// the slots a warp has room for); later ones read them there, or again from L1 or L2.
+__global__ void __launch_bounds__(kThreads, 2)
+    select_kernel(const EvictArgs a, int ctas, int staged) {
+  extern __shared__ float stage[];
   __shared__ __align__(16) int hists[2048 + 2 * 1024];
   __shared__ int2 warps[kWarps];
   __shared__ int2 counted;                        // this CTA's (above, equal)
@@ -128,33 +132,46 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const EvictArgs a, 
   float* wo = a.w_out.data + s * a.w_out.seq_stride + h * a.w_out.head_stride;
   int32_t* index = a.index + ((int64_t)s * a.Hkv + h) * a.index_row;
 
-  // the warp's slots
+  // the recent tokens, and zeros behind
+  for (int i = rank * kThreads + tid; i < p.r; i += ctas * kThreads) {
+    index[p.k - p.r + i] = m + i;
+    wo[p.k - p.r + i] = w[m + i];
+  }
+  for (int t = p.k + rank * kThreads + tid; t < a.width; t += ctas * kThreads) wo[t] = 0.f;
+  if (h == 0 && rank == 0 && tid == 0) a.new_lens[s] = p.k;
+
+  // the others: the warp's slots [lo, hi)
   const int warps_all = ctas * kWarps;
-  const int share = ((p.n + warps_all - 1) / warps_all + 31) / 32 * 32;
+  const int share = ((m + warps_all - 1) / warps_all + 31) / 32 * 32;
   const int64_t begin = (int64_t)(rank * kWarps + warp) * share;
-  const int lo = (int)min((int64_t)p.n, begin), hi = (int)min((int64_t)p.n, begin + share);
-  // f(slot, weight, valid) for the warp's slots up to `end`, 32 at a time; whole warps
-  auto each = [&](int end, auto f) {
+  const int lo = (int)min((int64_t)m, begin), hi = (int)min((int64_t)m, begin + share);
+  const float* src = w + lo;
+  // f(i, weight, valid) for the slots lo + i, 32 at a time; whole warps
+  auto each = [&](auto f) {
 #pragma unroll 1
-    for (int j0 = lo; j0 < end; j0 += 32 * kFlight) {
+    for (int i0 = 0; i0 < hi - lo; i0 += 32 * kFlight) {
       float x[kFlight];
 #pragma unroll
       for (int u = 0; u < kFlight; ++u) {
-        const int j = j0 + u * 32 + lane;
-        x[u] = j < end ? w[j] : 0.f;
+        const int i = i0 + u * 32 + lane;
+        x[u] = i < hi - lo ? src[i] : 0.f;
       }
 #pragma unroll
       for (int u = 0; u < kFlight; ++u)
-        if (j0 + u * 32 < end) f(j0 + u * 32 + lane, x[u], j0 + u * 32 + lane < end);
+        if (i0 + u * 32 < hi - lo)
+          f(i0 + u * 32 + lane, x[u], i0 + u * 32 + lane < hi - lo);
     }
   };
 
-  // the threshold: keys above it are kept, and the first `need` equal to it
-  uint32_t top = 0, mask = 0;                     // mask: the digits that are settled
+  // the threshold: keys above it are kept, and the first `need` equal to it, as far as the
+  // settled digits (mask) go.  All candidates: no digit is settled and they are all equal.
+  uint32_t top = 0, mask = 0;
   int higher = 0, listed = kList + 1;             // of the warp, in the last pass
   const uint32_t lower = (1u << lane) - 1;
-  const bool all = need >= m, none = need <= 0;
-  if (!all && !none) {
+  if (need <= 0) {                                // none: no key is as large
+    top = mask = 0xffffffffu;
+  } else if (need < m) {
+    float* mine = staged >= share ? stage + warp * staged : nullptr;
     for (int i = tid; i < 4096; i += kThreads) hists[i] = 0;
     __syncthreads();
 #pragma unroll 1
@@ -164,10 +181,12 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const EvictArgs a, 
       int zeros = 0;                              // zeros would queue at one counter
       higher = 0;
       listed = d == 0 ? kList + 1 : 0;            // (the first pass leaves all keys open)
-      each(min(hi, m), [&](int, float x, bool valid) {
+      each([&](int i, float x, bool valid) {
         const uint32_t key = weight_key(x);
         const bool in = valid && (key & mask) == top;
-        if (d > 0) {
+        if (d == 0) {
+          if (mine && valid) mine[i] = x;
+        } else {
           // the settled digits decide most keys: what they leave open is remembered
           higher += __popc(__ballot_sync(0xffffffffu, valid && (key & mask) > top));
           const uint32_t open = __ballot_sync(0xffffffffu, in);
@@ -180,6 +199,10 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const EvictArgs a, 
         if (in && key != 0u) atomicAdd(hist + ((key >> shift) & (bins - 1)), 1);
       });
       if (lane == 0 && zeros > 0) atomicAdd(hist, zeros);
+      if (d == 0 && mine) {
+        __syncwarp();
+        src = mine;
+      }
       if (ctas > 1) cluster_sync();
       else __syncthreads();
       // thread i: four bins, the highest first
@@ -225,15 +248,12 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const EvictArgs a, 
       if (need == found[2]) break;                // the whole bin is kept
     }
   }
-  if (all) need = m;
 
-  // .x counts the tokens above the threshold (or recent), .y those equal to its digits
-  auto above = [&](int j, uint32_t key) { return j >= m || (!all && !none && (key & mask) > top); };
-  auto equal = [&](int j, uint32_t key) { return j < m && !none && (all || (key & mask) == top); };
+  // .x counts the tokens above the threshold, .y those equal to its digits
   int2 mine = make_int2(0, 0), total;
   if (listed <= kList) {
     __syncwarp();
-    mine.x = higher + max(0, hi - max(lo, m));    // and the recent ones
+    mine.x = higher;
     for (int i0 = 0; i0 < listed; i0 += 32) {
       const bool in = i0 + lane < listed;
       const uint32_t key = in ? lists[warp][i0 + lane] & mask : 0u;
@@ -241,10 +261,10 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const EvictArgs a, 
       mine.y += __popc(__ballot_sync(0xffffffffu, in && key == top));
     }
   } else {
-    each(hi, [&](int j, float x, bool valid) {
-      const uint32_t key = weight_key(x);
-      mine.x += __popc(__ballot_sync(0xffffffffu, valid && above(j, key)));
-      mine.y += __popc(__ballot_sync(0xffffffffu, valid && equal(j, key)));
+    each([&](int, float x, bool valid) {
+      const uint32_t key = weight_key(x) & mask;
+      mine.x += __popc(__ballot_sync(0xffffffffu, valid && key > top));
+      mine.y += __popc(__ballot_sync(0xffffffffu, valid && key == top));
     });
   }
   int2 at = ahead_of_warp(mine, warps, &total);
@@ -257,21 +277,19 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const EvictArgs a, 
       at.y += v.y;
     }
   }
-  each(hi, [&](int j, float x, bool valid) {
-    const uint32_t key = weight_key(x);
-    const bool up = valid && above(j, key), eq = valid && equal(j, key);
+  each([&](int i, float x, bool valid) {
+    const uint32_t key = weight_key(x) & mask;
+    const bool up = valid && key > top, eq = valid && key == top;
     const uint32_t ups = __ballot_sync(0xffffffffu, up), eqs = __ballot_sync(0xffffffffu, eq);
     const int e = at.y + __popc(eqs & lower);
     if (up || (eq && e < need)) {
       const int t = at.x + __popc(ups & lower) + min(e, need);
-      index[t] = j;
+      index[t] = lo + i;
       wo[t] = x;
     }
     at.x += __popc(ups);
     at.y += __popc(eqs);
   });
-  for (int t = p.k + rank * kThreads + tid; t < a.width; t += ctas * kThreads) wo[t] = 0.f;
-  if (h == 0 && rank == 0 && tid == 0) a.new_lens[s] = p.k;
   if (ctas > 1) cluster_sync();                   // the others have read this CTA's counts
 }
 
@@ -283,9 +301,9 @@ constexpr int kCopyTokens = 16;
 constexpr int kCopyFlight = 2;
 __global__ void __launch_bounds__(kCopyThreads, 16) copy_kernel(const EvictArgs a) {
   // neighbouring CTAs take a block's heads: their rows are neighbours in the pool; the
-  // last tokens go first
-  const int h = blockIdx.x, s = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t0 = ((gridDim.y - 1 - blockIdx.y) * (kCopyThreads / 32) + warp) * kCopyTokens;
+  // last tokens of all sequences go first
+  const int h = blockIdx.x, s = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t0 = ((gridDim.z - 1 - blockIdx.z) * (kCopyThreads / 32) + warp) * kCopyTokens;
   const Plan p = plan_of(a, s);
   const bool recent = t0 >= p.k - p.r;            // all of the warp's tokens
   if (t0 >= p.k || !recent) grid_dependency_wait();
@@ -352,14 +370,21 @@ cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t grid = (int64_t)a.B * a.Hkv * ctas;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  e = launch_chained(select_kernel, dim3((unsigned)grid), dim3(kThreads), ctas, stream, a, ctas);
+  const int share = ((a.max_len + ctas * kWarps - 1) / (ctas * kWarps) + 31) / 32 * 32;
+  const int staged = share <= kStaged ? share : 0;
+  const size_t smem = sizeof(float) * kWarps * staged;
+  e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)(sizeof(float) * kWarps * kStaged));
+  if (e != cudaSuccess) return e;
+  e = launch_chained_smem(select_kernel, dim3((unsigned)grid), dim3(kThreads), ctas, smem, stream,
+                          a, ctas, staged);
   if (e != cudaSuccess) return e;
   count_launch();
   const int per_cta = kCopyThreads / 32 * kCopyTokens;
   const int tiles = (std::min(a.max_len, a.capacity) + per_cta - 1) / per_cta;
   if (tiles == 0) return cudaSuccess;
   if (tiles > 65535) return cudaErrorInvalidValue;
-  e = launch_chained(copy_kernel, dim3(a.Hkv, tiles, a.B), dim3(kCopyThreads), 1, stream, a);
+  e = launch_chained(copy_kernel, dim3(a.Hkv, a.B, tiles), dim3(kCopyThreads), 1, stream, a);
   if (e == cudaSuccess) count_launch();
   return e;
 }

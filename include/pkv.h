@@ -561,8 +561,10 @@ typedef struct {
  * A length above max_seq_len (or below 0) is limited to it and records PKV_EBOUNDS.
  * d_workspace: paged_decode_scored_workspace_bytes bytes, 16-byte aligned; with weights
  * it holds every score of the call (4 bytes for each query row and token).
- * Kernels, types and shapes as in paged_decode_attention_mq with num_splits = 0;
- * weights take up to 16 query rows per KV head, else PKV_EUNSUPPORTED.  PKV_EINVAL also for a cap or window below 0, a cap that is not
+ * Types and shapes as in paged_decode_attention_mq with num_splits = 0, and for q_len = 1
+ * any head_dim (a multiple of 8; other than 128, with f32 pools or with f32 q on the CUDA
+ * cores) and up to 16 query heads per KV head; weights take up to 16 query rows per KV
+ * head; else PKV_EUNSUPPORTED.  PKV_EINVAL also for a cap or window below 0, a cap that is not
  * finite, and scale / cap not finite in fp32. */
 PKV_API int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* d_q,
                                           pkv_dtype q_dtype, int q_len, const pkv_pool* pool,

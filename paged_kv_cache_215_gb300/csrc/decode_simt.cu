@@ -12,7 +12,6 @@
 // warps' states are combined through shared memory at the end.
 #include "device.cuh"
 #include "launch.h"
-#include "score.cuh"
 
 namespace pkv {
 namespace {
@@ -33,9 +32,7 @@ __device__ __forceinline__ float load_kv(const void* pool, size_t idx) {
   }
 }
 
-// kScore: a scored call (score.cuh); the partitions cut the blocks that hold seen keys,
-// and with a.scores every partition leaves a partial.
-template <int KVT, bool kScore>
+template <int KVT>
 __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeArgs a) {
   const int p = blockIdx.x, hkv = blockIdx.y, s = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -53,32 +50,12 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
     n = n < 0 ? 0 : cap;
   }
   const int nb = (n + a.BS - 1) / a.BS;
-  int jb = (int)((long long)p * nb / a.S), je = (int)((long long)(p + 1) * nb / a.S);
-  int tb = jb * a.BS, te = min(je * a.BS, n);
-  float q_scale = a.qk_scale_log2;
-  int first = 0;
-  if constexpr (kScore) {
-    if (n > a.max_len) {
-      if (threadIdx.x == 0) record_error(a.status, PKV_EBOUNDS);
-      n = a.max_len;
-    }
-    const KeyRange keys = key_range(a, s, n, 0);
-    const int b0 = keys.lo < keys.hi ? keys.lo / a.BS : 0;
-    const int blocks = keys.lo < keys.hi ? (keys.hi + a.BS - 1) / a.BS - b0 : 0;
-    first = b0 * a.BS;
-    jb = b0 + (int)((long long)p * blocks / a.S);
-    je = b0 + (int)((long long)(p + 1) * blocks / a.S);
-    tb = max(jb * a.BS, keys.lo);
-    te = min(je * a.BS, keys.hi);
-    if (a.cap_in != 0.f) q_scale = a.cap_in;
-    // the record covers the first block from its first token on
-    if (a.scores && blocks > 0 && jb == b0)
-      for (int i = threadIdx.x; i < (tb - first) * a.score_row; i += blockDim.x)
-        a.scores[(((int64_t)s * a.Hkv + hkv) * a.max_len + first) * a.score_row + i] = -INFINITY;
-  }
+  const int jb = (int)((long long)p * nb / a.S), je = (int)((long long)(p + 1) * nb / a.S);
+  const int tb = jb * a.BS, te = min(je * a.BS, n);
 
   for (int i = threadIdx.x; i < G * D; i += blockDim.x)
-    qs[i] = load_as_float(a.q, ((size_t)s * a.Hq + (size_t)hkv * G) * D + i, a.q_dtype) * q_scale;
+    qs[i] = load_as_float(a.q, ((size_t)s * a.Hq + (size_t)hkv * G) * D + i, a.q_dtype) *
+            a.qk_scale_log2;
   __syncthreads();
 
   float m[kMaxG], l[kMaxG], acc[kMaxG][kMaxDL];
@@ -120,14 +97,7 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
 #pragma unroll
         for (int k = 0; k < kMaxDL; ++k)
           if (k < DL) part = fmaf(kr[k], qs[g * D + lane + 32 * k], part);
-        float sc = warp_sum(part);
-        if constexpr (kScore) {
-          if (a.cap_in != 0.f) sc = a.cap_out * tanh_score(sc);
-          if (a.slopes)
-            sc = fmaf(-kLog2e * __ldg(a.slopes + hkv * G + g), (float)(n - 1 - t), sc);
-          if (a.scores && lane == 0)
-            a.scores[(((int64_t)s * a.Hkv + hkv) * a.max_len + t) * a.score_row + g] = sc;
-        }
+        const float sc = warp_sum(part);
         const float mn = fmaxf(m[g], sc);
         const float al = exp2f(m[g] - mn), pr = exp2f(sc - mn);
         m[g] = mn;
@@ -167,7 +137,7 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
     }
     const int h = hkv * G + g;
     const float o = L > 0.f ? O * a.v_scale / L : 0.f;
-    if (a.S == 1 && !(kScore && a.scores)) {
+    if (a.S == 1) {
       store_from_float(a.out, ((size_t)s * a.Hq + h) * D + d, a.out_dtype, o);
     } else {
       const size_t row = ((size_t)s * a.Hq + h) * a.S + p;
@@ -180,35 +150,40 @@ __global__ void __launch_bounds__(32 * kWarps) decode_simt_kernel(const DecodeAr
 
 }  // namespace
 
-template <bool kScore>
-static cudaError_t launch_simt(const DecodeArgs& a, cudaStream_t stream) {
+cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t stream) {
   if (a.G > kMaxG || a.D > 32 * kMaxDL || a.D % 32 != 0) return cudaErrorInvalidValue;
   const size_t smem = sizeof(float) * ((size_t)a.G * a.D + 2 * kWarps * a.G +
                                        (size_t)kWarps * a.G * a.D);
   dim3 grid(a.S, a.Hkv, a.B);
-  void (*kern)(const DecodeArgs);
+  cudaError_t e = cudaSuccess;
   switch (a.kv_dtype) {
-    case PKV_F32: kern = decode_simt_kernel<PKV_F32, kScore>; break;
-    case PKV_F16: kern = decode_simt_kernel<PKV_F16, kScore>; break;
-    case PKV_BF16: kern = decode_simt_kernel<PKV_BF16, kScore>; break;
-    case PKV_FP8_E4M3: kern = decode_simt_kernel<PKV_FP8_E4M3, kScore>; break;
+    case PKV_F32:
+      e = cudaFuncSetAttribute(decode_simt_kernel<PKV_F32>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e == cudaSuccess) decode_simt_kernel<PKV_F32><<<grid, 32 * kWarps, smem, stream>>>(a);
+      break;
+    case PKV_F16:
+      e = cudaFuncSetAttribute(decode_simt_kernel<PKV_F16>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e == cudaSuccess) decode_simt_kernel<PKV_F16><<<grid, 32 * kWarps, smem, stream>>>(a);
+      break;
+    case PKV_BF16:
+      e = cudaFuncSetAttribute(decode_simt_kernel<PKV_BF16>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e == cudaSuccess) decode_simt_kernel<PKV_BF16><<<grid, 32 * kWarps, smem, stream>>>(a);
+      break;
+    case PKV_FP8_E4M3:
+      e = cudaFuncSetAttribute(decode_simt_kernel<PKV_FP8_E4M3>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e == cudaSuccess)
+        decode_simt_kernel<PKV_FP8_E4M3><<<grid, 32 * kWarps, smem, stream>>>(a);
+      break;
     default: return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, 32 * kWarps, smem, stream>>>(a);
   e = cudaGetLastError();
   if (e == cudaSuccess) count_launch();
   return e;
-}
-
-cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t stream) {
-  return launch_simt<false>(a, stream);
-}
-
-cudaError_t launch_decode_simt_scored(const DecodeArgs& a, cudaStream_t stream) {
-  return launch_simt<true>(a, stream);
 }
 
 }  // namespace pkv

@@ -356,13 +356,16 @@ __global__ void __launch_bounds__(kCopyThreads, 16) copy_kernel(const EvictArgs 
 
 }  // namespace
 
-// CTAs a row: as many as run at once (two to an SM) while each has 1024 tokens or more.
-// (64 rows of 32768 tokens, whole call: 83.6 us with one CTA each, 71.0 with 2, 67.5 with
-// 4, 87.1 with 8; 256 rows of 2304: 95.6 with 1, 106.8 with 2.)
+// CTAs a row: 8192 slots or more each, and no more than run at once (two to an SM; from
+// clusters of 8 on, which find fewer places, one).  Whole calls with 1, 2, 4, 8 and 16
+// CTAs a row: 64 rows of 32768 slots 80.5, 68.1, 64.6, 84.6, 188 us; 24 rows of 42971
+// 50.2, 34.4, 23.9, 32.0, 67; 8 rows of 131072 123, 70.5, 44.2, 32.2, 43.7; 16 rows of
+// 8192 17.4, 17.2, 17.2, 24.8, 53; 128 rows of 8192 56.2, 58.3, 70.2, 113, 304.
 cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t stream) {
+  const int64_t rows = (int64_t)a.B * a.Hkv;
   int ctas = 1;
-  while (ctas < kMaxCtas && (int64_t)ctas * 1024 < a.max_len &&
-         (int64_t)a.B * a.Hkv * ctas * 2 <= 2 * sms)
+  while (ctas < kMaxCtas && (int64_t)ctas * (ctas < 8 ? 8192 : 32768) < a.max_len &&
+         rows * ctas * 2 <= (ctas < 4 ? 2 * sms : sms))
     ctas *= 2;
   cudaError_t e = cudaSuccess;
   if (e == cudaSuccess && ctas > 8)

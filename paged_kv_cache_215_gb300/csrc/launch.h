@@ -90,6 +90,7 @@ cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t stream);
 // The scored instances of both.
 cudaError_t launch_decode_mma_scored(const CUtensorMap* map, const DecodeArgs& a, int grid_x,
                                      cudaStream_t stream);
+bool simt_scored_supported(int D, int G);
 cudaError_t launch_decode_simt_scored(const DecodeArgs& a, cudaStream_t stream);
 // Chunked prefill on tcgen05 (one CTA per 128-row query tile, KV head, sequence).
 bool prefill_tc_supported(int kv_dtype, int q_dtype, int BS, int D, int G);

@@ -1346,6 +1346,13 @@ static ScoredWs scored_ws_mma(const pkv_geometry& g, int batch, int q_len, int m
   if (weights) add_record(g, batch, q_len, max_seq_len, &w);
   return w;
 }
+// Splits of the CUDA-core kernel in a scored call, cut at any token: 32 tokens or more
+// each, as many as keep the SMs busy.
+static int scored_splits(const pkv_geometry& g, int batch, int max_seq_len, int sms) {
+  const long long units = std::max<long long>(1, (long long)batch * g.num_kv_heads);
+  const long long s = std::min((8LL * sms + units - 1) / units, ((long long)max_seq_len + 31) / 32);
+  return (int)std::max<long long>(std::min<long long>(s, 1024), 1);
+}
 static ScoredWs scored_ws_simt(const pkv_geometry& g, int batch, int max_seq_len, int S,
                                bool weights) {
   ScoredWs w{};
@@ -1371,7 +1378,7 @@ size_t paged_decode_scored_workspace_bytes(const pkv_geometry* g, int batch, int
     need = scored_ws_mma(*g, batch, q_len, max_seq_len, plan, with_weights != 0).bytes;
   if (q_len == 1)
     need = std::max(need, scored_ws_simt(*g, batch, max_seq_len,
-                                         simt_auto_splits(*g, batch, max_seq_len, dev.sms),
+                                         scored_splits(*g, batch, max_seq_len, dev.sms),
                                          with_weights != 0).bytes);
   return need + 256;
 }
@@ -1498,8 +1505,8 @@ int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* 
     if (!map) return PKV_ECUDA;
     return launch_prefill_tc_scored(map, a, stream) == cudaSuccess ? PKV_OK : PKV_ECUDA;
   }
-  if (g.head_dim % 32 != 0 || g.head_dim > 256 || G > 16) return PKV_EUNSUPPORTED;
-  const int S = simt_auto_splits(g, batch, max_seq_len, dev.sms);
+  if (!simt_scored_supported(g.head_dim, G)) return PKV_EUNSUPPORTED;
+  const int S = scored_splits(g, batch, max_seq_len, dev.sms);
   const ScoredWs w = scored_ws_simt(g, batch, max_seq_len, S, weights != nullptr);
   if (w.bytes > 0 && (!ws || ws_bytes < w.bytes)) return PKV_ENOMEM;
   a.S = S;

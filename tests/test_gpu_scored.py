@@ -58,7 +58,10 @@ def expand(case, rules):
     ("bf16", 8, 2, 128, 16, 1), ("bf16", 8, 2, 128, 16, 4), ("f16", 4, 4, 128, 32, 1),
     ("f16", 14, 2, 128, 32, 2), ("e4m3", 8, 1, 128, 16, 1), ("e4m3", 8, 2, 128, 64, 2),
     ("bf16", 7, 1, 128, 64, 1), ("bf16", 16, 1, 128, 16, 1), ("f32", 4, 2, 64, 16, 1),
-    ("bf16", 12, 4, 96, 16, 1), ("e4m3", 4, 2, 64, 32, 1), ("f16", 5, 1, 256, 8, 1)])
+    ("bf16", 12, 4, 96, 16, 1), ("e4m3", 4, 2, 64, 32, 1), ("f16", 5, 1, 256, 8, 1),
+    ("f16", 3, 1, 40, 16, 1), ("e4m3", 2, 2, 16, 1, 1), ("f32", 16, 1, 8, 4, 1),
+    ("f32", 32, 2, 256, 16, 1), ("bf16", 16, 1, 128, 64, 1), ("f16", 32, 2, 128, 64, 1),
+    ("e4m3", 10, 2, 128, 64, 3)])
 def test_decode(kv, hq, hkv, dim, bs, q_len, rules):
     lens = [300, 1, bs, bs + 1, 0, 2 * bs - 1, 77]
     case = Case(lens, hq, hkv, dim, kv, bs, q_len, seed=hq + dim + q_len)

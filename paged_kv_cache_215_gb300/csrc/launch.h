@@ -95,8 +95,9 @@ cudaError_t launch_decode_simt_scored(const DecodeArgs& a, cudaStream_t stream);
 // Chunked prefill on tcgen05 (one CTA per 128-row query tile, KV head, sequence).
 bool prefill_tc_supported(int kv_dtype, int q_dtype, int BS, int D, int G);
 cudaError_t launch_prefill_tc(const CUtensorMap* map, const DecodeArgs& a, cudaStream_t stream);
-cudaError_t launch_prefill_tc_scored(const CUtensorMap* map, const DecodeArgs& a,
-                                     cudaStream_t stream);
+// The same under the rules of a scored call.
+cudaError_t launch_prefill_scored(const CUtensorMap* map, const DecodeArgs& a, int sms,
+                                  cudaStream_t stream);
 // Merge of the balanced-mode partials, one CTA per (unit, head in the unit).
 cudaError_t launch_merge_units(const DecodeArgs& a, bool pdl, cudaStream_t stream);
 // Cascade merge: the decode's balanced-mode partials of each row plus a.ext_count

@@ -1503,7 +1503,7 @@ int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* 
       return PKV_EUNSUPPORTED;
     const CUtensorMap* map = p->tmap_tiles();
     if (!map) return PKV_ECUDA;
-    return launch_prefill_tc_scored(map, a, stream) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+    return launch_prefill_scored(map, a, dev.sms, stream) == cudaSuccess ? PKV_OK : PKV_ECUDA;
   }
   if (!simt_scored_supported(g.head_dim, G)) return PKV_EUNSUPPORTED;
   const int S = scored_splits(g, batch, max_seq_len, dev.sms);

@@ -40,55 +40,12 @@
 // critical path, warp 13 takes every other key tile (in chunked prefill it
 // stays idle: its polling there would cost the softmax warps issue slots).  mbarriers (all waits bounded) pass the tiles between the roles; a
 // stage is refilled once every issuer's MMAs reading it have completed.
-#include "device.cuh"
-#include "launch.h"
-#include "score.cuh"
+#include "prefill_tc.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kD = 128;
-constexpr int kM = 128;                      // query rows per query tile (one UMMA M)
-constexpr int kQT = 2;                       // query tiles per CTA
-constexpr int kN = 64;                       // keys per K/V tile
-constexpr int kSoftmaxWarps = 4 * kQT;
-constexpr int kWarpS = kSoftmaxWarps;        // S MMAs of query tile t: warp kWarpS + t
-constexpr int kWarpPV = kWarpS + kQT;        // P V MMAs of query tile t: warp kWarpPV + t
-constexpr int kWarpTMA = kWarpPV + kQT;      // K/V loads
-constexpr int kWarpConv = kWarpTMA + 1;      // E4M3 pools: warps converting K/V tiles to f16;
-                                             // 16-bit pools: the second producer
-constexpr int kIssuers = 2 * kQT;            // MMA issuers committing each stage's release
-constexpr uint32_t kHalf = 16384;            // 128 rows x 128 B: one 64-column half of Q
-constexpr uint32_t kKVHalf = kN * 128;       // 64 rows x 128 B
-constexpr uint32_t kStageBytes = 4 * kKVHalf;        // K tile (16 KB) then V tile (16 KB)
-constexpr uint32_t kStage8Bytes = 2 * kKVHalf;       // an E4M3 tile: K then V, 128 B a key
-constexpr uint32_t kSmemQ = 0;                        // [query tile][half]
-constexpr uint32_t kSmemKV = kSmemQ + kQT * 2 * kHalf;
-constexpr uint32_t kTmemCols = 512;          // query tile t: S/P0 [256t, +64) S/P1 [+64, +128) O [+128, +256)
-constexpr uint32_t kAlignSlack = 1024;       // the tiles start on a 1024-byte boundary
-constexpr int kMaxStages = 6;
-constexpr float kTiny = 0x1p-126f;           // in the place of a scale of 0: -inf times it is -inf
-
-// Per pool dtype.  bf16 / f16: TMA fills kStages tiles the MMAs read directly.
-// E4M3: TMA lands the E4M3 tile (one 128-byte line per key: half the boxes) in
-// the V half of its stage, and kConvWarps warps convert it in place into the
-// stage's f16 K and V; the MMAs then run as for an f16 pool.  Every E4M3 value is
-// an f16 value, so with per-tensor scales the conversion is exact (k_scale rides
-// on the softmax scale, v_scale on the output); per-block scales are multiplied
-// in before the f16 rounding (relative error 2^-11).
-template <int KVT>
-struct PfCfg {
-  static constexpr bool kFp8 = KVT == PKV_FP8_E4M3;
-  static constexpr bool kBf16 = KVT == PKV_BF16;      // else f16 operands (f16 and E4M3 pools)
-  static constexpr int kStages = 5;                   // K/V tiles in flight
-  static constexpr int kConvWarps = kFp8 ? 3 : 0;
-  // producer warps (16-bit pools: a second one, after warp 12, that the
-  // shared-prefix pass uses; E4M3 tiles are half the bytes and their converters
-  // fill the warp budget)
-  static constexpr int kProducers = kFp8 ? 1 : 2;
-  static constexpr int kThreads = 32 * (kWarpConv + kConvWarps + kProducers - 1);
-  static constexpr uint32_t kSmemBytes = kSmemKV + kStages * kStageBytes;
-};
+using namespace tc;
 
 struct Bars {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
@@ -96,8 +53,6 @@ struct Bars {
   uint64_t s_full[kQT][2], p_full[kQT][2], p_free[kQT][2], o_done[kQT];
   uint64_t o_final[kQT];                      // query tile t's last P V has completed
   uint64_t v_zeroed;                          // the tail tile's V rows past the end are zero
-  uint64_t v_headed;                          // scored: the first tile's V rows ahead of every
-                                              // query's keys are zero
   uint64_t q_ready;                           // the Q tiles are staged
   uint64_t eref_ready;                        // E4M3 per-block scales: the reference exponent is in
   int eref[4];                                // per converter warp: largest exponent of the V scales
@@ -111,10 +66,6 @@ static_assert(PfCfg<PKV_FP8_E4M3>::kSmemBytes + sizeof(Bars) + kAlignSlack <= 22
 static_assert(PfCfg<PKV_FP8_E4M3>::kThreads <= 512, "threads");
 static_assert(PfCfg<PKV_BF16>::kThreads <= 512, "threads");
 
-__device__ __forceinline__ uint32_t sw128(int row, int chunk) {
-  return (uint32_t)row * 128u + ((uint32_t)(chunk ^ (row & 7)) << 4);
-}
-
 // Key tiles query tile `qt` needs: up to the one holding its last row's last key.
 __device__ __forceinline__ int key_tiles(const DecodeArgs& a, int n, int qt) {
   const int QT = kM / a.G, t0 = qt * QT;
@@ -124,24 +75,11 @@ __device__ __forceinline__ int key_tiles(const DecodeArgs& a, int n, int qt) {
   return p_last >= 0 ? (p_last + kN) / kN : 0;
 }
 
-// kRules: a chunk under the rules of score.cuh (windows, prefixes and documents alone, with
-// a cap, or with distances and perhaps a cap); each row sees its own interval of keys, and
-// the CTA reads from the first key that any of its rows sees.
-enum Rules { kNone = 0, kMasks = 1, kCap = 2, kDistance = 3 };
-// Threads of an instance.  The softmax warps of the scored ones hold a row of 64 scores
-// beside their rules: they take registers that the issuing and loading warps do not need
-// (setmaxnreg, by warpgroups of four warps, so two idle warps fill the last one up), at
-// launch 128 a thread.
-template <int KVT, int kRules>
-constexpr int threads_of() { return kRules == kNone ? PfCfg<KVT>::kThreads : 512; }
-constexpr int kSoftmaxRegs = 160, kOtherRegs = 96;
-static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= 512 * 128, "registers");
-
-template <int KVT, int kRules>
-__global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
+template <int KVT>
+__global__ void __launch_bounds__(PfCfg<KVT>::kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap, const DecodeArgs a) {
   using C = PfCfg<KVT>;
-  constexpr bool kBf16 = C::kBf16, kFp8 = C::kFp8, kScore = kRules != kNone;
+  constexpr bool kBf16 = C::kBf16, kFp8 = C::kFp8;
   constexpr int kStages = C::kStages;
   constexpr bool kSplitP = kBf16;            // f16 P (11 bits) needs no low term
   // f16 P is 2^(s - ref + kPOff) <= 2^15: weights down to 2^-21 of the row's
@@ -174,32 +112,10 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
     if (tid == 0) record_error(a.status, PKV_EBOUNDS);
     n = n < 0 ? 0 : cap;
   }
-  if constexpr (kScore) n = scored_len(a, s);
   // key tiles jt0 .. jt0 + T - 1 of the sequence; local tile j is global tile jt0 + j
   int tiles[kQT], jt0 = 0;                        // key tiles each slot computes
   int T = 0;                                      // key tiles the CTA loads
-  int read0 = 0;                                  // scored: the first key any row sees
-  if constexpr (kScore) {
-    int hi[kQT];
-    read0 = n;
-#pragma unroll
-    for (int t = 0; t < kQT; ++t) {
-      hi[t] = 0;
-      for (int i = lane; i < QT; i += 32) {
-        const int tok = (pair * kQT + t) * QT + i;
-        if (tok >= a.q_len) break;
-        const KeyRange k = key_range(a, s, n, tok);
-        if (k.lo >= k.hi) continue;
-        read0 = min(read0, k.lo);
-        hi[t] = max(hi[t], k.hi);
-      }
-      hi[t] = __reduce_max_sync(0xffffffffu, hi[t]);
-    }
-    read0 = __reduce_min_sync(0xffffffffu, read0);
-    jt0 = read0 / kN;
-#pragma unroll
-    for (int t = 0; t < kQT; ++t) tiles[t] = hi[t] > 0 ? (hi[t] + kN - 1) / kN - jt0 : 0;
-  } else if (casc) {
+  if (casc) {
     const int nt = (n + kN - 1) / kN;
     jt0 = (int)((long long)split * nt / a.S);
     const int jt1 = (int)((long long)(split + 1) * nt / a.S);
@@ -223,9 +139,6 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
   // the sequence's last key tile, if it is ragged and this CTA reads it (local index)
   const int jg_tail = (n % kN != 0) ? (n - 1) / kN : -1;
   const int j_tail = (jg_tail >= jt0 && jg_tail < jt0 + T) ? jg_tail - jt0 : -1;
-  // scored: rows of the first tile that no query sees (their block may be stale: the
-  // first seen key's is read in its place, and V is zeroed there), and that block
-  const int head = kScore ? read0 - jt0 * kN : 0, blk0 = kScore ? read0 / a.BS : 0;
 
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
@@ -244,7 +157,6 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
       mbar_init(&bars->o_final[t], 1);
     }
     mbar_init(&bars->v_zeroed, 1);
-    mbar_init(&bars->v_headed, 1);
     mbar_init(&bars->q_ready, 32 * kSoftmaxWarps);
     mbar_init(&bars->eref_ready, kFp8 ? C::kConvWarps : 1);
     bars->abort_flag = 0;
@@ -268,60 +180,7 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
   // its largest |q|) before the f16 rounding, exactly, and the same thread's
   // softmax takes 2^-q_e onto the scale.
   int q_e = 0;
-  if (kScore && warp < kSoftmaxWarps) {
-    // a warp's 32 rows, two rows an instruction (a thread for each row would touch 32
-    // lines with every load: 2.6 us a CTA, 6.4 us with the E4M3 prescale)
-    const int t = warp / 4, half = lane >> 4, c = lane & 15;
-    uint8_t* qdst = sm + kSmemQ + t * 2 * kHalf;
-    const uint32_t flip = a.qk_scale_log2 < 0.f ? 0x80008000u : 0u;
-    const bool to_f16 = kFp8 && a.q_dtype == PKV_BF16;
-    if (tiles[t] > 0) {
-#pragma unroll 1
-      for (int r0 = 0; r0 < 32; r0 += 16) {
-        uint4 v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int r = (warp & 3) * 32 + r0 + 2 * u + half, i = r / G, g = r - i * G;
-          const int tok = (pair * kQT + t) * QT + i;
-          const size_t qrow = ((size_t)s * a.q_len + tok) * a.Hq + (size_t)hkv * G + g;
-          v[u] = tok < a.q_len ? *(reinterpret_cast<const uint4*>(
-                                       static_cast<const uint16_t*>(a.q) + qrow * kD) + c)
-                               : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          uint32_t* w = reinterpret_cast<uint32_t*>(&v[u]);
-          if (to_f16) {
-            float amax = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = unpack2<true>(w[e]);
-              amax = fmax3(amax, fabsf(f.x), fabsf(f.y));
-            }
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1)
-              amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const int e_row = f16_fit_exponent(amax);
-            const float qscale = pow2i(e_row);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = unpack2<true>(w[e]);
-              w[e] = pack_f16(f.x * qscale, f.y * qscale);
-            }
-            // row lane of the warp is this thread's in the softmax
-            const int e_mine = __shfl_sync(0xffffffffu, e_row, (lane & 1) * 16);
-            if (lane >> 1 == r0 / 2 + u) q_e = e_mine;
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] ^= flip;
-          const int r = (warp & 3) * 32 + r0 + 2 * u + half;
-          *reinterpret_cast<uint4*>(qdst + (c >> 3) * kHalf + sw128(r, c & 7)) = v[u];
-        }
-      }
-    }
-    fence_proxy_async_smem();
-    mbar_arrive(&bars->q_ready);
-  } else if (warp < kSoftmaxWarps) {
+  if (warp < kSoftmaxWarps) {
     const int t = warp / 4, r = tid - 128 * t, i = r / G, g = r % G;
     // an empty tile is not staged: its S MMAs never run, and its Q space may
     // hold the ring's extra stage
@@ -375,12 +234,10 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
   }
 
   if (warp >= kSoftmaxWarps) {
-    if constexpr (kScore)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // ------------------------------------------------------------ issuers
     // Each issuer warp walks its loop and waits as a whole (so it stays
     // converged); its lane 0 issues the MMAs and the commits.
-    if (T > 0 && warp < PfCfg<KVT>::kThreads / 32) {
+    if (T > 0) {
       const bool leader = lane == 0;
       // every lane waits; the warp agrees on the outcome
       auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -427,8 +284,7 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
           // both 64-column halves (bs x 256 bytes).  Blocks past the sequence's
           // last one are replaced by its last block: their keys are masked and
           // their V rows zeroed before use.
-          const int jb = min(kScore ? max(first + (lane >> 1), blk0) : first + (lane >> 1),
-                             nblk - 1);
+          const int jb = min(first + (lane >> 1), nblk - 1);
           int blk = __shfl_sync(0xffffffffu, ids, jb - id_base);
           if (leader) mbar_arrive_expect_tx(&bars->kv_full[st], kStageBytes);
           __syncwarp();
@@ -456,8 +312,7 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
               id_base = first;
               ids = id_base + lane < nblk ? __ldg(trow + id_base + lane) : 0;
             }
-            const int jb = min(kScore ? max(first + (lane >> 1), blk0) : first + (lane >> 1),
-                             nblk - 1);
+            const int jb = min(first + (lane >> 1), nblk - 1);
             int blk = __shfl_sync(0xffffffffu, ids, jb - id_base);
             if (leader) mbar_arrive_expect_tx(&bars->s8_full[st], kStage8Bytes);
             __syncwarp();
@@ -509,20 +364,6 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (leader) mbar_arrive(&bars->v_zeroed);
-          }
-        }
-        if (kScore && prod == 1 && head > 0) {
-          ok = wait(&bars->kv_full[0], 0);
-          if (ok) {
-            uint8_t* vbuf = sm + stage_off(0) + 2 * kKVHalf;
-            for (int e = lane; e < head * 16; e += 32) {
-              const int row = e / 16, c16 = e % 16;
-              *reinterpret_cast<uint4*>(vbuf + ((row >> 3) * 2 + (c16 >> 3)) * 1024 +
-                                        sw128(row & 7, c16 & 7)) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (leader) mbar_arrive(&bars->v_headed);
           }
         }
         // every TMA load issued must land before the CTA may exit.  A stage's key
@@ -587,7 +428,7 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
           const int bpt = kN / a.BS;
           const int b1 = min((jt0 + T) * bpt, nblk);
           int ev = -100000;
-          for (int b = max(jt0 * bpt, blk0) + c * 32 + lane; b < b1; b += W * 32) {
+          for (int b = jt0 * bpt + c * 32 + lane; b < b1; b += W * 32) {
             int blk = __ldg(trow + b);
             blk = (blk < 0 || blk >= a.num_blocks) ? 0 : blk;
             const float vs =
@@ -611,7 +452,6 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
           uint8_t* dst = sm + stage_off(st);
           const uint8_t* src = dst + 2 * kKVHalf;              // E4M3 K rows, then V rows
           const int valid = n - (jt0 + j) * kN;                // keys of the tile in the sequence
-          const int skip = j == 0 ? head : 0;                  // keys ahead of every query's
           // two groups a step (eight loads in flight a lane before the warp syncs)
 #pragma unroll 1
           for (int gr = g0; gr < g1; gr += 2) {
@@ -630,8 +470,7 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
             if (scaled) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                int jb = min((jt0 + j) * (kN / a.BS) + (row0 + 4 * h) / a.BS, nblk - 1);
-                if (kScore) jb = max(jb, blk0);
+                const int jb = min((jt0 + j) * (kN / a.BS) + (row0 + 4 * h) / a.BS, nblk - 1);
                 int blk = __ldg(trow + jb);
                 blk = (blk < 0 || blk >= a.num_blocks) ? 0 : blk;
                 sv[h] = ldexpf(
@@ -644,7 +483,7 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
             convert(xk0, 1.f, false, o);
             store(dst, 0, row0, o);
             convert(xv0, sv[0], scaled, o);
-            if (row0 >= valid || (kScore && row0 < skip)) {
+            if (row0 >= valid) {
               // keys past the sequence end: zero V, so that P = 0 never meets NaN
 #pragma unroll
               for (int e = 0; e < 8; ++e) o[e] = 0u;
@@ -654,7 +493,7 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
               convert(xk1, 1.f, false, o);
               store(dst, 0, row1, o);
               convert(xv1, sv[1], scaled, o);
-              if (row1 >= valid || (kScore && row1 < skip)) {
+              if (row1 >= valid) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) o[e] = 0u;
               }
@@ -703,7 +542,6 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
             const int b = jl & 1;
             ok = wait(&bars->p_full[t][b], (jl >> 1) & 1);
             if (!kFp8 && ok && j == j_tail) ok = wait(&bars->v_zeroed, 0);
-            if (!kFp8 && kScore && ok && j == 0 && head > 0) ok = wait(&bars->v_headed, 0);
             if (!ok) break;
             tc_fence_after();
             if (leader) {
@@ -733,26 +571,15 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
       __syncwarp();
     }
   } else {
-    if constexpr (kScore)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ------------------------------------------------------------ softmax, one row per thread
     const int t = warp / 4, r = tid - 128 * t, i = r / G, g = r % G;
     const int tok = (pair * kQT + t) * QT + i;
     const bool live = tok < a.q_len;
     // this query's last visible key: causal within the chunk, or its prefix length
     const int pos = casc ? (live ? __ldg(a.key_limit + tok) : 0) - 1 : n - a.q_len + tok;
-    // scored: the row's keys, its slope and cap in log2 units
-    KeyRange keys{0, 0};
-    float slope = 0.f, cap_in = 0.f;
-    if constexpr (kScore) {
-      if (live) keys = key_range(a, s, n, tok);
-    }
-    if constexpr (kRules >= kCap) cap_in = fabsf(a.cap_in) * pow2i(-q_e);
-    if constexpr (kRules == kDistance) slope = a.slopes[hkv * G + g] * kLog2e;
     const int my_tiles = tiles[t];
     // Q carries the sign; 2^-q_e undoes the row's f16 prescale (E4M3 pools)
     float qs = fabsf(a.qk_scale_log2) * pow2i(-q_e);
-    if (kScore) qs = fmaxf(qs, kTiny);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tcol = tmem + lane_base + t * 256;
     float mref = -INFINITY, lsum = 0.f;
@@ -778,18 +605,14 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
       const int b = jl & 1;
       const int j = jl;
       const int kpos0 = (jt0 + j) * kN;
-      float qsb[4];                 // of 16 keys each: the scale, or with a cap the scale over it
-#pragma unroll
-      for (int g4 = 0; g4 < 4; ++g4) qsb[g4] = kRules >= kCap && a.cap_in != 0.f ? cap_in : qs;
+      float qsb[4] = {qs, qs, qs, qs};
       if (bscaled) {
         // issued before the wait for S, so the loads overlap it
 #pragma unroll
         for (int g4 = 0; g4 < 4; ++g4) {
-          const int jb = min((kpos0 + 16 * g4) / a.BS, nblk - 1);
-          int blk = __ldg(trow + (kScore ? max(jb, blk0) : jb));
+          int blk = __ldg(trow + min((kpos0 + 16 * g4) / a.BS, nblk - 1));
           blk = (blk < 0 || blk >= a.num_blocks) ? 0 : blk;
-          qsb[g4] = (kRules >= kCap && a.cap_in != 0.f ? cap_in : qs) * __ldg(a.block_scales + ((size_t)blk * 2 * a.L + a.layer) * a.Hkv + hkv);
-          if (kScore && qsb[g4] == 0.f) qsb[g4] = kTiny;
+          qsb[g4] = qs * __ldg(a.block_scales + ((size_t)blk * 2 * a.L + a.layer) * a.Hkv + hkv);
         }
       }
       if (!wait(&bars->s_full[t][b], (jl >> 1) & 1)) {
@@ -805,42 +628,7 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
       float mp[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) mp[e] = -INFINITY;
-      if constexpr (kScore) {
-        if constexpr (kRules >= kCap) {
-          // to log2 units here (the cap is no factor of the largest score)
-#pragma unroll
-          for (int g4 = 0; g4 < 4; ++g4) {
-            scale_scores<16>(sv + 16 * g4, qsb[g4]);
-            qsb[g4] = 1.f;
-          }
-          if (kRules == kCap || a.cap_in != 0.f) cap_scores<kN>(sv, a.cap_out);
-        }
-        if constexpr (kRules == kDistance) {
-          const float d0 = (float)(pos - kpos0);
-          if (__all_sync(0xffffffffu, pos >= kpos0 + kN - 1)) {
-            // every key lies behind its query: - slope (d0 - c), two keys an instruction
-            const uint64_t s2 = f2_pack(slope, slope);
-#pragma unroll
-            for (int c = 0; c < kN; c += 2) {
-              const uint64_t d2 = f2_pack((float)c - d0, (float)(c + 1) - d0);
-              f2_unpack(ffma2(s2, d2, f2_pack(sv[c], sv[c + 1])), sv[c], sv[c + 1]);
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < kN; ++c) sv[c] = fmaf(-slope, fabsf(d0 - (float)c), sv[c]);
-          }
-        }
-        const int c0 = keys.lo - kpos0, c1 = keys.hi - kpos0;
-        if (!__all_sync(0xffffffffu, c0 <= 0 && c1 >= kN)) {
-#pragma unroll
-          for (int c = 0; c < kN; ++c) sv[c] = c >= c0 && c < c1 ? sv[c] : -INFINITY;
-        }
-#pragma unroll
-        for (int c = 0; c < kN; c += 2) {
-          const int e = 2 * (c >> 4) + ((c >> 1) & 1);
-          mp[e] = fmax3(mp[e], sv[c], sv[c + 1]);
-        }
-      } else if (__all_sync(0xffffffffu, live && kpos0 + kN - 1 <= pos)) {
+      if (__all_sync(0xffffffffu, live && kpos0 + kN - 1 <= pos)) {
         // the warp's rows see every key of the tile: no mask
 #pragma unroll
         for (int c = 0; c < kN; c += 2) {
@@ -903,8 +691,7 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
           const int c = q4 * 16 + 2 * c2;
           // p = 2^(s * scale - ref): one FMA per two keys and the SFU per key
           float x0, x1;
-          const uint64_t sv2 = f2_pack(sv[c], sv[c + 1]);
-          f2_unpack(kRules >= kCap ? fadd2(sv2, nref2) : ffma2(sv2, qs2, nref2), x0, x1);
+          f2_unpack(ffma2(f2_pack(sv[c], sv[c + 1]), qs2, nref2), x0, x1);
           const float p0 = ex2_ftz(x0), p1 = ex2_ftz(x1);
           const uint64_t p2 = f2_pack(p0, p1);
           pp[c2 & 3] = fadd2(pp[c2 & 3], p2);
@@ -999,24 +786,15 @@ __global__ void __launch_bounds__(threads_of<KVT, kRules>(), 1)
 template <int KVT>
 size_t smem_bytes_t() { return PfCfg<KVT>::kSmemBytes + sizeof(Bars) + kAlignSlack; }
 
-template <int KVT, int kRules>
+template <int KVT>
 cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, dim3 grid, cudaStream_t stream) {
   const size_t smem = smem_bytes_t<KVT>();
-  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<KVT, kRules>,
+  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<KVT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  if (kRules != kNone) {
-    // the softmax warps wait for registers that only a launch with 128 a thread can give
-    static const bool enough = [] {
-      cudaFuncAttributes at{};
-      return cudaFuncGetAttributes(&at, prefill_tc_kernel<KVT, kRules>) == cudaSuccess &&
-             at.numRegs >= 128;
-    }();
-    if (!enough) return cudaErrorInvalidConfiguration;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads_of<KVT, kRules>());
+  cfg.blockDim = dim3(PfCfg<KVT>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1024,7 +802,7 @@ cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, dim3 grid, cud
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<KVT, kRules>, *map, a);
+  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<KVT>, *map, a);
 }
 
 bool prefill_tc_supported(int kv_dtype, int q_dtype, int BS, int D, int G) {
@@ -1035,8 +813,7 @@ bool prefill_tc_supported(int kv_dtype, int q_dtype, int BS, int D, int G) {
          kM % G == 0;
 }
 
-template <int kRules>
-static cudaError_t launch_chunk(const CUtensorMap* map, const DecodeArgs& a, cudaStream_t stream) {
+cudaError_t launch_prefill_tc(const CUtensorMap* map, const DecodeArgs& a, cudaStream_t stream) {
   const int QT = kM / a.G;
   const int qtiles = (a.q_len + QT - 1) / QT;
   if (qtiles == 0 || a.B == 0) return cudaSuccess;
@@ -1046,27 +823,15 @@ static cudaError_t launch_chunk(const CUtensorMap* map, const DecodeArgs& a, cud
   dim3 grid(a.Hkv, a.key_limit ? a.S : a.B, pairs);
   cudaError_t e;
   switch (a.kv_dtype) {
-    case PKV_BF16: e = launch_t<PKV_BF16, kRules>(map, a, grid, stream); break;
-    case PKV_F16: e = launch_t<PKV_F16, kRules>(map, a, grid, stream); break;
-    case PKV_FP8_E4M3: e = launch_t<PKV_FP8_E4M3, kRules>(map, a, grid, stream); break;
+    case PKV_BF16: e = launch_t<PKV_BF16>(map, a, grid, stream); break;
+    case PKV_F16: e = launch_t<PKV_F16>(map, a, grid, stream); break;
+    case PKV_FP8_E4M3: e = launch_t<PKV_FP8_E4M3>(map, a, grid, stream); break;
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;
   e = cudaGetLastError();
   if (e == cudaSuccess) count_launch();
   return e;
-}
-
-cudaError_t launch_prefill_tc(const CUtensorMap* map, const DecodeArgs& a, cudaStream_t stream) {
-  return launch_chunk<kNone>(map, a, stream);
-}
-
-cudaError_t launch_prefill_tc_scored(const CUtensorMap* map, const DecodeArgs& a,
-                                     cudaStream_t stream) {
-  if (a.key_limit) return cudaErrorInvalidValue;
-  return a.slopes           ? launch_chunk<kDistance>(map, a, stream)
-         : a.cap_in != 0.f ? launch_chunk<kCap>(map, a, stream)
-                           : launch_chunk<kMasks>(map, a, stream);
 }
 
 }  // namespace pkv

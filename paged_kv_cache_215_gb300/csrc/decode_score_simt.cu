@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(32 * kWarps) lanes_kernel(const DecodeArgs a, 
                            : nullptr;
   // the record covers the first block from its first token on
   if (record && seen > 0 && p == 0)
-    for (int i = keys.lo / a.BS * a.BS * a.score_row + threadIdx.x; i < keys.lo * a.score_row;
-         i += blockDim.x)
+    for (int64_t i = (int64_t)(keys.lo / a.BS * a.BS) * a.score_row + threadIdx.x;
+         i < (int64_t)keys.lo * a.score_row; i += blockDim.x)
       record[i] = -INFINITY;
   __syncthreads();
 

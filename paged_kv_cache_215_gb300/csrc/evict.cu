@@ -386,7 +386,7 @@ cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t stream) {
   const int per_cta = kCopyThreads / 32 * kCopyTokens;
   const int tiles = (std::min(a.max_len, a.capacity) + per_cta - 1) / per_cta;
   if (tiles == 0) return cudaSuccess;
-  if (tiles > 65535) return cudaErrorInvalidValue;
+  static_assert(kMaxEvictKept == 65535 * (kCopyThreads / 32) * kCopyTokens, "the copy's grid");
   e = launch_chained(copy_kernel, dim3(a.Hkv, a.B, tiles), dim3(kCopyThreads), 1, stream, a);
   if (e == cudaSuccess) count_launch();
   return e;

@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -1405,9 +1406,14 @@ int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* 
   const pkv_scores none{};
   const pkv_scores& sc = scores ? *scores : none;
   const double x_scale = (double)scale * k_scale;
-  if (!(sc.cap >= 0.f) || !std::isfinite(sc.cap) || sc.window < 0 ||
-      (sc.cap > 0.f && !std::isfinite((float)(x_scale / sc.cap))))
-    return PKV_EINVAL;
+  if (!(sc.cap >= 0.f) || !std::isfinite(sc.cap) || sc.window < 0) return PKV_EINVAL;
+  if (sc.cap > 0.f) {
+    // what the kernels multiply by: scale / cap and cap * log2(e)
+    const float in = std::fabs((float)(x_scale / sc.cap));
+    if (!(in <= FLT_MAX) || (x_scale != 0.0 && in < FLT_MIN) ||
+        !std::isfinite((float)(sc.cap * 1.4426950408889634)))
+      return PKV_EINVAL;
+  }
   if (batch == 0) return PKV_OK;
   if (!d_out || !d_q || !d_block_tables || !d_seq_lens || max_blocks_per_seq < 1 ||
       !aligned16(d_q) || !aligned16(d_out) || (d_workspace && !aligned16(d_workspace)))
@@ -1584,6 +1590,10 @@ int kv_evict(pkv_pool* p, int layer, const int32_t* d_new_tables, int max_new_bl
   a.row_bytes = g.head_dim * elem_bytes(g.kv_dtype);
   a.max_len = max_seq_len;
   a.recent = recent;
+  // (new_lens is written while other KV heads still read the lengths and budgets)
+  auto apart = [&](const int32_t* x) { return x + batch <= d_new_lens || d_new_lens + batch <= x; };
+  if (!apart(d_seq_lens) || !apart(d_keep)) return PKV_EINVAL;
+  if (std::min(max_seq_len, a.capacity) > kMaxEvictKept) return PKV_EUNSUPPORTED;
   DeviceInfo dev;
   if (!device_info(&dev)) return PKV_ECUDA;
   return launch_evict(a, dev.sms, stream) == cudaSuccess ? PKV_OK : PKV_ECUDA;

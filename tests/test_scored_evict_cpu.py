@@ -123,3 +123,31 @@ def test_scores_hand_on_what_they_hold_at_the_call(pkv, monkeypatch):
     assert seen[0] == ("out", "q", 7, "storage", 2, "tables", "lens", 9, 0.5, 4.0, 5, "slopes",
                        None, None, 1.0, 1.0, "w", "w0", "ws", None)
     assert seen[1][9:14] == (0.0, 0, None, None, None)
+
+
+def test_caps_at_the_ends_of_fp32(pkv):
+    p = FakePool(pkv, nb=8)
+    bad = pkv.PKV_EINVAL
+    assert scored(pkv, p.h, rules(pkv, 3e38)) == bad          # cap * log2(e) overflows
+    assert scored(pkv, p.h, rules(pkv, 1e38), scale=0.125) == bad     # scale / cap is subnormal
+    assert scored(pkv, p.h, rules(pkv, 1e30), scale=1e-9) == bad
+    for cap, scale in ((1e30, 0.125), (1e30, 0.0), (1e-30, 0.125)):
+        # (without a workspace: nothing is launched where there is a GPU)
+        assert scored(pkv, p.h, rules(pkv, cap), scale=scale, ws=None) in (pkv.PKV_ECUDA,
+                                                                           pkv.PKV_ENOMEM)
+    p.close()
+
+
+def test_evict_refuses_lengths_written_over_read_ones(pkv):
+    p = FakePool(pkv, nb=8)
+    bad, far = pkv.PKV_EINVAL, lambda d: ctypes.c_void_p((1 << 22) + d)
+    assert evict(pkv, p.h, out=far(0), lens=far(0)) == bad
+    assert evict(pkv, p.h, out=far(0), lens=far(4)) == bad    # two sequences: one apart
+    assert evict(pkv, p.h, out=far(4), keep=far(0)) == bad
+    # more than a sequence may keep: refused too, but for another reason where they are apart
+    big = dict(most=1 << 23, mb=1 << 20, nb=1 << 20, width=1 << 23, index=X, iw=1 << 23,
+               o=rows(pkv, 1 << 40, 1 << 24, 1 << 23), out=far(0))
+    assert evict(pkv, p.h, lens=far(8), keep=far(-8), **big) == pkv.PKV_EUNSUPPORTED
+    assert evict(pkv, p.h, lens=far(7), keep=far(-8), **big) == bad
+    assert evict(pkv, p.h, lens=far(8), keep=far(-4), **big) == bad
+    p.close()

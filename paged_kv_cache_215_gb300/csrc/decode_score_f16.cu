@@ -2,6 +2,8 @@
 // (decode_mma.cuh) for scored calls on f16 pools: block sizes 16 / 32 / 64, up to 16
 // query rows per KV head, a consumer warp for every 8 of them; and for one query token
 // without slopes the plain decode's loop, with or without a cap and a record.
+//
+// 8 requests of up to 8192 tokens, 32 heads on 32, distances: 122 us (0.97 of the copy rate).
 #include "decode_mma.cuh"
 
 namespace pkv {

@@ -2,6 +2,9 @@
 // (decode_mma.cuh) for scored calls on E4M3 pools: block sizes 16 / 32 / 64, up to 16
 // query rows per KV head, a consumer warp for every 8 of them; and for one query token
 // without slopes the plain decode's loop, with or without a cap and a record.
+//
+// 128K tokens of 8 heads, capped: 57 us (0.70 of the copy rate; the instructions that
+// convert, cap and weigh a byte's score take as long as its load).
 #include "decode_mma.cuh"
 
 namespace pkv {

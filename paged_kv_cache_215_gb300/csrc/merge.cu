@@ -434,6 +434,10 @@ __device__ __forceinline__ void merge_row128(const DecodeArgs& a, const RowParti
 
 // CTA (x, h, s): the first CTAs along x merge the rows of (s, h) (one each, or with
 // kWarpRows a warp each), the others (with a record) take its tokens.
+//
+// Bound by latency: partials of 32 requests 5.4 us alone, of one request of 128K tokens
+// (304 partials a row) 8.9; with the record of 32 ragged requests of up to 8192 tokens
+// (35 MB, most of it in L2) 17 us.
 template <bool kWarpRows, bool kRecord>
 __global__ void __launch_bounds__(kThreads, 2)
     merge_scored_kernel(const DecodeArgs a, const WeightRows in, const WeightRows out) {

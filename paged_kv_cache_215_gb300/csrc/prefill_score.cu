@@ -45,8 +45,9 @@ constexpr float kTiny = 0x1p-126f;           // in the place of a scale of 0: -i
 
 // Warps past the loading one: E4M3 pools' converters, or the one of 16-bit pools that zeroes
 // V rows which no query sees.  With three converters the softmax waited 820 of a key tile's
-// 2280 cycles for S, with seven 450 of 2100 (592 -> 560 us a call).  The softmax warps hold a row of 64 scores beside their rules:
-// they take registers that the others do not need (setmaxnreg, by warpgroups).
+// 2280 cycles for S, with seven 450 of 2100 (592 -> 560 us a call).  The softmax warps hold
+// a row of 64 scores beside their rules: they take registers that the others do not need
+// (setmaxnreg, by warpgroups).
 template <bool kFp8>
 struct Roles {
   static constexpr int kExtra = kFp8 ? 7 : 1;

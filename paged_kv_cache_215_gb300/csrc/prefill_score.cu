@@ -19,14 +19,12 @@
 // waits for a ring stage follows every tile of it.
 //
 // Measured, a call (with a CTA for each item): 2 x 2048 bf16 tokens over 8192 in documents,
-// capped, 172 us (181); 4 x 2048 tokens over 16384 E4M3 ones in a window of 4096, 560 us
-// (569); 3 prompts of 1001 f16 tokens, 64 heads on 8, that see a prefix, 81 us (110).  Of the
+// capped, 141 us (181); 4 x 2048 tokens over 16384 E4M3 ones in a window of 4096, 559 us
+// (569); 3 prompts of 1001 f16 tokens, 64 heads on 8, that see a prefix, 80 us (110).  Of the
 // cycles between two items' key tiles some 4000 are the wait for Q, 3500 the output's stores.
-// A key tile takes 1700 (f16), 2100 (E4M3: the converters share the issue slots) and 2900
-// (capped bf16: the instructions of the cap and of P's low half); its matrix products alone
-// would take 1100 (1650 with P's low half), and the softmax warps are behind them.  Two
-// threads a row, in 16 softmax warps that vote on every tile's largest score, took 159, 614
-// and 86 us.
+// A key tile takes 1700 cycles (f16) and 2100 (E4M3: the converters share the issue slots);
+// its matrix products alone would take 1100 (1650 with P's low half on bf16 pools), and the
+// softmax warps are behind them.
 #include <algorithm>
 
 #include "prefill_tc.cuh"
@@ -45,18 +43,31 @@ constexpr int kStages = 5;                   // K/V tiles in flight
 constexpr int kPlans = 4;                     // items planned ahead
 constexpr float kTiny = 0x1p-126f;           // in the place of a scale of 0: -inf times it is -inf
 
-// Warps past the loading one: E4M3 pools' converters, or the one of 16-bit pools that zeroes
-// V rows which no query sees.  With three converters the softmax waited 820 of a key tile's
-// 2280 cycles for S, with seven 450 of 2100 (592 -> 560 us a call).  The softmax warps hold
-// a row of 64 scores beside their rules: they take registers that the others do not need
-// (setmaxnreg, by warpgroups).
-template <bool kFp8>
+// A CTA's warps: the softmax's, the MMA issuers, the loads, then E4M3 pools' converters or
+// the one of 16-bit pools that zeroes V rows which no query sees.  (With three converters
+// the softmax waited 820 of a key tile's 2280 cycles for S, with seven 450 of 2100: 592 ->
+// 560 us a call.)
+//
+// A softmax thread has a row of 64 scores, or with a cap, whose instructions then bound the
+// call, half of one: the other half's thread is in a warp of the same quarter of tensor
+// memory's lanes, and the two warps vote on every tile whether a score passes the row's
+// reference.  One and two threads a row, us: capped documents bf16 159 and 141, f16 143 and
+// 140, E4M3 199 and 166; without a cap windows bf16 602 and 611, E4M3 558 and 614, an f16
+// prompt 81 and 84, distances bf16 180 and 203.  The softmax warps take registers that the
+// others do not need (setmaxnreg, by warpgroups).
+template <int KVT, int kRules>
 struct Roles {
-  static constexpr int kExtra = kFp8 ? 7 : 1;
-  static constexpr int kThreads = kFp8 ? 640 : 512;
-  static constexpr int kLaunchRegs = kFp8 ? 96 : 128;
-  static constexpr int kSoftmaxRegs = kFp8 ? 152 : 160, kOtherRegs = kFp8 ? 56 : 96;
-  static_assert(kThreads >= 32 * (kWarpTMA + 1 + kExtra), "warps");
+  static constexpr bool kFp8 = KVT == PKV_FP8_E4M3;
+  static constexpr int kHalves = kRules == kCap ? 2 : 1;             // threads a row
+  static constexpr int kCols = kN / kHalves;                         // scores a thread
+  static constexpr int kSoftmaxWarps = 4 * kHalves * kQT;
+  static constexpr int kWarpS = kSoftmaxWarps, kWarpPV = kWarpS + kQT, kWarpTMA = kWarpPV + kQT,
+                       kWarpExtra = kWarpTMA + 1, kExtra = kFp8 ? 7 : 1;
+  static constexpr int kThreads = 32 * kSoftmaxWarps + (kFp8 ? 384 : 256);
+  static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;       // 72 to 128
+  static constexpr int kSoftmaxRegs = kHalves == 2 ? (kFp8 ? 80 : 96) : kFp8 ? 152 : 160;
+  static constexpr int kOtherRegs = kFp8 ? 56 : kHalves == 2 ? 48 : 96;
+  static_assert(kThreads >= 32 * (kWarpExtra + kExtra) && kSoftmaxWarps % 4 == 0, "warps");
   static_assert(32 * kSoftmaxWarps * kSoftmaxRegs + (kThreads - 32 * kSoftmaxWarps) * kOtherRegs <=
                     kThreads * kLaunchRegs, "registers");
 };
@@ -86,6 +97,7 @@ struct Bars {
   uint64_t o_final[kQT];                     // the item's last P V has completed
   uint64_t q_ready[kQT];                     // the item's Q tile is staged
   uint32_t tmem;
+  float swap[kQT][kM];                       // between two threads of a row
   uint64_t plan_full[kPlans], plan_empty[kPlans];
   Item plan[kPlans];                         // the CTA's items, found ahead by the loading warp
   Item none;                                 // one without key tiles
@@ -176,23 +188,25 @@ __device__ __forceinline__ void prefetch_q(const DecodeArgs& a, const Item& it, 
   }
 }
 
-// Q tile t of an item into shared memory, by the four softmax warps of tile t: a warp's 32
-// rows, two rows an instruction (a thread for each row would touch 32 lines with every
-// load), all in flight at once.  E4M3 pools run f16 MMAs: a bf16 row is scaled by 2^e, e
-// from its largest |q| as in f16_fit_exponent, before the f16 rounding, exactly; returns e
-// of the thread's own row.  A negative softmax scale is moved onto Q (an exact sign flip).
-template <bool kFp8>
+// Q tile t of an item into shared memory, by the softmax warps of tile t: a warp's 32 rows
+// (or 16 of them: half `half`), two rows an instruction (a thread for each row would touch
+// 32 lines with every load), all in flight at once.  E4M3 pools run f16 MMAs: a bf16 row is
+// scaled by 2^e, e from its largest |q| as in f16_fit_exponent, before the f16 rounding,
+// exactly; returns e of the thread's own row (of two halves: of row lane % 16 of the
+// warp's).  A negative softmax scale is moved onto Q (an exact sign flip).
+template <bool kFp8, int kHalves>
 __device__ __forceinline__ int stage_q(const DecodeArgs& a, const Item& it, int t, uint8_t* sm,
-                                       int warp, int lane) {
-  const int gs = 31 - __clz(a.G), half = lane >> 4, c = lane & 15;   // (G is a power of two)
+                                       int warp, int half, int lane) {
+  const int gs = 31 - __clz(a.G), c = lane & 15;       // (G is a power of two)
   const int tok0 = (it.pair * kQT + t) * (kM >> gs);
   uint8_t* qdst = sm + kSmemQ + t * 2 * kHalf + (c >> 3) * kHalf;
   const uint4* src = static_cast<const uint4*>(a.q) + c;
   const uint32_t flip = a.qk_scale_log2 < 0.f ? 0x80008000u : 0u;
-  const int r0 = (warp & 3) * 32 + half;
-  uint4 v[16];
+  const int r0 = (warp & 3) * 32 + half * 16 + (lane >> 4);
+  constexpr int kPairs = 16 / kHalves;       // of rows
+  uint4 v[kPairs];
 #pragma unroll
-  for (int u = 0; u < 16; ++u) {
+  for (int u = 0; u < kPairs; ++u) {
     const int r = r0 + 2 * u, tok = tok0 + (r >> gs), g = r & (a.G - 1);
     const size_t qrow = ((size_t)it.s * a.q_len + tok) * a.Hq + (size_t)it.hkv * a.G + g;
     v[u] = tok < a.q_len ? src[qrow * (kD / 8)] : make_uint4(0, 0, 0, 0);
@@ -201,7 +215,7 @@ __device__ __forceinline__ int stage_q(const DecodeArgs& a, const Item& it, int 
   if (kFp8 && a.q_dtype == PKV_BF16) {
     // |q| as 16-bit integers order like the values; two rows a register
 #pragma unroll
-    for (int u = 0; u < 16; u += 2) {
+    for (int u = 0; u < kPairs; u += 2) {
       uint32_t m[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -212,13 +226,12 @@ __device__ __forceinline__ int stage_q(const DecodeArgs& a, const Item& it, int 
       uint32_t pk = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) pk = __vmaxu2(pk, __shfl_xor_sync(0xffffffffu, pk, o));
-      // row `lane` of the warp is this thread's in the softmax
       const uint32_t mine = __shfl_sync(0xffffffffu, pk, (lane & 1) * 16);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         auto fit = [](uint32_t e) { return e == 255u ? 0 : min(141 - (int)e, 120); };
         const float qscale = pow2i(fit((pk >> (16 * h + 7)) & 255u));
-        if (lane >> 1 == u + h) q_e = fit((mine >> (16 * h + 7)) & 255u);
+        if (lane % (2 * kPairs) / 2 == u + h) q_e = fit((mine >> (16 * h + 7)) & 255u);
         uint32_t* w = reinterpret_cast<uint32_t*>(&v[u + h]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -229,13 +242,48 @@ __device__ __forceinline__ int stage_q(const DecodeArgs& a, const Item& it, int 
     }
   }
 #pragma unroll
-  for (int u = 0; u < 16; ++u) {
-    const int r = r0 + 2 * u;
-    *reinterpret_cast<uint4*>(qdst + sw128(r, c & 7)) =
+  for (int u = 0; u < kPairs; ++u)
+    *reinterpret_cast<uint4*>(qdst + sw128(r0 + 2 * u, c & 7)) =
         make_uint4(v[u].x ^ flip, v[u].y ^ flip, v[u].z ^ flip, v[u].w ^ flip);
-  }
   fence_proxy_async_smem();
   return q_e;
+}
+
+__device__ __forceinline__ void tmem_ld8_sync(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+// 32 consecutive columns of the warp's 32 lanes, and the wait for them, in one statement: the
+// registers are only defined once the load has completed.
+__device__ __forceinline__ void tmem_ld32_sync(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(taddr)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The two warps of a quarter of a query tile meet at a named barrier; whether one of their
+// threads says so.  (Every wait's outcome is agreed on here, so that the two always go the
+// same way and meet again.)
+__device__ __forceinline__ void pair_sync(int id) {
+  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ bool pair_any(int id, bool said) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+               "bar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r) : "r"((uint32_t)said), "r"(id) : "memory");
+  return r != 0;
 }
 
 // 32 bytes in one store, or in two where the address is only a multiple of 16.
@@ -252,13 +300,20 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wi
 }
 
 template <int KVT, int kRules>
-__global__ void __launch_bounds__(Roles<KVT == PKV_FP8_E4M3>::kThreads, 1)
+__global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
     prefill_score_kernel(const __grid_constant__ CUtensorMap tmap, const DecodeArgs a, int pairs) {
   using C = PfCfg<KVT>;
   constexpr bool kBf16 = C::kBf16, kFp8 = C::kFp8;
-  using Ro = Roles<kFp8>;
+  using Ro = Roles<KVT, kRules>;
+  constexpr int kHalves = Ro::kHalves, kCols = Ro::kCols, kSoftmaxWarps = Ro::kSoftmaxWarps;
+  constexpr int kWarpS = Ro::kWarpS, kWarpPV = Ro::kWarpPV, kWarpTMA = Ro::kWarpTMA;
   constexpr bool kSplitP = kBf16;            // f16 P (11 bits) needs no low term
-  constexpr float kPOff = kSplitP ? 0.f : 7.f;   // f16 P is 2^(s - ref + kPOff)
+  // P = 2^(s - ref + kPOff), ref at most kSlack below the row's largest score so far: in
+  // two bf16 terms far from overflow, so that O is hardly ever rescaled (documents 172 ->
+  // 160 us; keys of four times the usual size had a warp do it every fourth tile); in f16
+  // 2^15 at most, and weights down to 2^-21 of the largest keep every bit (a slack of 12
+  // with 2^-17 saved 1% and added a quarter to an f16 output's error).
+  constexpr float kPOff = kSplitP ? 0.f : 7.f, kSlack = kSplitP ? 60.f : 8.f;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -280,12 +335,12 @@ __global__ void __launch_bounds__(Roles<KVT == PKV_FP8_E4M3>::kThreads, 1)
     for (int t = 0; t < kQT; ++t) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(&bars->s_full[t][b], 1);
-        mbar_init(&bars->p_full[t][b], 128);
+        mbar_init(&bars->p_full[t][b], kHalves == 1 ? 128 : kSoftmaxWarps / kQT);
         mbar_init(&bars->p_free[t][b], 1);
       }
       mbar_init(&bars->o_done[t], 1);
       mbar_init(&bars->o_final[t], 1);
-      mbar_init(&bars->q_ready[t], 128);
+      mbar_init(&bars->q_ready[t], kSoftmaxWarps / kQT);
     }
     for (int i = 0; i < kPlans; ++i) {
       mbar_init(&bars->plan_full[i], 1);
@@ -395,7 +450,7 @@ __global__ void __launch_bounds__(Roles<KVT == PKV_FP8_E4M3>::kThreads, 1)
           const int last = st + (issued - 1 - st) / kStages * kStages;
           mbar_wait_bounded(kFp8 ? &bars->s8_full[st] : &bars->kv_full[st], (last / kStages) & 1);
         }
-    } else if (!kFp8 && warp == kWarpConv) {
+    } else if (!kFp8 && warp == Ro::kWarpExtra) {
       // ---------------------------------------------------------- unseen V rows of 16-bit pools
       // Keys past the sequence's end in its last tile, and ahead of every row's first key:
       // zero V once the tile has landed, so that P = 0 never meets what lies there.
@@ -423,12 +478,12 @@ __global__ void __launch_bounds__(Roles<KVT == PKV_FP8_E4M3>::kThreads, 1)
         }
         g0 += it.T;
       }
-    } else if (kFp8 && warp >= kWarpConv && warp < kWarpConv + Ro::kExtra) {
+    } else if (kFp8 && warp >= Ro::kWarpExtra && warp < Ro::kWarpExtra + Ro::kExtra) {
       // ---------------------------------------------------------- E4M3 -> f16
       // As in prefill_tc.cu: a tile's 64 keys are 16 groups of 4 rows; converter c takes
       // groups [16 c / W, 16 (c + 1) / W), two a step.
       constexpr int W = Ro::kExtra;
-      const int c = warp - kWarpConv, gr0 = 16 * c / W, gr1 = 16 * (c + 1) / W;
+      const int c = warp - Ro::kWarpExtra, gr0 = 16 * c / W, gr1 = 16 * (c + 1) / W;
       const int up = (lane >> 2) & 1, ch = 4 * up + (lane & 3);     // f16 half, source chunk
       const int rsub = 2 * (lane >> 4) + (up ^ ((lane >> 3) & 1));  // row within the group
       const bool scaled = a.block_scales != nullptr;
@@ -578,11 +633,31 @@ __global__ void __launch_bounds__(Roles<KVT == PKV_FP8_E4M3>::kThreads, 1)
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ softmax, one row per thread
+    // ------------------------------------------------------------ softmax, one or two threads a row
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Ro::kSoftmaxRegs));
-    const int G = a.G, QT = kM / G, t = warp / 4, r = tid - 128 * t, row_tok = r / G,
-              row_head = r % G;
+    const int G = a.G, QT = kM / G, t = warp / 4 % kQT;
+    const int half = kHalves == 2 ? warp / (4 * kQT) : 0;
+    const int r = (warp & 3) * 32 + lane, row_tok = r / G, row_head = r % G;
     const uint32_t tcol = tmem + ((uint32_t)((warp & 3) * 32) << 16) + t * 256;
+    const int meet = 1 + t * 4 + (warp & 3);           // the two warps' barrier
+    float* swap = &bars->swap[t][r];
+    // both threads' values of a row by f (the warp's barrier ahead has freed the place)
+    auto both = [&](float v, auto f) {
+      if (kHalves == 1) return v;
+      if (half == 1) *swap = v;
+      pair_sync(meet);
+      if (half == 0) {
+        v = f(v, *swap);
+        *swap = v;
+      }
+      pair_sync(meet);
+      return half == 1 ? *swap : v;
+    };
+    // a wait that both warps pass, or neither
+    auto wait_both = [&](uint64_t* bar, uint32_t parity) {
+      const bool got = wait(bar, parity);
+      return kHalves == 1 ? got : !pair_any(meet, !got);
+    };
     const bool bscaled = kFp8 && a.block_scales != nullptr;
     int c = 0, finals = 0;                 // the query tile's key tiles and finished items so far
     int q_e = 0;
@@ -599,106 +674,141 @@ __global__ void __launch_bounds__(Roles<KVT == PKV_FP8_E4M3>::kThreads, 1)
       if constexpr (kRules == kDistance) slope = a.slopes[it->hkv * G + row_head] * kLog2e;
       float mref = -INFINITY, lsum = 0.f;
       for (int j = 0; j < my_tiles && ok; ++j, ++c) {
-        const int b = c & 1, kpos0 = (it->jt0 + j) * kN;
+        const int b = c & 1, kpos0 = (it->jt0 + j) * kN + half * kCols;
         // of 16 keys each: the scale (with a cap over it; E4M3: times their block's K scale)
-        float qsb[4];
+        float qsb[kCols / 16];
 #pragma unroll
-        for (int g4 = 0; g4 < 4; ++g4) qsb[g4] = kRules >= kCap && a.cap_in != 0.f ? cap_in : qs;
+        for (int g4 = 0; g4 < kCols / 16; ++g4) qsb[g4] = kRules >= kCap && a.cap_in != 0.f ? cap_in : qs;
         if (bscaled) {
           // issued before the wait for S, so the loads overlap it
           const int32_t* trow = a.tables + (size_t)it->s * a.max_blocks;
           const int nblk = (it->n + a.BS - 1) / a.BS;
 #pragma unroll
-          for (int g4 = 0; g4 < 4; ++g4) {
+          for (int g4 = 0; g4 < kCols / 16; ++g4) {
             int blk = trow[max(min((kpos0 + 16 * g4) / a.BS, nblk - 1), it->blk0)];
             blk = (blk < 0 || blk >= a.num_blocks) ? 0 : blk;
             qsb[g4] *= a.block_scales[((size_t)blk * 2 * a.L + a.layer) * a.Hkv + it->hkv];
             if (qsb[g4] == 0.f) qsb[g4] = kTiny;
           }
         }
-        if (!wait(&bars->s_full[t][b], (c >> 1) & 1)) {
-          ok = false;
-          break;
-        }
+        ok = wait(&bars->s_full[t][b], (c >> 1) & 1);      // (two warps agree on it below)
+        if (kHalves == 1 && !ok) break;
         tc_fence_after();
-        float sv[kN];
-        tmem_ld64_sync(tcol + b * kN, sv);
+        float sv[kCols];
+        if constexpr (kHalves == 2) tmem_ld32_sync(tcol + b * kN + half * kCols, sv);
+        else tmem_ld64_sync(tcol + b * kN, sv);
         if constexpr (kRules >= kCap) {
           // to log2 units here (the cap is no factor of the largest score)
 #pragma unroll
-          for (int g4 = 0; g4 < 4; ++g4) {
+          for (int g4 = 0; g4 < kCols / 16; ++g4) {
             scale_scores<16>(sv + 16 * g4, qsb[g4]);
             qsb[g4] = 1.f;
           }
-          if (kRules == kCap || a.cap_in != 0.f) cap_scores<kN>(sv, a.cap_out);
+          if (kRules == kCap || a.cap_in != 0.f) cap_scores<kCols>(sv, a.cap_out);
         }
         if constexpr (kRules == kDistance) {
           const float d0 = (float)(pos - kpos0);
-          if (__all_sync(0xffffffffu, pos >= kpos0 + kN - 1)) {
+          if (__all_sync(0xffffffffu, pos >= kpos0 + kCols - 1)) {
             // every key lies behind its query: - slope (d0 - x), two keys an instruction
             const uint64_t s2 = f2_pack(slope, slope);
 #pragma unroll
-            for (int x = 0; x < kN; x += 2) {
+            for (int x = 0; x < kCols; x += 2) {
               const uint64_t d2 = f2_pack((float)x - d0, (float)(x + 1) - d0);
               f2_unpack(ffma2(s2, d2, f2_pack(sv[x], sv[x + 1])), sv[x], sv[x + 1]);
             }
           } else {
 #pragma unroll
-            for (int x = 0; x < kN; ++x) sv[x] = fmaf(-slope, fabsf(d0 - (float)x), sv[x]);
+            for (int x = 0; x < kCols; ++x) sv[x] = fmaf(-slope, fabsf(d0 - (float)x), sv[x]);
           }
         }
         const int c0 = keys.lo - kpos0, c1 = keys.hi - kpos0;
-        if (!__all_sync(0xffffffffu, c0 <= 0 && c1 >= kN)) {
+        if (!__all_sync(0xffffffffu, c0 <= 0 && c1 >= kCols)) {
 #pragma unroll
-          for (int x = 0; x < kN; ++x) sv[x] = x >= c0 && x < c1 ? sv[x] : -INFINITY;
+          for (int x = 0; x < kCols; ++x) sv[x] = x >= c0 && x < c1 ? sv[x] : -INFINITY;
         }
-        // row max over the scores (8 partial maxima, two per 16-key group: short dependency
-        // chains); the scales are positive, so each group's commutes with its max
-        float mp[8];
+        // the largest of the thread's scores (partial maxima: short dependency chains); the
+        // scales are positive, so each group's commutes with its max
+        float mp[kCols / 8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mp[e] = -INFINITY;
+        for (int e = 0; e < kCols / 8; ++e) mp[e] = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < kN; x += 2) {
+        for (int x = 0; x < kCols; x += 2) {
           const int e = 2 * (x >> 4) + ((x >> 1) & 1);
           mp[e] = fmax3(mp[e], sv[x], sv[x + 1]);
         }
-        const float mx = fmaxf(fmaxf(qsb[0] * fmaxf(mp[0], mp[1]), qsb[1] * fmaxf(mp[2], mp[3])),
-                               fmaxf(qsb[2] * fmaxf(mp[4], mp[5]), qsb[3] * fmaxf(mp[6], mp[7])));
-        bool rescale = false;
-        float alpha = 1.f;
-        if (mx > mref + 8.f) {            // also the first visible key (mref = -inf)
-          alpha = exp2f(mref - mx);       // 0 when mref = -inf
-          mref = mx;
-          rescale = j > 0;
-        }
-        const float ref = mref == -INFINITY ? 0.f : mref;
-        uint64_t pp[4];                   // partial row sums, two lanes each
+        float mx = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pp[e] = 0ull;
-        // a rescale needs O stable: the P V before this key tile's has completed
-        if (__any_sync(0xffffffffu, rescale)) {
-          if (j > 0) {
+        for (int g4 = 0; g4 < kCols / 16; ++g4)
+          mx = fmaxf(mx, qsb[g4] * fmaxf(mp[2 * g4], mp[2 * g4 + 1]));
+        // The reference moves where a score passes it by kSlack (the first seen key does);
+        // what was summed is then brought to the new one, once the P V before this key
+        // tile's has completed.  (Before its first key a row's O is 0.)
+        float alpha = 1.f;
+        if constexpr (kHalves == 1) {
+          bool rescale = false;
+          if (mx > mref + kSlack) {
+            rescale = mref != -INFINITY;
+            alpha = exp2f(mref - mx);     // 0 when mref = -inf
+            mref = mx;
+          }
+          if (__any_sync(0xffffffffu, rescale)) {
             if (!wait(&bars->o_done[t], (c - 1) & 1)) {
               ok = false;
               break;
             }
             tc_fence_after();
-          }
-          const float f = rescale ? alpha : 1.f;
+            const float f = rescale ? alpha : 1.f;
 #pragma unroll
-          for (int x = 0; x < kD; x += 32) {
-            float o[32];
-            tmem_ld32(tcol + 128 + x, o);
-            tmem_ld_wait();
+            for (int x = 0; x < kD; x += 32) {
+              float o[32];
+              tmem_ld32_sync(tcol + 128 + x, o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= f;
-            tmem_st32(tcol + 128 + x, o);
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tmem_st32(tcol + 128 + x, o);
+            }
           }
+        } else {
+          // the vote also lets P be written over S, which both warps have read
+          tc_fence_before();
+          if (pair_any(meet, !ok || mx > mref + kSlack)) {
+            if (pair_any(meet, !ok)) {
+              ok = false;
+              break;
+            }
+            mx = both(mx, [](float x, float y) { return fmaxf(x, y); });
+            bool rescale = false;
+            if (mx > mref + kSlack) {
+              rescale = mref != -INFINITY;
+              alpha = exp2f(mref - mx);
+              mref = mx;
+            }
+            if (pair_any(meet, rescale)) {
+              if (!wait_both(&bars->o_done[t], (c - 1) & 1)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const float f = rescale ? alpha : 1.f;
+#pragma unroll 1
+              for (int x = half * (kD / 2); x < (half + 1) * (kD / 2); x += 8) {
+                uint32_t o[8];            // (few: the scores hold the registers)
+                tmem_ld8_sync(tcol + 128 + x, o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st8(tcol + 128 + x, o);
+              }
+            }
+          }
+          tc_fence_after();
         }
+        const float ref = mref == -INFINITY ? 0.f : mref;
+        uint64_t pp[4];                   // partial row sums, two lanes each
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pp[e] = 0ull;
         // P over S in TMEM, packed pairs: hi in columns 0..31 of the buffer, lo in 32..63
         const uint64_t nref2 = f2_pack(kPOff - ref, kPOff - ref);
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
+        for (int q4 = 0; q4 < kCols / 16; ++q4) {
           const uint64_t qs2 = f2_pack(qsb[q4], qsb[q4]);
           uint32_t phi[8], plo[8];
 #pragma unroll
@@ -722,8 +832,8 @@ __global__ void __launch_bounds__(Roles<KVT == PKV_FP8_E4M3>::kThreads, 1)
               phi[c2] = pack2<kBf16>(p0, p1);
             }
           }
-          tmem_st8(tcol + b * kN + q4 * 8, phi);
-          if (kSplitP) tmem_st8(tcol + b * kN + 32 + q4 * 8, plo);
+          tmem_st8(tcol + b * kN + half * (kCols / 2) + q4 * 8, phi);
+          if (kSplitP) tmem_st8(tcol + b * kN + 32 + half * (kCols / 2) + q4 * 8, plo);
         }
         float ps = 0.f;
 #pragma unroll
@@ -735,7 +845,9 @@ __global__ void __launch_bounds__(Roles<KVT == PKV_FP8_E4M3>::kThreads, 1)
         lsum = lsum * alpha + ps;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&bars->p_full[t][b]);
+        // (one thread a row: gathering the warp for one arrival, E4M3 window 559 -> 574 us)
+        if (kHalves == 2) __syncwarp();
+        if (kHalves == 1 || leader) mbar_arrive(&bars->p_full[t][b]);
       }
       if (!ok) break;
       // the next item's Q (every S of this one is computed, so its Q has been read), whose
@@ -751,14 +863,22 @@ __global__ void __launch_bounds__(Roles<KVT == PKV_FP8_E4M3>::kThreads, 1)
       }
       if (q + 1 < items) {
         it = &bars->plan[(q + 1) % kPlans];
-        ok = wait(&bars->plan_full[(q + 1) % kPlans], ((q + 1) / kPlans) & 1);
+        ok = wait_both(&bars->plan_full[(q + 1) % kPlans], ((q + 1) / kPlans) & 1);
         if (!ok) break;
         const int next = (it->pair * kQT + t) * QT + row_tok;
         keys = {0, 0};
         if (next < a.q_len) keys = key_range(a, it->s, it->n, next);
         if (it->tiles_of(t) > 0) {
-          q_e = stage_q<kFp8>(a, *it, t, sm, warp, lane);
-          mbar_arrive(&bars->q_ready[t]);
+          q_e = stage_q<kFp8, kHalves>(a, *it, t, sm, warp, half, lane);
+          __syncwarp();
+          if (leader) mbar_arrive(&bars->q_ready[t]);
+          if (kFp8 && kHalves == 2) {
+            // a row's exponent from the thread whose warp staged it (the barrier of the wait
+            // above has freed the place)
+            if (lane >> 4 == half) *swap = __int_as_float(q_e);
+            pair_sync(meet);
+            if (lane >> 4 != half) q_e = __float_as_int(*swap);
+          }
         }
       }
       // O row / l -> out (every lane reads TMEM; live rows store).  The next item's first
@@ -766,20 +886,19 @@ __global__ void __launch_bounds__(Roles<KVT == PKV_FP8_E4M3>::kThreads, 1)
       const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
       float inv = 0.f;
       if (my_tiles > 0) {
-        if (!wait(&bars->o_final[t], finals++ & 1)) {
-          ok = false;
-          break;
-        }
+        ok = wait_both(&bars->o_final[t], finals++ & 1);
+        if (!ok) break;
         tc_fence_after();
+        lsum = both(lsum, [](float x, float y) { return x + y; });
         inv = lsum > 0.f ? a.v_scale / lsum : 0.f;
         if (bscaled) inv = ldexpf(inv, ev);
       }
-#pragma unroll
-      for (int x = 0; x < kD; x += 32) {
+#pragma unroll(kHalves == 2 ? 1 : 4)
+      for (int x0 = 0; x0 < kD / kHalves; x0 += 32) {
+        const int x = half * (kD / 2) + x0;
         float o[32];
         if (my_tiles > 0) {
-          tmem_ld32(tcol + 128 + x, o);
-          tmem_ld_wait();
+          tmem_ld32_sync(tcol + 128 + x, o);
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
@@ -826,7 +945,7 @@ __global__ void __launch_bounds__(Roles<KVT == PKV_FP8_E4M3>::kThreads, 1)
 
 template <int KVT, int kRules>
 cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, int sms, cudaStream_t stream) {
-  using Ro = Roles<KVT == PKV_FP8_E4M3>;
+  using Ro = Roles<KVT, kRules>;
   const size_t smem = kSmemBytes + sizeof(Bars) + kAlignSlack;
   auto kernel = prefill_score_kernel<KVT, kRules>;
   cudaError_t e =

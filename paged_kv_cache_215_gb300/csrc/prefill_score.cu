@@ -77,17 +77,22 @@ struct Item {
   int n;                     // the sequence's tokens
   int jt0, T;                // key tiles jt0 .. jt0 + T - 1; T = 0: no row sees a key
   int tiles[kQT];            // of them, query tile t's: the first tiles[t]
+  // What no row sees may hold anything, and its blocks' table entries may be stale: keys
+  // ahead of every row's first, from `end` on, and the gaps that rows without keys leave.
   int head;                  // keys of the first tile ahead of every row's
-  int blk0;                  // the block of the first seen key (entries ahead may be stale)
-  int tail;                  // local index of the sequence's ragged last tile, or -1
+  int blk0;                  // the block of the first seen key
+  int end;                   // n, or with documents the end of the item's last seen key
+  int tail;                  // local index of the tile that `end` cuts, or -1
+  int gap0, gap1;            // tiles [gap0, gap1) hold all gaps (bars->gaps)
   int ev;                    // E4M3 block scales: V is taken over 2^ev
 
   __device__ __forceinline__ int tiles_of(int t) const { return t == 0 ? tiles[0] : tiles[1]; }
 };
-// Whether tile j of an item has V rows that no query sees.
+// Whether tile j of an item has V rows that no row sees at its ends.
 __device__ __forceinline__ bool needs_zeros(const Item& it, int j) {
   return (j == 0 && it.head > 0) || j == it.tail;
 }
+constexpr int kGapWords = kQT * kM / 32;      // a bit for each token of an item
 
 struct Bars {
   uint64_t kv_full[kStages], kv_empty[kStages];
@@ -96,10 +101,13 @@ struct Bars {
   uint64_t s_full[kQT][2], p_full[kQT][2], p_free[kQT][2], o_done[kQT];
   uint64_t o_final[kQT];                     // the item's last P V has completed
   uint64_t q_ready[kQT];                     // the item's Q tile is staged
+  uint64_t gap_full;                         // a tile with gaps has landed
   uint32_t tmem;
   float swap[kQT][kM];                       // between two threads of a row
   uint64_t plan_full[kPlans], plan_empty[kPlans];
   Item plan[kPlans];                         // the CTA's items, found ahead by the loading warp
+  uint32_t gaps[kPlans][kGapWords];          // a bit an own position (where gap0 < gap1)
+  int blocks[kStages][kN / 16];              // E4M3: the blocks in a stage
   Item none;                                 // one without key tiles
   volatile int abort_flag;
 };
@@ -121,9 +129,11 @@ __device__ __forceinline__ int items_of_cta(long long items) {
   return full + (item_index(full) < items);
 }
 
-// Item `index`; whole warps (each finds the same).
-__device__ __forceinline__ Item item_of(const DecodeArgs& a, long long index, int pairs, int lane) {
+// Item `index`; whole warps (each finds the same).  `empty`: some row sees no key.
+__device__ __forceinline__ Item item_of(const DecodeArgs& a, long long index, int pairs, int lane,
+                                        bool* empty) {
   Item it;
+  bool none = false;
   const int QT = kM / a.G;
   it.hkv = (int)(index % a.Hkv);
   const long long r = index / a.Hkv;
@@ -138,12 +148,14 @@ __device__ __forceinline__ Item item_of(const DecodeArgs& a, long long index, in
       const int tok = (it.pair * kQT + t) * QT + i;
       if (tok >= a.q_len) break;
       const KeyRange k = key_range(a, it.s, it.n, tok);
+      none = none || k.lo >= k.hi;
       if (k.lo >= k.hi) continue;
       lo = min(lo, k.lo);
       hi[t] = max(hi[t], k.hi);
     }
     hi[t] = __reduce_max_sync(0xffffffffu, hi[t]);
   }
+  *empty = __any_sync(0xffffffffu, none);
   lo = __reduce_min_sync(0xffffffffu, lo);
   it.jt0 = lo / kN;
   it.T = 0;
@@ -154,21 +166,92 @@ __device__ __forceinline__ Item item_of(const DecodeArgs& a, long long index, in
   }
   it.head = it.T > 0 ? lo - it.jt0 * kN : 0;
   it.blk0 = lo / a.BS;
-  const int last = it.n % kN != 0 ? (it.n - 1) / kN - it.jt0 : -1;
+  it.end = it.n;
+  if (a.doc_starts) {        // (without documents every key from the first on is some row's)
+    it.end = hi[0];
+#pragma unroll
+    for (int t = 1; t < kQT; ++t) it.end = max(it.end, hi[t]);
+  }
+  const int last = it.end % kN != 0 ? (it.end - 1) / kN - it.jt0 : -1;
   it.tail = last < it.T ? last : -1;
+  it.gap0 = it.gap1 = 0;
   it.ev = 0;
   return it;
 }
 
+// The keys between an item's first and last that no row of it sees; whole warps.  A row
+// that sees its own position sees all from its first key to there, so only positions of the
+// item's own rows can be gaps: those that neither a row from there on nor a row inside the
+// prefix (which sees the prefix to its end) reaches.
+__device__ __forceinline__ void find_gaps(const DecodeArgs& a, Item& it, uint32_t* gaps, int lane) {
+  constexpr int kFar = 0x7fffffff;
+  const int toks = kQT * kM / a.G, tok0 = it.pair * toks, pos0 = it.n - a.q_len + tok0;
+  const int prefix = a.prefix_lens ? min(a.prefix_lens[it.s], it.n) : 0;
+  auto first = [&](int i) {
+    if (i >= toks || tok0 + i >= a.q_len) return kFar;
+    const KeyRange k = key_range(a, it.s, it.n, tok0 + i);
+    return k.lo < k.hi ? k.lo : kFar;
+  };
+  int in_prefix = kFar;                          // the first key of the rows inside it
+  for (int i = lane; i < toks && pos0 + i < prefix; i += 32) in_prefix = min(in_prefix, first(i));
+  in_prefix = __reduce_min_sync(0xffffffffu, in_prefix);
+  int behind = kFar, lo = kFar, hi = -1;         // the first key of the rows behind; gaps' range
+  for (int w = (toks + 31) / 32 - 1; w >= 0; --w) {
+    int m = first(32 * w + lane);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_down_sync(0xffffffffu, m, o);
+      if (lane + o < 32) m = min(m, y);
+    }
+    m = min(m, behind);
+    const int pos = pos0 + 32 * w + lane;
+    const bool gap = pos >= it.jt0 * kN + it.head && pos < it.end && m > pos &&
+                     (pos >= prefix || in_prefix > pos);
+    if (gap) {
+      lo = min(lo, pos);
+      hi = max(hi, pos);
+    }
+    const uint32_t word = __ballot_sync(0xffffffffu, gap);
+    if (lane == 0) gaps[w] = word;
+    behind = __shfl_sync(0xffffffffu, m, 0);
+  }
+  __syncwarp();
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (hi >= 0) {
+    it.gap0 = lo / kN - it.jt0;
+    it.gap1 = hi / kN - it.jt0 + 1;
+  }
+}
+__device__ __forceinline__ bool in_gap(const DecodeArgs& a, const Item& it, const uint32_t* gaps,
+                                       int pos) {
+  const int toks = kQT * kM / a.G, i = pos - (it.n - a.q_len + it.pair * toks);
+  return i >= 0 && i < toks && (gaps[i / 32] >> (i % 32) & 1u);
+}
+
+// The block that is read in the place of block b of local tile j: b itself where some row may
+// see a key of it, else one with a seen key.
+__device__ __forceinline__ int block_read(const DecodeArgs& a, const Item& it, const uint32_t* gaps,
+                                          int j, int b) {
+  b = min(max(b, it.blk0), (it.end - 1) / a.BS);
+  if (j >= it.gap0 && j < it.gap1) {
+    int x = b * a.BS;
+    while (x < (b + 1) * a.BS && in_gap(a, it, gaps, x)) ++x;
+    if (x == (b + 1) * a.BS) b = it.blk0;
+  }
+  return b;
+}
+
 // E4M3 block scales: the largest power-of-two exponent among the V scales of an item's
 // blocks (0 if there is none); whole warps.
-__device__ __forceinline__ int v_exponent(const DecodeArgs& a, const Item& it, int lane) {
-  const int bpt = kN / a.BS, nblk = (it.n + a.BS - 1) / a.BS;
+__device__ __forceinline__ int v_exponent(const DecodeArgs& a, const Item& it, const uint32_t* gaps,
+                                          int lane) {
+  const int bpt = kN / a.BS, nblk = (it.end + a.BS - 1) / a.BS;
   const int32_t* trow = a.tables + (size_t)it.s * a.max_blocks;
   const int b1 = min((it.jt0 + it.T) * bpt, nblk);
   int ev = -100000;
   for (int b = max(it.jt0 * bpt, it.blk0) + lane; b < b1; b += 32) {
-    int blk = trow[b];
+    int blk = trow[block_read(a, it, gaps, b / bpt - it.jt0, b)];
     blk = (blk < 0 || blk >= a.num_blocks) ? 0 : blk;
     const float vs = a.block_scales[((size_t)(blk * 2 + 1) * a.L + a.layer) * a.Hkv + it.hkv];
     if (vs > 0.f && isfinite(vs)) ev = max(ev, ilogbf(vs));
@@ -346,6 +429,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
       mbar_init(&bars->plan_full[i], 1);
       mbar_init(&bars->plan_empty[i], kSoftmaxWarps + kIssuers + Ro::kExtra);
     }
+    mbar_init(&bars->gap_full, 1);
     bars->abort_flag = 0;
     bars->none = Item{};
     fence_mbar_init();
@@ -387,16 +471,19 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
     if (warp == kWarpTMA) {
       // ---------------------------------------------------------- loads
       const int bpt = kN / a.BS;             // blocks per key tile
-      int issued = 0;
+      int issued = 0, gap_tiles = 0;
       Item it{}, next{};
       for (int q = -1; q < items && ok; ++q) {
         // item q + 1 is planned ahead of item q's loads
         if (q + 1 < items) {
-          next = item_of(a, item_index(q + 1), pairs, lane);
-          if (kFp8 && a.block_scales && next.T > 0) next.ev = v_exponent(a, next, lane);
+          bool empty;
+          next = item_of(a, item_index(q + 1), pairs, lane, &empty);
           if (q + 1 >= kPlans)
             ok = wait(&bars->plan_empty[(q + 1) % kPlans], ((q + 1) / kPlans - 1) & 1);
           if (!ok) break;
+          uint32_t* gaps = bars->gaps[(q + 1) % kPlans];
+          if (a.doc_starts && empty && next.T > 0) find_gaps(a, next, gaps, lane);
+          if (kFp8 && a.block_scales && next.T > 0) next.ev = v_exponent(a, next, gaps, lane);
           prefetch_q(a, next, lane);
           if (leader) {
             bars->plan[(q + 1) % kPlans] = next;
@@ -404,7 +491,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
           }
           __syncwarp();
         }
-        const int nblk = (it.n + a.BS - 1) / a.BS;
+        const int nblk = (it.end + a.BS - 1) / a.BS;
         const int32_t* trow = a.tables + (size_t)it.s * a.max_blocks;
         int ids = 0, id_base = -1;           // block ids, 32 at a time
         for (int j = 0; j < it.T && ok; ++j) {
@@ -417,18 +504,26 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
             ids = id_base + lane < nblk ? trow[id_base + lane] : 0;
           }
           // lane l < 2 * bpt loads one box: block l / 2 of the tile, K or V (l & 1).  Blocks
-          // past the sequence's last one and ahead of the first seen key's are replaced by
-          // those: their keys are hidden and their V rows zeroed before use.
+          // without a key that some row may see are replaced by one with: their keys are
+          // hidden and their V rows zeroed before use.
           const int jb = min(max(first + (lane >> 1), it.blk0), nblk - 1);
           int blk = __shfl_sync(0xffffffffu, ids, jb - id_base);
-          uint64_t* bar = kFp8 ? &bars->s8_full[st] : &bars->kv_full[st];
+          const bool gapped = j >= it.gap0 && j < it.gap1;
+          if (gapped && block_read(a, it, bars->gaps[q % kPlans], j, jb) != jb)
+            blk = trow[it.blk0];
+          uint64_t* full = kFp8 ? &bars->s8_full[st] : &bars->kv_full[st];
+          uint64_t* bar = gapped ? &bars->gap_full : full;
+          if (blk < 0 || blk >= a.num_blocks) {
+            if (lane < 2 * bpt) record_error(a.status, PKV_EBOUNDS);
+            blk = 0;
+          }
+          if (kFp8) {
+            if (lane < 2 * bpt) bars->blocks[st][lane >> 1] = blk;
+            __syncwarp();
+          }
           if (leader) mbar_arrive_expect_tx(bar, kFp8 ? kStage8Bytes : kStageBytes);
           __syncwarp();
           if (lane < 2 * bpt) {
-            if (blk < 0 || blk >= a.num_blocks) {
-              record_error(a.status, PKV_EBOUNDS);
-              blk = 0;
-            }
             const int kv = lane & 1;
             const int z = (blk * 2 + kv) * a.L + a.layer;
             uint8_t* dst = sm + stage_off(st);
@@ -440,6 +535,24 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
                           it.hkv * a.BS / 8, z);
           }
           issued = g + 1;
+          if (gapped) {
+            // V rows in gaps are zeroed ahead of everyone's view of the tile (a wait for this
+            // load, where a sequence has rows without keys among others)
+            ok = wait(&bars->gap_full, gap_tiles++ & 1);
+            if (!ok) break;
+            uint8_t* vbuf = sm + stage_off(st) + (kFp8 ? 3 : 2) * kKVHalf;
+            constexpr int kRow = kFp8 ? 8 : 16;    // 16-byte pieces
+            for (int i = lane; i < kN * kRow; i += 32) {
+              const int r = i / kRow, c16 = i % kRow;
+              if (!in_gap(a, it, bars->gaps[q % kPlans], (it.jt0 + j) * kN + r)) continue;
+              const uint32_t at = kFp8 ? sw128(r, c16)
+                                       : ((r >> 3) * 2 + (c16 >> 3)) * 1024 + sw128(r & 7, c16 & 7);
+              *reinterpret_cast<uint4*>(vbuf + at) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (leader) mbar_arrive(full);
+          }
         }
         g0 += it.T;
         it = next;
@@ -452,8 +565,8 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
         }
     } else if (!kFp8 && warp == Ro::kWarpExtra) {
       // ---------------------------------------------------------- unseen V rows of 16-bit pools
-      // Keys past the sequence's end in its last tile, and ahead of every row's first key:
-      // zero V once the tile has landed, so that P = 0 never meets what lies there.
+      // Keys behind the last one that may be seen, and ahead of every row's first key: zero V
+      // once the tile has landed, so that P = 0 never meets what lies there.
       for (int q = 0; q < items && ok; ++q) {
         const Item it = planned(q);
         // (it follows every tile: a wait for a phase two ahead would end at once)
@@ -463,7 +576,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
           if (!ok) break;
           if (needs_zeros(it, j)) {
             uint8_t* vbuf = sm + stage_off(st) + 2 * kKVHalf;
-            const int r0 = j == 0 ? it.head : 0, r1 = it.n - (it.jt0 + j) * kN;
+            const int r0 = j == 0 ? it.head : 0, r1 = it.end - (it.jt0 + j) * kN;
             for (int i = lane; i < kN * 16; i += 32) {
               const int r = i / 16, c16 = i % 16;
               if (r < r0 || r >= r1)
@@ -489,15 +602,13 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
       const bool scaled = a.block_scales != nullptr;
       for (int q = 0; q < items && ok; ++q) {
         const Item it = planned(q);
-        const int nblk = (it.n + a.BS - 1) / a.BS;
-        const int32_t* trow = a.tables + (size_t)it.s * a.max_blocks;
         for (int j = 0; j < it.T && ok; ++j) {
           const int g = g0 + j, st = g % kStages;
           ok = wait(&bars->s8_full[st], (g / kStages) & 1);
           if (!ok) break;
           uint8_t* dst = sm + stage_off(st);
           const uint8_t* src = dst + 2 * kKVHalf;          // E4M3 K rows, then V rows
-          const int valid = it.n - (it.jt0 + j) * kN;      // keys of the tile in the sequence
+          const int valid = it.end - (it.jt0 + j) * kN;    // keys of the tile that may be seen
           const int skip = j == 0 ? it.head : 0;           // keys ahead of every row's
           const bool zeros = needs_zeros(it, j);
 #pragma unroll 1
@@ -512,9 +623,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
               xk[h] = *reinterpret_cast<const uint4*>(src + sw128(r, ch));
               xv[h] = *reinterpret_cast<const uint4*>(src + kKVHalf + sw128(r, ch));
               if (scaled) {
-                const int jb = min(max((it.jt0 + j) * (kN / a.BS) + r / a.BS, it.blk0), nblk - 1);
-                int blk = trow[jb];
-                blk = (blk < 0 || blk >= a.num_blocks) ? 0 : blk;
+                const int blk = bars->blocks[st][r / a.BS];
                 sv[h] = ldexpf(
                     a.block_scales[((size_t)(blk * 2 + 1) * a.L + a.layer) * a.Hkv + it.hkv],
                     -it.ev);
@@ -539,7 +648,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
                     o[e] = pack_f16(f.x * sv[h], f.y * sv[h]);
                   }
                 }
-                // keys that nobody sees: zero V, so that P = 0 never meets NaN
+                // keys that no row sees: zero V, so that P = 0 never meets NaN
                 if (kv && zeros && (r >= valid || r < skip)) {
 #pragma unroll
                   for (int e = 0; e < 8; ++e) o[e] = 0u;
@@ -682,10 +791,10 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
         if (bscaled) {
           // issued before the wait for S, so the loads overlap it
           const int32_t* trow = a.tables + (size_t)it->s * a.max_blocks;
-          const int nblk = (it->n + a.BS - 1) / a.BS;
 #pragma unroll
           for (int g4 = 0; g4 < kCols / 16; ++g4) {
-            int blk = trow[max(min((kpos0 + 16 * g4) / a.BS, nblk - 1), it->blk0)];
+            int blk = trow[block_read(a, *it, bars->gaps[q % kPlans], j,
+                                      (kpos0 + 16 * g4) / a.BS)];
             blk = (blk < 0 || blk >= a.num_blocks) ? 0 : blk;
             qsb[g4] *= a.block_scales[((size_t)blk * 2 * a.L + a.layer) * a.Hkv + it->hkv];
             if (qsb[g4] == 0.f) qsb[g4] = kTiny;

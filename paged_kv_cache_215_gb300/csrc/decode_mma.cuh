@@ -97,8 +97,8 @@ struct Cursor {
 template <int kMode>
 __device__ __forceinline__ int clamp_len(const DecodeArgs& a, int s) {
   if constexpr (is_scored(kMode)) {
-    const int n = scored_len(a, s);
-    return n - first_read(a, s, n);
+    const KeyRange r = read_range(a, s, scored_len(a, s));
+    return r.hi - r.lo;
   }
   int n = __ldg(a.seq_lens + s);
   int cap = a.max_blocks * a.BS;
@@ -191,10 +191,12 @@ struct Consumer {
   int lim[NT][2];          // last key position each of the thread's columns may see
   // scored calls (positions count from the first token read): the columns' rules (of
   // this warp, in shared memory: registers are short and most blocks need none of them),
-  // and over all columns the smallest and largest first and last keys
+  // and over all columns the largest first and the smallest last key; of one query token
+  // its first and last key
   ColumnRule* rules;
   int col0;                // the first of the warp's 8 columns (a warp for each 8 rows)
-  int from_min, from_max, lim_min, lim_max;
+  int from_max, lim_min;
+  int from_min, lim_max;
   float cap_in_;
   float* score_rows;       // the unit's rows in a.scores, or nullptr
   // E4M3 with block-wise scales: acc is held in units of 2^ev_ref_, the largest
@@ -250,7 +252,7 @@ struct Consumer {
   __device__ __forceinline__ void load_q(const DecodeArgs& a, int s, int n, int hkv, int lane) {
     if constexpr (kSingle) {
       load_q_decode(a, s, hkv, lane);
-      if constexpr (kScore) load_rules_one(a, s, n, hkv);
+      if constexpr (kScore) load_rules_one(a, s, hkv);
       return;
     }
     const int c = lane & 3;
@@ -275,7 +277,7 @@ struct Consumer {
       qk_scale_log2_ = a.qk_scale_log2 * pow2i(-e);
       if constexpr (kScore) cap_in_ = a.cap_in * pow2i(-e);
     }
-    if constexpr (kScore) load_rules(a, s, n, hkv, lane);
+    if constexpr (kScore) load_rules(a, s, hkv, lane);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const long long qr = q_row(a, s, hkv, column(nt * 8 + (lane >> 2)));
@@ -308,19 +310,19 @@ struct Consumer {
     }
   }
 
-  // One query token: its first and last key of the n tokens that the unit reads.
-  __device__ __forceinline__ void load_rules_one(const DecodeArgs& a, int s, int n, int hkv) {
-    const int len = scored_len(a, s), off = len - n;
-    const KeyRange k = key_range(a, s, len, 0);
+  // One query token: its first and last key of the tokens that the unit reads (read_range).
+  __device__ __forceinline__ void load_rules_one(const DecodeArgs& a, int s, int hkv) {
+    const KeyRange k = key_range(a, s, scored_len(a, s), 0);
+    const int off = k.lo / BS * BS;
     from_min = k.lo - off;
     lim_max = k.hi - 1 - off;
     if constexpr (one_record(kMode))
       score_rows = a.scores + (((int64_t)s * a.Hkv + hkv) * a.max_len + off) * a.score_row;
   }
 
-  // The columns' rules in a unit that reads n tokens.
-  __device__ __forceinline__ void load_rules(const DecodeArgs& a, int s, int n, int hkv, int lane) {
-    const int len = scored_len(a, s), off = len - n;
+  // The columns' rules.
+  __device__ __forceinline__ void load_rules(const DecodeArgs& a, int s, int hkv, int lane) {
+    const int len = scored_len(a, s), off = read_range(a, s, len).lo;
     ColumnRule r{0x7fffffff, -1, 0, 0.f};           // a column that sees no key
     __syncwarp();                                   // the unit before has read its rules
     const int row = col0 + lane;
@@ -336,10 +338,8 @@ struct Consumer {
       if (a.slopes) r.slope = a.slopes[hkv * a.G + g] * kLog2e;
     }
     if (lane < 8) rules[lane] = r;
-    from_min = __reduce_min_sync(0xffffffffu, r.from);
     from_max = __reduce_max_sync(0xffffffffu, live ? r.from : -1);
     lim_min = __reduce_min_sync(0xffffffffu, live ? r.lim : 0x7fffffff);
-    lim_max = __reduce_max_sync(0xffffffffu, r.lim);
     __syncwarp();
     score_rows = nullptr;
     if (a.scores)
@@ -375,6 +375,25 @@ struct Consumer {
         }
     }
     if (score_rows) record(a, s, jbase, valid, lane);
+  }
+
+  // Whether a column sees the thread's tokens of V's fragments: four bits a tile, for its
+  // tokens 2c, 2c + 1, 2c + 8 and 2c + 9 (the scores of a token lie in four lanes).
+  __device__ __forceinline__ uint32_t seen_tokens(const float (&s)[kTiles][NT][4], int lane) const {
+    const int c = lane & 3;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        bool any = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          any = any || s[mt][nt][k] != -INFINITY || s[mt][nt][k + 1] != -INFINITY;
+        const uint32_t two = __ballot_sync(0xffffffffu, any) >> (8 * c);
+        bits |= ((two & 0xfu ? 1u : 0u) | (two & 0xf0u ? 2u : 0u)) << (4 * mt + k);
+      }
+    return bits;
   }
 
   __device__ __forceinline__ void record_one(const DecodeArgs& a, const float (&s)[kTiles][4],
@@ -759,7 +778,11 @@ struct Consumer {
     float mx[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
-    if constexpr (kScore) apply_rules(a, s, ks_b, jbase, valid, full, lane);
+    uint32_t seen = 0;
+    if constexpr (kScore) {
+      apply_rules(a, s, ks_b, jbase, valid, full, lane);
+      if (!full) seen = seen_tokens(s, lane);
+    }
 #pragma unroll
     for (int mt = 0; mt < kTiles; ++mt) {
       if constexpr (kScore) {
@@ -853,21 +876,19 @@ struct Consumer {
 
     // ---- O^T += V^T P^T
     // Rows of V past the sequence's end are unwritten slots, and in a scored call rows
-    // that no column sees may hold anything: their lanes are zeroed (only in a tail
-    // block) so that 0 * NaN never reaches the sum.
-    int v0 = 0, v1 = valid;
-    if constexpr (kScore) {
-      v0 = from_min - jbase;
-      v1 = min(valid, lim_max + 1 - jbase);
-    }
-    const bool tail = v1 < BS || (kScore && v0 > 0);
+    // that no column sees may hold anything: their lanes are zeroed (only in a block that
+    // has some) so that 0 * NaN never reaches the sum.
+    const bool tail = kScore ? !full : valid < BS;
 #pragma unroll
     for (int mt = 0; mt < kTiles; ++mt) {
       // tokens of this thread in the A fragment: 2c, 2c+1 (regs 0,1) and 8+2c, 9+2c (regs 2,3)
       uint32_t mk_lo = 0xffffffffu, mk_hi = 0xffffffffu;
       if (tail) {
         const int tl = mt * 16 + 2 * c;
-        auto in = [&](int t) { return t < v1 && (!kScore || t >= v0); };
+        auto in = [&](int t) {
+          const int x = t - mt * 16 - 2 * c;           // 0, 1, 8 or 9
+          return kScore ? (seen >> (4 * mt + (x & 1) + (x >> 2)) & 1u) != 0 : t < valid;
+        };
         mk_lo = (in(tl) ? 0x0000ffffu : 0u) | (in(tl + 1) ? 0xffff0000u : 0u);
         mk_hi = (in(tl + 8) ? 0x0000ffffu : 0u) | (in(tl + 9) ? 0xffff0000u : 0u);
       }
@@ -1219,7 +1240,7 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
         if constexpr (kMode == kSuffix)
           jo = first_token(a, cur.s, min(max(__ldg(a.seq_lens + cur.s), 0), a.max_blocks * BS)) /
                BS;
-        if constexpr (is_scored(kMode)) jo = (scored_len(a, cur.s) - cur.n) / BS;
+        if constexpr (is_scored(kMode)) jo = read_range(a, cur.s, scored_len(a, cur.s)).lo / BS;
         const int32_t* entry = a.tables + (size_t)cur.s * a.max_blocks + jo + jj;
         ids = jj >= cur.nb ? 0 : is_scored(kMode) ? *entry : __ldg(entry);
       }

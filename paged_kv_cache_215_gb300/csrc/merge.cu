@@ -279,7 +279,7 @@ __device__ __forceinline__ void accumulate_tokens(const DecodeArgs& a, const Wei
   __shared__ float lse[16];
   // the attention ahead has waited for everything before it, and writes none of these
   const int n = scored_len(a, s);
-  const int from = first_read(a, s, n);
+  const KeyRange read = read_range(a, s, n);
   const float* win =
       in.data ? in.data + s * in.seq_stride + h * in.head_stride + j0 + threadIdx.x : nullptr;
   float y[TOKENS][ROW], w[TOKENS];
@@ -295,7 +295,7 @@ __device__ __forceinline__ void accumulate_tokens(const DecodeArgs& a, const Wei
   for (int k = 0; k < TOKENS; ++k) {
     const int j = j0 + k * kThreads + threadIdx.x;
     const float* row = scores + k * kThreads * ROW;
-    if (j >= from && j < n) {
+    if (j >= read.lo && j < read.hi) {
       if constexpr (ROW >= 4) {
 #pragma unroll
         for (int r = 0; r < ROW; r += 4)

@@ -39,23 +39,23 @@ __device__ __forceinline__ KeyRange key_range(const DecodeArgs& a, int s, int n,
   return {lo, hi};
 }
 
-// The first key that any query token of the sequence sees; n if none sees a key.
-__device__ __forceinline__ int first_key(const DecodeArgs& a, int s, int n) {
-  if (a.window <= 0 && !a.doc_starts) return n > 0 ? 0 : n;
-  int first = n;
-  for (int i = max(0, a.q_len - n); i < a.q_len; ++i) {
-    const KeyRange k = key_range(a, s, n, i);
-    if (k.lo < k.hi) first = min(first, k.lo);
-    if (!a.doc_starts) break;                  // the window's starts only grow
+// The tokens [lo, hi) the scored decode reads of a sequence: from the block of the first key
+// that any query token sees up to the last one that any sees; hi <= lo if none sees a key.
+__device__ __forceinline__ KeyRange read_range(const DecodeArgs& a, int s, int n) {
+  KeyRange all{n, n};
+  if (!a.doc_starts) {                         // every query sees its own key
+    if (n > 0) all.lo = a.window > 0 ? max(0, max(n - a.q_len, 0) - a.window + 1) : 0;
+  } else {
+    all.hi = 0;
+    for (int i = max(0, a.q_len - n); i < a.q_len; ++i) {
+      const KeyRange k = key_range(a, s, n, i);
+      if (k.lo >= k.hi) continue;
+      all.lo = min(all.lo, k.lo);
+      all.hi = max(all.hi, k.hi);
+    }
+    if (all.hi == 0) return {0, 0};
   }
-  return first;
-}
-
-// The first token the scored decode reads of a sequence: its first seen key's block;
-// n if there is none.
-__device__ __forceinline__ int first_read(const DecodeArgs& a, int s, int n) {
-  const int f = first_key(a, s, n);
-  return f >= n ? n : f / a.BS * a.BS;
+  return {all.lo / a.BS * a.BS, all.hi};
 }
 
 // tanh within 2^-22 of itself: below 0.6 an odd polynomial (fitted by weighted least

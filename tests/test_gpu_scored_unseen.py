@@ -84,3 +84,23 @@ def test_chunk(kv, hq, hkv, bs, q_len, rules, kind):
     want = case.reference(**r)
     hide_unseen(case, **r)
     case.check(run(case, torch.float32, **r), want)
+
+
+@pytest.mark.parametrize("kind", ["behind", "between", "every third", "any"])
+@pytest.mark.parametrize("rules", RULES)
+@pytest.mark.parametrize("kv,hq,hkv,bs,q_len", [
+    ("bf16", 4, 2, 16, 8), ("f16", 2, 2, 32, 16), ("e4m3", 2, 1, 16, 7), ("scaled", 8, 2, 64, 4),
+    ("bf16", 6, 2, 64, 5)])
+def test_drafts(kv, hq, hkv, bs, q_len, rules, kind):
+    lens = [q_len, 150, 2 * bs + 3, 0, bs + q_len - 1]
+    case = Case(lens, hq, hkv, 128, "e4m3" if kv == "scaled" else kv, bs, q_len, seed=32,
+                block_scales=kv == "scaled")
+    r = rules_of(case, kind, rules, seed=q_len)
+    want = case.reference(**r)
+    hide_unseen(case, **r)
+    before = torch.rand(len(lens), hkv, 160).cuda()
+    w = torch.full((len(lens), hkv, 160), -5.0, device="cuda")
+    case.check(run(case, torch.float32, w, before, **r), want, w, before)
+    for b, n in enumerate(lens):                           # columns behind the sequence
+        assert (w[b, :, n:] == -5.0).all()
+    case.check(run(case, torch.float32, **r), want)

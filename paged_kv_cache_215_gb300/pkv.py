@@ -214,6 +214,15 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _workspace(nbytes: int, device, stream) -> torch.Tensor:
+    """Scratch of a call on `stream`, from that stream's memory: what another stream has
+    freed may still be in use there, and what this one frees stays behind the call."""
+    if stream is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+
+
 def _ptr(t: Optional[torch.Tensor]):
     if t is None:
         return None
@@ -439,11 +448,8 @@ class KVPool:
         the new lengths, index [B, Hkv, any] int32 the slots they had.  The old blocks are
         only read; free them afterwards.  One call a layer, all into the same blocks."""
         if workspace is None and index is None:
-            workspace = torch.empty(max(16, evict_workspace_bytes(self.geom, tables.shape[0],
-                                                                  max_seq_len)),
-                                    dtype=torch.uint8, device=self.storage.device)
-            if stream is not None:
-                workspace.record_stream(stream)
+            workspace = _workspace(evict_workspace_bytes(self.geom, tables.shape[0], max_seq_len),
+                                   self.storage.device, stream)
         rc = _tensors.evict(self.handle.value if self.handle else 0, self.storage, layer,
                             new_tables, tables, seq_lens, max_seq_len, keep, recent, weights,
                             new_weights, new_lens, index, workspace, stream)
@@ -512,7 +518,7 @@ def paged_decode_attention(out, q, pool: KVPool, layer, tables, seq_lens, max_se
                            stream=None):
     if workspace is None:
         nb = workspace_bytes(pool.geom, q.shape[0], max_seq_len, num_splits)
-        workspace = torch.empty(max(nb, 16), dtype=torch.uint8, device=pool.storage.device)
+        workspace = _workspace(nb, pool.storage.device, stream)
     args = (_ptr(out), TORCH_CODE[out.dtype], _ptr(q), TORCH_CODE[q.dtype], pool.handle, layer,
             _ptr(tables), tables.shape[1], _ptr(seq_lens), q.shape[0], max_seq_len, scale,
             k_scale, v_scale, num_splits, _ptr(workspace), workspace.numel())
@@ -531,7 +537,7 @@ def paged_decode_attention_partial(out, lse, q, pool: KVPool, layer, tables, seq
     the natural log-sum-exp lse [B, Hq] of every row (for merging key ranges)."""
     if workspace is None:
         nb = workspace_bytes(pool.geom, q.shape[0], max_seq_len, 0)
-        workspace = torch.empty(max(nb, 16), dtype=torch.uint8, device=pool.storage.device)
+        workspace = _workspace(nb, pool.storage.device, stream)
     assert out.dtype == torch.float32 and lse.dtype == torch.float32
     _check(_lib.paged_decode_attention_partial(
         _ptr(out), _ptr(lse), _ptr(q), TORCH_CODE[q.dtype], pool.handle, layer, _ptr(tables),
@@ -558,7 +564,7 @@ def paged_decode_step(out, q, k_new, v_new, pool: KVPool, layer, tables, seq_len
     (fused into one attention launch on the tensor-core kernel)."""
     if workspace is None:
         nb = workspace_bytes(pool.geom, q.shape[0], max_seq_len, num_splits)
-        workspace = torch.empty(max(nb, 16), dtype=torch.uint8, device=pool.storage.device)
+        workspace = _workspace(nb, pool.storage.device, stream)
     _check(_lib.paged_decode_step(
         _ptr(out), TORCH_CODE[out.dtype], _ptr(q), TORCH_CODE[q.dtype], _ptr(k_new), _ptr(v_new),
         TORCH_CODE[k_new.dtype], pool.handle, layer, _ptr(tables), tables.shape[1],
@@ -577,7 +583,7 @@ def paged_decode_attention_mq(out, q, pool: KVPool, layer, tables, seq_lens, max
     if workspace is None:
         nb = int(_lib.paged_decode_workspace_bytes_mq(ctypes.byref(pool.geom), B, q_len,
                                                       max_seq_len, num_splits))
-        workspace = torch.empty(max(nb, 16), dtype=torch.uint8, device=pool.storage.device)
+        workspace = _workspace(nb, pool.storage.device, stream)
     _check(_lib.paged_decode_attention_mq(
         _ptr(out), TORCH_CODE[out.dtype], _ptr(q), TORCH_CODE[q.dtype], q_len, pool.handle, layer,
         _ptr(tables), tables.shape[1], _ptr(seq_lens), B, max_seq_len, scale, k_scale, v_scale,
@@ -605,7 +611,7 @@ def paged_decode_attention_cascade(out, q, pool: KVPool, layer, prefix_table, pr
     B = q.shape[0]
     if workspace is None:
         nb = cascade_workspace_bytes(pool.geom, B, tables.shape[1], max_seq_len, prefix_len_max)
-        workspace = torch.empty(max(nb, 16), dtype=torch.uint8, device=pool.storage.device)
+        workspace = _workspace(nb, pool.storage.device, stream)
     _check(_lib.paged_decode_attention_cascade(
         _ptr(out), TORCH_CODE[out.dtype], _ptr(q), TORCH_CODE[q.dtype], pool.handle, layer,
         _ptr(prefix_table), int(prefix_table.numel()) if prefix_table is not None else 0,
@@ -654,12 +660,9 @@ def paged_decode_attention_scored(out, q, pool: KVPool, layer, tables, seq_lens,
     KV head; pass one tensor as both to accumulate."""
     if workspace is None:
         q_len = q.shape[1] if q.dim() == 4 else 1
-        workspace = torch.empty(
-            max(16, scored_workspace_bytes(pool.geom, q.shape[0], q_len, max_seq_len,
-                                           weights is not None)),
-            dtype=torch.uint8, device=pool.storage.device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _workspace(scored_workspace_bytes(pool.geom, q.shape[0], q_len, max_seq_len,
+                                                      weights is not None),
+                               pool.storage.device, stream)
     r = scores if scores is not None else _NO_RULES
     rc = _tensors.attend_scored(out, q, pool.handle.value if pool.handle else 0, pool.storage,
                                 layer, tables, seq_lens, max_seq_len, scale, r.cap, r.window,

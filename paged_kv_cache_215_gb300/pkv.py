@@ -496,14 +496,17 @@ def fp8_scales(k_parts, v_parts, stream=None):
     """Per-tensor E4M3 scales (k_scale, v_scale) of K and V held in pieces (for
     example the cached tokens and the new ones): kv_absmax of every piece, then
     kv_fp8_scale of each tensor, on the device; the two floats are read back."""
+    if stream is not None:
+        with torch.cuda.stream(stream):              # what is made and read back here too
+            return fp8_scales(k_parts, v_parts)
     dev = k_parts[0].device
     amax = torch.zeros(len(k_parts) + len(v_parts), dtype=torch.float32, device=dev)
     for i, x in enumerate(list(k_parts) + list(v_parts)):
-        kv_absmax(x, amax[i:i + 1], stream)
+        kv_absmax(x, amax[i:i + 1])
     sc = torch.empty(2, dtype=torch.float32, device=dev)
     nk = len(k_parts)
-    kv_fp8_scale(amax[:nk], sc[0:1], stream)
-    kv_fp8_scale(amax[nk:], sc[1:2], stream)
+    kv_fp8_scale(amax[:nk], sc[0:1])
+    kv_fp8_scale(amax[nk:], sc[1:2])
     k, v = sc.cpu().tolist()
     return k, v
 

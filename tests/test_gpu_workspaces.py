@@ -106,3 +106,15 @@ def test_evictions_on_two_streams_leave_each_others_scratch_alone():
             t = torch.arange(2000)
             at = lambda table, x: case.pool[table[0].cpu().long()[x // 16].cuda(), :, 0, h, (x % 16).cuda()]
             assert torch.equal(at(fresh, t), at(case.tables, j))
+
+
+def test_scales_are_read_back_behind_their_stream():
+    from paged_kv_cache_215_gb300 import pkv
+    x = [torch.randn(1000, device="cuda") for _ in range(3)]
+    want = pkv.fp8_scales(x[:2], x[2:])
+    pkv.fp8_scales([9 * x[0]], [7 * x[1]])                 # what is free now holds other scales
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)                      # what is launched there runs later
+    assert pkv.fp8_scales(x[:2], x[2:], stream=side) == want and min(want) > 0

@@ -392,11 +392,13 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
   constexpr int kWarpS = Ro::kWarpS, kWarpPV = Ro::kWarpPV, kWarpTMA = Ro::kWarpTMA;
   constexpr bool kSplitP = kBf16;            // f16 P (11 bits) needs no low term
   // P = 2^(s - ref + kPOff), ref at most kSlack below the row's largest score so far: in
-  // two bf16 terms far from overflow, so that O is hardly ever rescaled (documents 172 ->
-  // 160 us; keys of four times the usual size had a warp do it every fourth tile); in f16
-  // 2^15 at most, and weights down to 2^-21 of the largest keep every bit (a slack of 12
-  // with 2^-17 saved 1% and added a quarter to an f16 output's error).
-  constexpr float kPOff = kSplitP ? 0.f : 7.f, kSlack = kSplitP ? 60.f : 8.f;
+  // two bf16 terms 2^8 at most, as in the plain chunk (values above 2^120 / keys overflow),
+  // and 2^-24 or more for the largest, so that O is hardly ever rescaled (capped documents
+  // with a slack of 8, 16, 24, 32, 60: 165, 159, 150, 146, 145 us; keys of four times the
+  // usual size have a warp do it every fourth tile at 8); in f16 2^15 at most, and weights
+  // down to 2^-21 of the largest keep every bit (a slack of 12 with 2^-17 saved 1% and added
+  // a quarter to an f16 output's error).
+  constexpr float kSlack = kSplitP ? 32.f : 8.f, kPOff = kSplitP ? 8.f - kSlack : 7.f;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);

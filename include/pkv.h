@@ -604,8 +604,8 @@ PKV_API size_t paged_decode_scored_workspace_bytes(const pkv_geometry* geom, int
  * copied).  weights have rows of max_seq_len columns or more.  d_workspace:
  * kv_evict_workspace_bytes bytes (0 with d_index), 16-byte aligned.  E4M3 pools with
  * block scales attached: PKV_EUNSUPPORTED (a token cannot leave its block's scale).
- * PKV_EINVAL for NULL pointers, sizes below 0, overlapping rows of new_weights, and a
- * d_new_lens that overlaps d_seq_lens or d_keep; PKV_EUNSUPPORTED where a sequence could
+ * PKV_EINVAL for NULL pointers, sizes below 0, overlapping rows of new_weights, rows of
+ * new_weights that overlap rows of weights (max_seq_len columns each), and a d_new_lens that overlaps d_seq_lens or d_keep; PKV_EUNSUPPORTED where a sequence could
  * keep more than 4194240 tokens. */
 PKV_API int kv_evict(pkv_pool* pool, int layer, const int32_t* d_new_tables, int max_new_blocks,
                      const int32_t* d_tables, int max_blocks_per_seq, const int32_t* d_seq_lens,

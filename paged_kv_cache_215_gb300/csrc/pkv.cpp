@@ -1158,6 +1158,42 @@ static bool same_or_apart(const pkv_rows* out, const pkv_rows* in, int64_t token
           (heads == 1 || out->head_stride == in->head_stride));
 }
 
+// Whether an fp32 row of in_cols elements of `in` meets one of out_cols elements of `out`,
+// whose rows are apart (out_rows_ok).  (Strides are any 63-bit numbers: sums in 128.)
+static bool rows_meet(const pkv_rows& in, int64_t in_cols, const pkv_rows& out, int64_t out_cols,
+                      int64_t tokens, int heads) {
+  using Wide = __int128;
+  if (in_cols <= 0 || out_cols <= 0) return false;
+  // out's rows in the order of memory: `inner` of them a stride `near` apart, `outer` times
+  const bool heads_in = out.token_stride >= out.head_stride ? heads > 1 : tokens == 1;
+  const Wide near = heads_in ? out.head_stride : out.token_stride;
+  const Wide far = heads_in ? out.token_stride : out.head_stride;
+  const int64_t inner = heads_in ? heads : tokens, outer = heads_in ? tokens : heads;
+  const Wide apart = ((Wide)reinterpret_cast<intptr_t>(in.data) -
+                      (Wide)reinterpret_cast<intptr_t>(out.data)) / 4;
+  const Wide in_end = apart + (Wide)(tokens - 1) * in.token_stride +
+                      (Wide)(heads - 1) * in.head_stride + in_cols;
+  const Wide out_end = (outer - 1) * (outer > 1 ? far : 0) + (inner - 1) * (inner > 1 ? near : 0) +
+                       out_cols;
+  if (in_end <= 0 || apart >= out_end) return false;          // the usual case
+  for (int64_t t = 0; t < (in.token_stride ? tokens : 1); ++t)
+    for (int64_t h = 0; h < (in.head_stride ? heads : 1); ++h) {
+      const Wide x = apart + (Wide)t * in.token_stride + (Wide)h * in.head_stride;
+      // the first of out's rows that ends behind x
+      Wide start = 0;
+      if (x >= out_cols) {
+        const Wide y = x - out_cols;                          // it starts behind y
+        const Wide o = outer > 1 ? std::min<Wide>(y / far, outer - 1) : 0;
+        const Wide i = inner > 1 ? (y - o * far) / near + 1 : 1;
+        if (i < inner) start = o * far + i * near;
+        else if (o + 1 < outer) start = (o + 1) * far;
+        else continue;
+      }
+      if (start < x + in_cols) return true;
+    }
+  return false;
+}
+
 // One token or one head: its stride is never used; 0 keeps it out of the
 // alignment rule.
 static void set_rows(const pkv_rows* r, int64_t tokens, int heads, int64_t* ts, int64_t* hs) {
@@ -1552,7 +1588,8 @@ int kv_evict(pkv_pool* p, int layer, const int32_t* d_new_tables, int max_new_bl
   const pkv_rows out{new_weights->data, new_weights->seq_stride, new_weights->head_stride};
   if (!rows_ok(&in, PKV_F32) ||
       !out_rows_ok(&out, PKV_F32, batch, g.num_kv_heads, std::max(new_width, 1)) ||
-      in.data == out.data)
+      in.data == out.data ||
+      rows_meet(in, max_seq_len, out, new_width, batch, g.num_kv_heads))
     return PKV_EINVAL;
   if (p->d_block_scales || batch > 65535 || g.num_kv_heads > 65535) return PKV_EUNSUPPORTED;
   EvictArgs a{};

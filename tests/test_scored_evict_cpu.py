@@ -151,3 +151,33 @@ def test_evict_refuses_lengths_written_over_read_ones(pkv):
     assert evict(pkv, p.h, lens=far(7), keep=far(-8), **big) == bad
     assert evict(pkv, p.h, lens=far(8), keep=far(-4), **big) == bad
     p.close()
+
+
+def test_evict_refuses_new_weights_that_meet_the_weights(pkv):
+    """Against every pair of rows: 2 sequences, 2 heads, 40 columns read, 8 written."""
+    p = FakePool(pkv, nb=8)
+    at, most, width = 1 << 24, 40, 8
+    met = apart = 0
+    for seq_in, head_in in ((80, 40), (200, 100), (50, 130), (0, 0), (400, 0), (0, 48)):
+        for seq_out, head_out in ((16, 8), (200, 100), (100, 200), (8, 60), (43, 9), (60, 52)):
+            for d in range(-260, 420, 13):
+                read = {d + s * seq_in + h * head_in + j
+                        for s in range(2) for h in range(2) for j in range(most)}
+                written = {s * seq_out + h * head_out + j
+                           for s in range(2) for h in range(2) for j in range(width)}
+                w, o = rows(pkv, at + 4 * d, seq_in, head_in), rows(pkv, at, seq_out, head_out)
+                # (a workspace too small: nothing is launched where there is a GPU)
+                got = evict(pkv, p.h, w=w, o=o, most=most, width=width, wsb=0)
+                assert got == (pkv.PKV_EINVAL if read & written else pkv.PKV_ENOMEM), \
+                    (seq_in, head_in, seq_out, head_out, d)
+                met += bool(read & written)
+                apart += not read & written
+    assert met > 300 and apart > 300
+    far = (1 << 62) - 1                                       # strides whose sums pass 64 bits
+    assert evict(pkv, p.h, w=rows(pkv, at, far, far), o=rows(pkv, at + 156, far, 16),
+                 width=8, most=40, wsb=0) == pkv.PKV_EINVAL
+    assert evict(pkv, p.h, w=rows(pkv, at, far, far), o=rows(pkv, at - 512, far, 16),
+                 width=8, most=40, wsb=0) == pkv.PKV_ENOMEM
+    one = lambda a, b: evict(pkv, p.h, B=1, w=rows(pkv, a, 0, 64), o=rows(pkv, b, 0, 64), wsb=0)
+    assert one(at, at + 4 * 127) == pkv.PKV_EINVAL and one(at, at + 4 * 128) == pkv.PKV_ENOMEM
+    p.close()

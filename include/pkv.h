@@ -564,8 +564,9 @@ typedef struct {
  * Types and shapes as in paged_decode_attention_mq with num_splits = 0, and for q_len = 1
  * any head_dim (a multiple of 8; other than 128, with f32 pools or with f32 q on the CUDA
  * cores) and up to 16 query heads per KV head; weights take up to 16 query rows per KV
- * head; else PKV_EUNSUPPORTED.  PKV_EINVAL also for a cap or window below 0, a cap that is not
- * finite, and a scale (not 0) / cap or a cap * log2(e) that no normal fp32 number holds. */
+ * head; max_seq_len up to 2^31 - 2^16; else PKV_EUNSUPPORTED.  PKV_EINVAL also for a cap
+ * or window below 0, a cap that is not finite, and a scale (not 0) / cap or a
+ * cap * log2(e) that no normal fp32 number holds. */
 PKV_API int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* d_q,
                                           pkv_dtype q_dtype, int q_len, const pkv_pool* pool,
                                           int layer, const int32_t* d_block_tables,
@@ -604,9 +605,10 @@ PKV_API size_t paged_decode_scored_workspace_bytes(const pkv_geometry* geom, int
  * copied).  weights have rows of max_seq_len columns or more.  d_workspace:
  * kv_evict_workspace_bytes bytes (0 with d_index), 16-byte aligned.  E4M3 pools with
  * block scales attached: PKV_EUNSUPPORTED (a token cannot leave its block's scale).
- * PKV_EINVAL for NULL pointers, sizes below 0, overlapping rows of new_weights, rows of
- * new_weights that overlap rows of weights (max_seq_len columns each), and a d_new_lens that overlaps d_seq_lens or d_keep; PKV_EUNSUPPORTED where a sequence could
- * keep more than 4194240 tokens. */
+ * PKV_EINVAL for NULL pointers, sizes below 0, rows of new_weights that overlap one
+ * another or the rows of weights, and a d_new_lens that overlaps d_seq_lens or d_keep;
+ * PKV_EUNSUPPORTED where a sequence could keep more than 4194240 tokens, and for a
+ * max_seq_len or new_width above 2^31 - 2^16. */
 PKV_API int kv_evict(pkv_pool* pool, int layer, const int32_t* d_new_tables, int max_new_blocks,
                      const int32_t* d_tables, int max_blocks_per_seq, const int32_t* d_seq_lens,
                      int batch, int max_seq_len, const int32_t* d_keep, int recent,

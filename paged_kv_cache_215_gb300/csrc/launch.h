@@ -213,6 +213,7 @@ struct EvictArgs {
   int max_len, recent;
   int capacity;              // tokens the new tables, weights and index hold
 };
+constexpr int kMaxSlots = 0x7fff0000;         // of a sequence (a slot + a tile fits 32 bits)
 constexpr int kMaxEvictKept = 65535 * 64;     // tokens a sequence keeps (a grid's third extent)
 cudaError_t launch_evict(const EvictArgs& a, int sms, cudaStream_t stream);
 

@@ -1469,11 +1469,12 @@ int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* 
       w_in = {weights_in->data, weights_in->seq_stride, weights_in->head_stride};
     }
   }
+  if (batch > 65535 || g.num_kv_heads > 65535 || max_seq_len > kMaxSlots ||
+      (int64_t)q_len * g.num_q_heads > 0x7fffffff)
+    return PKV_EUNSUPPORTED;
   DeviceInfo dev;
   if (!device_info(&dev)) return PKV_ECUDA;
   const int G = g.num_q_heads / g.num_kv_heads;
-  if (batch > 65535 || g.num_kv_heads > 65535) return PKV_EUNSUPPORTED;
-  if ((int64_t)q_len * g.num_q_heads > 0x7fffffff) return PKV_EUNSUPPORTED;
 
   DecodeArgs a{};
   a.q = d_q;
@@ -1591,7 +1592,9 @@ int kv_evict(pkv_pool* p, int layer, const int32_t* d_new_tables, int max_new_bl
       in.data == out.data ||
       rows_meet(in, max_seq_len, out, new_width, batch, g.num_kv_heads))
     return PKV_EINVAL;
-  if (p->d_block_scales || batch > 65535 || g.num_kv_heads > 65535) return PKV_EUNSUPPORTED;
+  if (p->d_block_scales || batch > 65535 || g.num_kv_heads > 65535 || max_seq_len > kMaxSlots ||
+      new_width > kMaxSlots)
+    return PKV_EUNSUPPORTED;
   EvictArgs a{};
   const long long slots = (long long)max_new_blocks * g.block_size;
   a.capacity = (int)std::min<long long>(std::min(slots, (long long)new_width),

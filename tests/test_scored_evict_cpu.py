@@ -181,3 +181,18 @@ def test_evict_refuses_new_weights_that_meet_the_weights(pkv):
     one = lambda a, b: evict(pkv, p.h, B=1, w=rows(pkv, a, 0, 64), o=rows(pkv, b, 0, 64), wsb=0)
     assert one(at, at + 4 * 127) == pkv.PKV_EINVAL and one(at, at + 4 * 128) == pkv.PKV_ENOMEM
     p.close()
+
+
+def test_sequences_whose_slots_leave_32_bits_are_refused(pkv):
+    p = FakePool(pkv, nb=8)
+    most = 2 ** 31 - 2 ** 16                                  # (no workspace: nothing is launched)
+    for n, codes in ((most, (pkv.PKV_ECUDA, pkv.PKV_ENOMEM)), (most + 1, (pkv.PKV_EUNSUPPORTED,)),
+                     (2 ** 31 - 1, (pkv.PKV_EUNSUPPORTED,))):
+        assert scored(pkv, p.h, most=n, mb=1 << 27, ws=None) in codes
+        w = rows(pkv, 1 << 40, 1 << 32, 1 << 31)
+        assert scored(pkv, p.h, None, w, most=n, mb=1 << 27, ws=None) in codes
+        codes = tuple(c for c in codes if c != pkv.PKV_ECUDA)
+        assert evict(pkv, p.h, w=w, most=n, mb=1 << 27, ws=None) in codes
+        wide = rows(pkv, 1 << 44, 1 << 32, 1 << 31)
+        assert evict(pkv, p.h, o=wide, width=n, ws=None) in codes
+    p.close()

@@ -354,7 +354,7 @@ struct Consumer {
     float* flat = &s[0][0][0];
     if (a.cap_in != 0.f) {
       scale_scores<kTiles * NT * 4>(flat, cap_in_ * ks_b);
-      cap_scores_fine<kTiles * NT * 4>(flat, a.cap_out);
+      cap_scores_fine<kTiles * NT * 4>(flat, a.cap_out, full);
     } else {
       scale_scores<kTiles * NT * 4>(flat, qk_scale_log2_ * ks_b);
     }
@@ -491,7 +491,7 @@ struct Consumer {
     float qs = T::kFp8 ? qk_scale_log2_ * ks_b : qk_scale_log2_;
     if constexpr (one_cap(kMode)) {
       scale_scores<kTiles * 4>(&s[0][0], T::kFp8 ? cap_in_ * ks_b : cap_in_);
-      cap_scores_fine<kTiles * 4>(&s[0][0], a.cap_out);
+      cap_scores_fine<kTiles * 4>(&s[0][0], a.cap_out, first <= 0 && valid >= BS);
       qs = 1.f;
     }
     float mx0 = -INFINITY, mx1 = -INFINITY;

@@ -97,7 +97,7 @@ constexpr int kGapWords = kQT * kM / 32;      // a bit for each token of an item
 struct Bars {
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t s8_full[kStages];                 // E4M3: the stage's E4M3 tile has landed
-  uint64_t v_fixed[kStages];                 // the stage's unseen V rows are zero (16-bit pools)
+  uint64_t v_fixed[kStages];                 // the stage's unseen rows are zero (16-bit pools)
   uint64_t s_full[kQT][2], p_full[kQT][2], p_free[kQT][2], o_done[kQT];
   uint64_t o_final[kQT];                     // the item's last P V has completed
   uint64_t q_ready[kQT];                     // the item's Q tile is staged
@@ -391,6 +391,8 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
   constexpr int kHalves = Ro::kHalves, kCols = Ro::kCols, kSoftmaxWarps = Ro::kSoftmaxWarps;
   constexpr int kWarpS = Ro::kWarpS, kWarpPV = Ro::kWarpPV, kWarpTMA = Ro::kWarpTMA;
   constexpr bool kSplitP = kBf16;            // f16 P (11 bits) needs no low term
+  // where a cap's polynomial goes by the scores, keys that no row sees are zeroed with V's rows
+  constexpr bool kZeroK = kRules >= kCap;
   // P = 2^(s - ref + kPOff), ref at most kSlack below the row's largest score so far: in
   // two bf16 terms 2^8 at most, as in the plain chunk (values above 2^120 / keys overflow),
   // and 2^-24 or more for the largest, so that O is hardly ever rescaled (capped documents
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
       // ---------------------------------------------------------- loads
       const int bpt = kN / a.BS;             // blocks per key tile
       int issued = 0, gap_tiles = 0;
-      Item it{}, next{};
+      Item held{}, next{};
       for (int q = -1; q < items && ok; ++q) {
         // item q + 1 is planned ahead of item q's loads
         if (q + 1 < items) {
@@ -493,6 +495,8 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
           }
           __syncwarp();
         }
+        // (registers are short: read in place; E4M3 a copy, in place its window call takes 568 us for 553)
+        const Item& it = kFp8 ? held : q < 0 ? bars->none : bars->plan[q % kPlans];
         const int nblk = (it.end + a.BS - 1) / a.BS;
         const int32_t* trow = a.tables + (size_t)it.s * a.max_blocks;
         int ids = 0, id_base = -1;           // block ids, 32 at a time
@@ -538,11 +542,12 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
           }
           issued = g + 1;
           if (gapped) {
-            // V rows in gaps are zeroed ahead of everyone's view of the tile (a wait for this
+            // rows in gaps are zeroed ahead of everyone's view of the tile (a wait for this
             // load, where a sequence has rows without keys among others)
             ok = wait(&bars->gap_full, gap_tiles++ & 1);
             if (!ok) break;
             uint8_t* vbuf = sm + stage_off(st) + (kFp8 ? 3 : 2) * kKVHalf;
+            uint8_t* kbuf = vbuf - (kFp8 ? 1 : 2) * kKVHalf;
             constexpr int kRow = kFp8 ? 8 : 16;    // 16-byte pieces
             for (int i = lane; i < kN * kRow; i += 32) {
               const int r = i / kRow, c16 = i % kRow;
@@ -550,6 +555,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
               const uint32_t at = kFp8 ? sw128(r, c16)
                                        : ((r >> 3) * 2 + (c16 >> 3)) * 1024 + sw128(r & 7, c16 & 7);
               *reinterpret_cast<uint4*>(vbuf + at) = make_uint4(0, 0, 0, 0);
+              if (kZeroK) *reinterpret_cast<uint4*>(kbuf + at) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -557,7 +563,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
           }
         }
         g0 += it.T;
-        it = next;
+        if (kFp8) held = next;
       }
       // every load issued must land before the CTA may exit
       if (leader)
@@ -566,7 +572,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
           mbar_wait_bounded(kFp8 ? &bars->s8_full[st] : &bars->kv_full[st], (last / kStages) & 1);
         }
     } else if (!kFp8 && warp == Ro::kWarpExtra) {
-      // ---------------------------------------------------------- unseen V rows of 16-bit pools
+      // ---------------------------------------------------------- unseen rows of 16-bit pools
       // Keys behind the last one that may be seen, and ahead of every row's first key: zero V
       // once the tile has landed, so that P = 0 never meets what lies there.
       for (int q = 0; q < items && ok; ++q) {
@@ -577,13 +583,15 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
           ok = wait(&bars->kv_full[st], (g / kStages) & 1);
           if (!ok) break;
           if (needs_zeros(it, j)) {
-            uint8_t* vbuf = sm + stage_off(st) + 2 * kKVHalf;
+            uint8_t* kbuf = sm + stage_off(st);
+            uint8_t* vbuf = kbuf + 2 * kKVHalf;
             const int r0 = j == 0 ? it.head : 0, r1 = it.end - (it.jt0 + j) * kN;
             for (int i = lane; i < kN * 16; i += 32) {
               const int r = i / 16, c16 = i % 16;
-              if (r < r0 || r >= r1)
-                *reinterpret_cast<uint4*>(vbuf + ((r >> 3) * 2 + (c16 >> 3)) * 1024 +
-                                          sw128(r & 7, c16 & 7)) = make_uint4(0, 0, 0, 0);
+              if (r >= r0 && r < r1) continue;
+              const uint32_t at = ((r >> 3) * 2 + (c16 >> 3)) * 1024 + sw128(r & 7, c16 & 7);
+              *reinterpret_cast<uint4*>(vbuf + at) = make_uint4(0, 0, 0, 0);
+              if (kZeroK) *reinterpret_cast<uint4*>(kbuf + at) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -651,7 +659,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
                   }
                 }
                 // keys that no row sees: zero V, so that P = 0 never meets NaN
-                if (kv && zeros && (r >= valid || r < skip)) {
+                if ((kv || kZeroK) && zeros && (r >= valid || r < skip)) {
 #pragma unroll
                   for (int e = 0; e < 8; ++e) o[e] = 0u;
                 }
@@ -692,6 +700,11 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
           const int g = g0 + j, st = g % kStages;
           ok = wait(&bars->kv_full[st], (g / kStages) & 1);
           const bool mine = j < it.tiles_of(t);
+          // (issuers that go by zeroing follow every one, so that they count alike)
+          if (!kFp8 && (kZeroK || !scores) && ok && needs_zeros(it, j)) {
+            ok = wait(&bars->v_fixed[st], (fixes >> st) & 1);
+            fixes ^= 1u << st;
+          }
           if (scores) {
             // S overwrites the TMEM buffer of P two key tiles back: its P V must have read it
             if (ok && mine && c >= 2) ok = wait(&bars->p_free[t][c & 1], ((c - 2) >> 1) & 1);
@@ -708,11 +721,6 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
               tc_commit(&bars->s_full[t][c & 1]);
             }
           } else {
-            // (both query tiles' issuers follow every zeroing, so that they count alike)
-            if (!kFp8 && ok && needs_zeros(it, j)) {
-              ok = wait(&bars->v_fixed[st], (fixes >> st) & 1);
-              fixes ^= 1u << st;
-            }
             if (ok && mine) ok = wait(&bars->p_full[t][c & 1], (c >> 1) & 1);
             if (!ok) break;
             tc_fence_after();

@@ -93,7 +93,8 @@ __device__ __forceinline__ void odd_polynomial(float* x, float cap_out, const fl
 // cap_out tanh(x) of many scores: while no score of the warp is above 1 in magnitude
 // (scores within the cap) a polynomial serves them all, without the special-function unit
 // that the softmax's exponentials need.  The polynomials are fitted by weighted least
-// squares to the smallest largest relative error.
+// squares to the smallest largest relative error.  (A key that no query sees has no part in
+// the choice, or what lies in its slot would decide the bits of the others.)
 
 // In a chunk, whose softmax is bound by these instructions and rounds its weights to 2^-16
 // or less ahead of the values: within 2^-20.5, by the shortest polynomial (4 to 7
@@ -135,13 +136,13 @@ __device__ __forceinline__ void cap_scores(float* x, float cap_out) {
 }
 
 // In a decode, whose weights may be recorded in fp32: 2^-24 before rounding, 2^-22.5 with
-// it.  x[i] = cap_out tanh(x[i]).
+// it.  x[i] = cap_out tanh(x[i]).  `all_seen`: of the warp; other scores get no polynomial.
 template <int N>
-__device__ __forceinline__ void cap_scores_fine(float* x, float cap_out) {
+__device__ __forceinline__ void cap_scores_fine(float* x, float cap_out, bool all_seen) {
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < N; i += 2) top = fmax3(top, fabsf(x[i]), fabsf(x[i + 1]));
-  if (__all_sync(0xffffffffu, top <= 1.f)) {
+  if (all_seen && __all_sync(0xffffffffu, top <= 1.f)) {
     const float c[6] = {-0x1.55546cp-2f, 0x1.10ecc4p-3f,  -0x1.b642ecp-5f,
                         0x1.4d9306p-6f,  -0x1.9a364ap-8f, 0x1.156af0p-10f};
     odd_polynomial<N>(x, cap_out, c);

@@ -8,9 +8,9 @@ namespace pkv {
 cudaError_t launch_decode_mma_bf16(const CUtensorMap*, const DecodeArgs&, int, int, cudaStream_t);
 cudaError_t launch_decode_mma_f16(const CUtensorMap*, const DecodeArgs&, int, int, cudaStream_t);
 cudaError_t launch_decode_mma_fp8(const CUtensorMap*, const DecodeArgs&, int, int, cudaStream_t);
-cudaError_t launch_decode_score_bf16(const CUtensorMap*, const DecodeArgs&, int, cudaStream_t);
-cudaError_t launch_decode_score_f16(const CUtensorMap*, const DecodeArgs&, int, cudaStream_t);
-cudaError_t launch_decode_score_fp8(const CUtensorMap*, const DecodeArgs&, int, cudaStream_t);
+cudaError_t launch_decode_score_bf16(const CUtensorMap*, const ScoredArgs&, int, cudaStream_t);
+cudaError_t launch_decode_score_f16(const CUtensorMap*, const ScoredArgs&, int, cudaStream_t);
+cudaError_t launch_decode_score_fp8(const CUtensorMap*, const ScoredArgs&, int, cudaStream_t);
 
 using mma::kD;
 using mma::kLineBytes;
@@ -50,7 +50,7 @@ cudaError_t launch_decode_mma(const CUtensorMap* map, const DecodeArgs& a, int g
   }
 }
 
-cudaError_t launch_decode_mma_scored(const CUtensorMap* map, const DecodeArgs& a, int gx,
+cudaError_t launch_decode_mma_scored(const CUtensorMap* map, const ScoredArgs& a, int gx,
                                      cudaStream_t stream) {
   if (a.stages < 2 || a.stages > 16 || a.HG < 1 || a.HG > kMaxHG) return cudaErrorInvalidValue;
   if (a.R < 1 || a.R > 16) return cudaErrorInvalidValue;

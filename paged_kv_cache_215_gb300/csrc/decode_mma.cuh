@@ -36,6 +36,7 @@
 // to the scores and to the output.
 #pragma once
 #include <algorithm>
+#include <type_traits>
 
 #include "device.cuh"
 #include "launch.h"
@@ -52,6 +53,9 @@ namespace mma {
 enum Mode { kPlain = 0, kSuffix = 1, kScored = 2, kOne = 4, kOneCap = 5, kOneRecord = 6,
             kOneCapRecord = 7 };
 __host__ __device__ constexpr bool is_scored(int mode) { return mode >= kScored; }
+// What an instance's call hands it.
+template <int kMode>
+using Args = std::conditional_t<is_scored(kMode), ScoredArgs, DecodeArgs>;
 __host__ __device__ constexpr bool is_one(int mode) { return mode >= kOne; }
 __host__ __device__ constexpr bool one_cap(int mode) { return is_one(mode) && (mode & 1); }
 __host__ __device__ constexpr bool one_record(int mode) { return is_one(mode) && (mode & 2); }
@@ -95,7 +99,7 @@ struct Cursor {
 };
 
 template <int kMode>
-__device__ __forceinline__ int clamp_len(const DecodeArgs& a, int s) {
+__device__ __forceinline__ int clamp_len(const Args<kMode>& a, int s) {
   if constexpr (is_scored(kMode)) {
     const KeyRange r = read_range(a, s, scored_len(a, s));
     return r.hi - r.lo;
@@ -114,7 +118,7 @@ __device__ __forceinline__ int blocks_of(int n, int BS) { return (n + BS - 1) / 
 
 // Move to the next block; crosses into the next non-empty unit when needed.
 template <int kMode>
-__device__ __forceinline__ void cursor_next(Cursor& c, const DecodeArgs& a) {
+__device__ __forceinline__ void cursor_next(Cursor& c, const Args<kMode>& a) {
   ++c.j;
   ++c.gb;
   --c.remaining;
@@ -249,7 +253,7 @@ struct Consumer {
     return ((long long)s * a.q_len + i) * a.Hq + (long long)hkv * a.G + g;
   }
 
-  __device__ __forceinline__ void load_q(const DecodeArgs& a, int s, int n, int hkv, int lane) {
+  __device__ __forceinline__ void load_q(const Args<kMode>& a, int s, int n, int hkv, int lane) {
     if constexpr (kSingle) {
       load_q_decode(a, s, hkv, lane);
       if constexpr (kScore) load_rules_one(a, s, hkv);
@@ -311,7 +315,7 @@ struct Consumer {
   }
 
   // One query token: its first and last key of the tokens that the unit reads (read_range).
-  __device__ __forceinline__ void load_rules_one(const DecodeArgs& a, int s, int hkv) {
+  __device__ __forceinline__ void load_rules_one(const Args<kMode>& a, int s, int hkv) {
     const KeyRange k = key_range(a, s, scored_len(a, s), 0);
     const int off = k.lo / BS * BS;
     from_min = k.lo - off;
@@ -321,7 +325,7 @@ struct Consumer {
   }
 
   // The columns' rules.
-  __device__ __forceinline__ void load_rules(const DecodeArgs& a, int s, int hkv, int lane) {
+  __device__ __forceinline__ void load_rules(const Args<kMode>& a, int s, int hkv, int lane) {
     const int len = scored_len(a, s), off = read_range(a, s, len).lo;
     ColumnRule r{0x7fffffff, -1, 0, 0.f};           // a column that sees no key
     __syncwarp();                                   // the unit before has read its rules
@@ -347,7 +351,7 @@ struct Consumer {
   }
 
   // Scores of a block into log2 units: cap, distance, mask, record (score.cuh).
-  __device__ __forceinline__ void apply_rules(const DecodeArgs& a, float (&s)[kTiles][NT][4],
+  __device__ __forceinline__ void apply_rules(const Args<kMode>& a, float (&s)[kTiles][NT][4],
                                               float ks_b, int jbase, int valid, bool full,
                                               int lane) {
     const int c = lane & 3, t0 = jbase + (lane >> 2);
@@ -396,7 +400,7 @@ struct Consumer {
     return bits;
   }
 
-  __device__ __forceinline__ void record_one(const DecodeArgs& a, const float (&s)[kTiles][4],
+  __device__ __forceinline__ void record_one(const Args<kMode>& a, const float (&s)[kTiles][4],
                                              int jbase, int valid, int lane) {
     const int c = lane & 3;
     float* row = score_rows + (int64_t)(jbase + (lane >> 2)) * a.score_row + 2 * c;
@@ -415,7 +419,7 @@ struct Consumer {
   }
 
   // The block's scores of the tokens before `valid` into the record.
-  __device__ __forceinline__ void record(const DecodeArgs& a, const float (&s)[kTiles][NT][4],
+  __device__ __forceinline__ void record(const Args<kMode>& a, const float (&s)[kTiles][NT][4],
                                          int jbase, int valid, int lane) {
     const int c = lane & 3;
 #pragma unroll
@@ -438,7 +442,7 @@ struct Consumer {
 
   // The single-token path (one query token, G <= 8 heads as the 8 columns).
   // ks_b / vs_b: the block's own E4M3 scales (block-wise scaling), else 1.
-  __device__ __forceinline__ void block_decode(const DecodeArgs& a, uint32_t kbase, uint32_t vbase,
+  __device__ __forceinline__ void block_decode(const Args<kMode>& a, uint32_t kbase, uint32_t vbase,
                                         uint32_t region_bytes, int row0, int jbase, int valid,
                                         int lane, float ks_b, float vs_b) {
     // scored: keys [first, valid) of the block are seen
@@ -628,7 +632,7 @@ struct Consumer {
     }
   }
 
-  __device__ __forceinline__ void load_q_decode(const DecodeArgs& a, int s, int hkv, int lane) {
+  __device__ __forceinline__ void load_q_decode(const Args<kMode>& a, int s, int hkv, int lane) {
     const int g = lane >> 2, c = lane & 3;
     const bool live = g < a.G;
     const size_t row = ((size_t)s * a.Hq + (size_t)hkv * a.G + (live ? g : 0)) * kD;
@@ -714,7 +718,7 @@ struct Consumer {
   // the first region of K / V in the stage; `row0` is the warp's first row;
   // `jbase` the block's first token position; `valid` its tokens inside the
   // sequence; `full`: no key of the block is hidden from any query row.
-  __device__ __forceinline__ void block(const DecodeArgs& a, uint32_t kbase, uint32_t vbase,
+  __device__ __forceinline__ void block(const Args<kMode>& a, uint32_t kbase, uint32_t vbase,
                                         uint32_t region_bytes, int row0, int jbase, int valid,
                                         bool full, int lane, float ks_b, float vs_b) {
     if constexpr (kSingle) {
@@ -1000,7 +1004,7 @@ struct Consumer {
 
   // Write the piece's result: directly to out (whole = true) or as a partial
   // (balanced: rows part_base + column; fixed: part_base + q_row * S).
-  __device__ __forceinline__ void finish(const DecodeArgs& a, int s, int hkv, int lane, bool whole,
+  __device__ __forceinline__ void finish(const Args<kMode>& a, int s, int hkv, int lane, bool whole,
                                          size_t part_base, bool balanced) {
     if constexpr (kScore) {
       finish_scored(a, s, hkv, lane, whole, part_base);
@@ -1061,7 +1065,7 @@ __device__ __forceinline__ size_t part_base(const DecodeArgs& a, int w, long lon
 // The CTA's run of the balanced stream of at most 32 sequences, a lane each (one warp;
 // the general form is in the kernel).
 template <int kMode, int BS>
-__device__ __forceinline__ void find_run_of_few(const DecodeArgs& a, SmemHeader* hdr, int lane) {
+__device__ __forceinline__ void find_run_of_few(const Args<kMode>& a, SmemHeader* hdr, int lane) {
   const int nb = lane < a.B ? blocks_of(clamp_len<kMode>(a, lane), BS) : 0;
   if (blockIdx.x == 0 && lane < a.B && nb == 0)
     for (int hg = 0; hg < a.NHG; ++hg) a.unit_info[(size_t)lane * a.NHG + hg] = make_int2(0, 0);
@@ -1092,7 +1096,7 @@ __device__ __forceinline__ void find_run_of_few(const DecodeArgs& a, SmemHeader*
 
 template <int KVT, int BS, int NT, bool kCausal, int kMode>
 __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
-    decode_mma_kernel(const __grid_constant__ CUtensorMap tmap, const DecodeArgs a) {
+    decode_mma_kernel(const __grid_constant__ CUtensorMap tmap, const Args<kMode> a) {
   using T = KvTraits<KVT>;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte alignment for the 128-byte swizzle pattern
@@ -1380,7 +1384,8 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
   // a shared-prefix decode merges every row with its prefix partials, and a call
   // that returns each row's log-sum-exp, or records weights by it, has the merge write
   // every row
-  const bool whole_ok = a.ext_lse == nullptr && a.out_lse == nullptr && a.scores == nullptr;
+  bool whole_ok = a.ext_lse == nullptr && a.out_lse == nullptr;
+  if constexpr (kScore) whole_ok = whole_ok && a.scores == nullptr;
   int stage = 0;
   uint32_t round = 0;
   while (cur.remaining > 0) {
@@ -1453,7 +1458,7 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
 }
 
 template <int KVT, int BS, int NT, bool kCausal, int kMode = kPlain>
-cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, int gx, int gy,
+cudaError_t launch_t(const CUtensorMap* map, const Args<kMode>& a, int gx, int gy,
                      cudaStream_t stream) {
   // the ring needs mma_smem_bytes; a larger request (a.smem_bytes) caps how many
   // CTAs can share an SM

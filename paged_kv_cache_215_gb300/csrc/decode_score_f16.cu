@@ -9,7 +9,7 @@
 namespace pkv {
 
 template <int kMode>
-static cudaError_t launch_mode(const CUtensorMap* map, const DecodeArgs& a, int gx,
+static cudaError_t launch_mode(const CUtensorMap* map, const ScoredArgs& a, int gx,
                                cudaStream_t stream) {
   using mma::launch_t;
   switch (a.BS) {
@@ -20,7 +20,7 @@ static cudaError_t launch_mode(const CUtensorMap* map, const DecodeArgs& a, int 
   }
 }
 
-cudaError_t launch_decode_score_f16(const CUtensorMap* map, const DecodeArgs& a, int gx,
+cudaError_t launch_decode_score_f16(const CUtensorMap* map, const ScoredArgs& a, int gx,
                                     cudaStream_t stream) {
   if (a.q_len > 1 || a.R > 8 || a.slopes) return launch_mode<mma::kScored>(map, a, gx, stream);
   if (a.cap_in != 0.f)

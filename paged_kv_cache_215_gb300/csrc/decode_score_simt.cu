@@ -38,7 +38,7 @@ __device__ __forceinline__ void load_row8(const void* pool, int64_t at, float (&
 
 // MG: query heads a KV head at most.
 template <int KVT, int MG>
-__global__ void __launch_bounds__(32 * kWarps) lanes_kernel(const DecodeArgs a, int lanes) {
+__global__ void __launch_bounds__(32 * kWarps) lanes_kernel(const ScoredArgs a, int lanes) {
   constexpr int kFlight = MG <= 8 ? 2 : 1;          // tokens a group has in flight
   extern __shared__ float sm[];
   grid_dependency_wait();
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(32 * kWarps) lanes_kernel(const DecodeArgs a, 
 }
 
 template <int KVT>
-cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
+cudaError_t launch_t(const ScoredArgs& a, cudaStream_t stream) {
   int lanes = 1;
   while (8 * lanes < a.D) lanes *= 2;
   const int all = kWarps * (32 / lanes);
@@ -204,7 +204,7 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t stream) {
 
 bool simt_scored_supported(int D, int G) { return D % 8 == 0 && D <= 256 && G <= 16; }
 
-cudaError_t launch_decode_simt_scored(const DecodeArgs& a, cudaStream_t stream) {
+cudaError_t launch_decode_simt_scored(const ScoredArgs& a, cudaStream_t stream) {
   if (!simt_scored_supported(a.D, a.G)) return cudaErrorInvalidValue;
   cudaError_t e;
   switch (a.kv_dtype) {

@@ -65,9 +65,13 @@ struct DecodeArgs {
   // row (split * q_len + i) * Hq + head.
   const int32_t* key_limit;
   float* out_lse;
-  // Scored attention (score.cuh).  Lengths are limited to max_len.  With a cap, scores
-  // are cap_out * tanh(cap_in * <q, k>) (log2 units; cap_in carries the softmax scale
-  // and k_scale), without one (cap_in = 0) qk_scale_log2 * <q, k>.
+};
+
+// A scored call's (score.cuh), apart: in the plain kernels' arguments they cost a plain
+// decode 0.3%.  Lengths are limited to max_len.  With a cap, scores are
+// cap_out * tanh(cap_in * <q, k>) (log2 units; cap_in carries the softmax scale and
+// k_scale), without one (cap_in = 0) qk_scale_log2 * <q, k>.
+struct ScoredArgs : DecodeArgs {
   int max_len;
   float cap_in, cap_out;
   int window;                // 0: none
@@ -88,15 +92,15 @@ cudaError_t launch_decode_mma(const CUtensorMap* map, const DecodeArgs& a, int g
                               cudaStream_t stream);
 cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t stream);
 // The scored instances of both.
-cudaError_t launch_decode_mma_scored(const CUtensorMap* map, const DecodeArgs& a, int grid_x,
+cudaError_t launch_decode_mma_scored(const CUtensorMap* map, const ScoredArgs& a, int grid_x,
                                      cudaStream_t stream);
 bool simt_scored_supported(int D, int G);
-cudaError_t launch_decode_simt_scored(const DecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_decode_simt_scored(const ScoredArgs& a, cudaStream_t stream);
 // Chunked prefill on tcgen05 (one CTA per 128-row query tile, KV head, sequence).
 bool prefill_tc_supported(int kv_dtype, int q_dtype, int BS, int D, int G);
 cudaError_t launch_prefill_tc(const CUtensorMap* map, const DecodeArgs& a, cudaStream_t stream);
 // The same under the rules of a scored call.
-cudaError_t launch_prefill_scored(const CUtensorMap* map, const DecodeArgs& a, int sms,
+cudaError_t launch_prefill_scored(const CUtensorMap* map, const ScoredArgs& a, int sms,
                                   cudaStream_t stream);
 // Merge of the balanced-mode partials, one CTA per (unit, head in the unit).
 cudaError_t launch_merge_units(const DecodeArgs& a, bool pdl, cudaStream_t stream);
@@ -127,7 +131,7 @@ inline int score_row(int R) {
 }
 // Merge of a scored call's partials (balanced or fixed) and, beside it (out not nullptr),
 // *out = *in (nullptr data: 0) + the softmax weights of the scores in a.scores.
-cudaError_t launch_merge_scored(const DecodeArgs& a, const WeightRows* in, const WeightRows* out,
+cudaError_t launch_merge_scored(const ScoredArgs& a, const WeightRows* in, const WeightRows* out,
                                 cudaStream_t stream);
 
 struct AppendArgs {

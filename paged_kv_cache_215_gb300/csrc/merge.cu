@@ -247,7 +247,7 @@ struct RowPartials {
   size_t q_row;
   bool ok;
 };
-__device__ __forceinline__ RowPartials row_partials(const DecodeArgs& a, int s, int h, int r) {
+__device__ __forceinline__ RowPartials row_partials(const ScoredArgs& a, int s, int h, int r) {
   RowPartials p;
   const int i = r / a.G, g = r % a.G;
   p.q_row = ((size_t)s * a.q_len + i) * a.Hq + (size_t)h * a.G + g;
@@ -273,7 +273,7 @@ __device__ __forceinline__ RowPartials row_partials(const DecodeArgs& a, int s, 
 // scores already in flight, so that it runs beside the merge instead of behind it.
 // ROW floats of scores a token, TOKENS a thread.
 template <int ROW>
-__device__ __forceinline__ void accumulate_tokens(const DecodeArgs& a, const WeightRows& in,
+__device__ __forceinline__ void accumulate_tokens(const ScoredArgs& a, const WeightRows& in,
                                                   const WeightRows& out, int s, int h, int j0) {
   constexpr int TOKENS = ROW <= 4 ? 4 : ROW == 8 ? 2 : 1;
   __shared__ float lse[16];
@@ -351,7 +351,7 @@ __host__ __device__ constexpr int tokens_per_cta(int row) {
 // largest of those is known, so that a row of few partials takes two trips to memory (its
 // place, its partials).
 template <int kGroup>
-__device__ __forceinline__ void merge_row128(const DecodeArgs& a, const RowPartials& p, int w,
+__device__ __forceinline__ void merge_row128(const ScoredArgs& a, const RowPartials& p, int w,
                                              int lane) {
   constexpr int kFirst = kGroup == 1 ? 8 : 4;
   __shared__ float tops[kGroup];
@@ -440,7 +440,7 @@ __device__ __forceinline__ void merge_row128(const DecodeArgs& a, const RowParti
 // (35 MB, most of it in L2) 17 us.
 template <bool kWarpRows, bool kRecord>
 __global__ void __launch_bounds__(kThreads, 2)
-    merge_scored_kernel(const DecodeArgs a, const WeightRows in, const WeightRows out) {
+    merge_scored_kernel(const ScoredArgs a, const WeightRows in, const WeightRows out) {
   grid_launch_dependents();
   const int row_ctas = kWarpRows ? 1 : a.R, h = blockIdx.y, s = blockIdx.z;
   if constexpr (kRecord) {
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 }  // namespace
 
-cudaError_t launch_merge_scored(const DecodeArgs& a, const WeightRows* in, const WeightRows* out,
+cudaError_t launch_merge_scored(const ScoredArgs& a, const WeightRows* in, const WeightRows* out,
                                 cudaStream_t stream) {
   if (a.D > kMaxD || a.R > kWarps || a.score_row > 16 || a.B > 65535 || a.Hkv > 65535)
     return cudaErrorInvalidValue;

@@ -1476,7 +1476,7 @@ int paged_decode_attention_scored(void* d_out, pkv_dtype out_dtype, const void* 
   if (!device_info(&dev)) return PKV_ECUDA;
   const int G = g.num_q_heads / g.num_kv_heads;
 
-  DecodeArgs a{};
+  ScoredArgs a{};
   a.q = d_q;
   a.out = d_out;
   a.pool = p->d_pool;

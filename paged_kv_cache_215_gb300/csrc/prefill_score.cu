@@ -114,7 +114,7 @@ struct Bars {
 constexpr uint32_t kSmemBytes = kSmemKV + kStages * kStageBytes;
 static_assert(kSmemBytes + sizeof(Bars) + kAlignSlack <= 227u * 1024u, "smem");
 
-__device__ __forceinline__ long long item_count(const DecodeArgs& a, int pairs) {
+__device__ __forceinline__ long long item_count(const ScoredArgs& a, int pairs) {
   return (long long)a.Hkv * a.B * pairs;
 }
 // The CTA's k-th item's index: rounds of gridDim.x items, dealt out to and fro.
@@ -130,7 +130,7 @@ __device__ __forceinline__ int items_of_cta(long long items) {
 }
 
 // Item `index`; whole warps (each finds the same).  `empty`: some row sees no key.
-__device__ __forceinline__ Item item_of(const DecodeArgs& a, long long index, int pairs, int lane,
+__device__ __forceinline__ Item item_of(const ScoredArgs& a, long long index, int pairs, int lane,
                                         bool* empty) {
   Item it;
   bool none = false;
@@ -183,7 +183,7 @@ __device__ __forceinline__ Item item_of(const DecodeArgs& a, long long index, in
 // that sees its own position sees all from its first key to there, so only positions of the
 // item's own rows can be gaps: those that neither a row from there on nor a row inside the
 // prefix (which sees the prefix to its end) reaches.
-__device__ __forceinline__ void find_gaps(const DecodeArgs& a, Item& it, uint32_t* gaps, int lane) {
+__device__ __forceinline__ void find_gaps(const ScoredArgs& a, Item& it, uint32_t* gaps, int lane) {
   constexpr int kFar = 0x7fffffff;
   const int toks = kQT * kM / a.G, tok0 = it.pair * toks, pos0 = it.n - a.q_len + tok0;
   const int prefix = a.prefix_lens ? min(a.prefix_lens[it.s], it.n) : 0;
@@ -223,7 +223,7 @@ __device__ __forceinline__ void find_gaps(const DecodeArgs& a, Item& it, uint32_
     it.gap1 = hi / kN - it.jt0 + 1;
   }
 }
-__device__ __forceinline__ bool in_gap(const DecodeArgs& a, const Item& it, const uint32_t* gaps,
+__device__ __forceinline__ bool in_gap(const ScoredArgs& a, const Item& it, const uint32_t* gaps,
                                        int pos) {
   const int toks = kQT * kM / a.G, i = pos - (it.n - a.q_len + it.pair * toks);
   return i >= 0 && i < toks && (gaps[i / 32] >> (i % 32) & 1u);
@@ -231,7 +231,7 @@ __device__ __forceinline__ bool in_gap(const DecodeArgs& a, const Item& it, cons
 
 // The block that is read in the place of block b of local tile j: b itself where some row may
 // see a key of it, else one with a seen key.
-__device__ __forceinline__ int block_read(const DecodeArgs& a, const Item& it, const uint32_t* gaps,
+__device__ __forceinline__ int block_read(const ScoredArgs& a, const Item& it, const uint32_t* gaps,
                                           int j, int b) {
   b = min(max(b, it.blk0), (it.end - 1) / a.BS);
   if (j >= it.gap0 && j < it.gap1) {
@@ -244,7 +244,7 @@ __device__ __forceinline__ int block_read(const DecodeArgs& a, const Item& it, c
 
 // E4M3 block scales: the largest power-of-two exponent among the V scales of an item's
 // blocks (0 if there is none); whole warps.
-__device__ __forceinline__ int v_exponent(const DecodeArgs& a, const Item& it, const uint32_t* gaps,
+__device__ __forceinline__ int v_exponent(const ScoredArgs& a, const Item& it, const uint32_t* gaps,
                                           int lane) {
   const int bpt = kN / a.BS, nblk = (it.end + a.BS - 1) / a.BS;
   const int32_t* trow = a.tables + (size_t)it.s * a.max_blocks;
@@ -261,7 +261,7 @@ __device__ __forceinline__ int v_exponent(const DecodeArgs& a, const Item& it, c
 }
 
 // Q rows of an item towards L2, by a warp: two 128-byte lines a row.
-__device__ __forceinline__ void prefetch_q(const DecodeArgs& a, const Item& it, int lane) {
+__device__ __forceinline__ void prefetch_q(const ScoredArgs& a, const Item& it, int lane) {
   const int QT = kM / a.G, tok0 = it.pair * kQT * QT, toks = min(kQT * QT, a.q_len - tok0);
   const char* q = static_cast<const char*>(a.q) +
                   (((size_t)it.s * a.q_len + tok0) * a.Hq + (size_t)it.hkv * a.G) * kD * 2;
@@ -278,7 +278,7 @@ __device__ __forceinline__ void prefetch_q(const DecodeArgs& a, const Item& it, 
 // exactly; returns e of the thread's own row (of two halves: of row lane % 16 of the
 // warp's).  A negative softmax scale is moved onto Q (an exact sign flip).
 template <bool kFp8, int kHalves>
-__device__ __forceinline__ int stage_q(const DecodeArgs& a, const Item& it, int t, uint8_t* sm,
+__device__ __forceinline__ int stage_q(const ScoredArgs& a, const Item& it, int t, uint8_t* sm,
                                        int warp, int half, int lane) {
   const int gs = 31 - __clz(a.G), c = lane & 15;       // (G is a power of two)
   const int tok0 = (it.pair * kQT + t) * (kM >> gs);
@@ -384,7 +384,7 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wi
 
 template <int KVT, int kRules>
 __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
-    prefill_score_kernel(const __grid_constant__ CUtensorMap tmap, const DecodeArgs a, int pairs) {
+    prefill_score_kernel(const __grid_constant__ CUtensorMap tmap, const ScoredArgs a, int pairs) {
   using C = PfCfg<KVT>;
   constexpr bool kBf16 = C::kBf16, kFp8 = C::kFp8;
   using Ro = Roles<KVT, kRules>;
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
           }
           __syncwarp();
         }
-        // (registers are short: read in place; E4M3 a copy, in place its window call takes 568 us for 553)
+        // (in place, registers are short; on E4M3 pools a copy: a window call 568 -> 553 us)
         const Item& it = kFp8 ? held : q < 0 ? bars->none : bars->plan[q % kPlans];
         const int nblk = (it.end + a.BS - 1) / a.BS;
         const int32_t* trow = a.tables + (size_t)it.s * a.max_blocks;
@@ -1063,7 +1063,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
 }
 
 template <int KVT, int kRules>
-cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, int sms, cudaStream_t stream) {
+cudaError_t launch_t(const CUtensorMap* map, const ScoredArgs& a, int sms, cudaStream_t stream) {
   using Ro = Roles<KVT, kRules>;
   const size_t smem = kSmemBytes + sizeof(Bars) + kAlignSlack;
   auto kernel = prefill_score_kernel<KVT, kRules>;
@@ -1084,7 +1084,7 @@ cudaError_t launch_t(const CUtensorMap* map, const DecodeArgs& a, int sms, cudaS
 }
 
 template <int KVT>
-cudaError_t launch_rules(const CUtensorMap* map, const DecodeArgs& a, int sms,
+cudaError_t launch_rules(const CUtensorMap* map, const ScoredArgs& a, int sms,
                          cudaStream_t stream) {
   return a.slopes           ? launch_t<KVT, kDistance>(map, a, sms, stream)
          : a.cap_in != 0.f ? launch_t<KVT, kCap>(map, a, sms, stream)
@@ -1093,7 +1093,7 @@ cudaError_t launch_rules(const CUtensorMap* map, const DecodeArgs& a, int sms,
 
 }  // namespace
 
-cudaError_t launch_prefill_scored(const CUtensorMap* map, const DecodeArgs& a, int sms,
+cudaError_t launch_prefill_scored(const CUtensorMap* map, const ScoredArgs& a, int sms,
                                   cudaStream_t stream) {
   cudaError_t e;
   switch (a.kv_dtype) {

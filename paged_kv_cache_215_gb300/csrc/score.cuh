@@ -16,7 +16,7 @@
 namespace pkv {
 
 // The sequence's length as the scored calls take it: limited to [0, a.max_len].
-__device__ __forceinline__ int scored_len(const DecodeArgs& a, int s) {
+__device__ __forceinline__ int scored_len(const ScoredArgs& a, int s) {
   int n = a.seq_lens[s];
   if (n < 0 || n > a.max_len) {
     record_error(a.status, PKV_EBOUNDS);
@@ -29,7 +29,7 @@ struct KeyRange {
   int lo, hi;                // keys [lo, hi); hi <= lo: none
 };
 
-__device__ __forceinline__ KeyRange key_range(const DecodeArgs& a, int s, int n, int i) {
+__device__ __forceinline__ KeyRange key_range(const ScoredArgs& a, int s, int n, int i) {
   const int p = n - a.q_len + i;
   if (p < 0) return {0, 0};
   int lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
@@ -41,7 +41,7 @@ __device__ __forceinline__ KeyRange key_range(const DecodeArgs& a, int s, int n,
 
 // The tokens [lo, hi) the scored decode reads of a sequence: from the block of the first key
 // that any query token sees up to the last one that any sees; hi <= lo if none sees a key.
-__device__ __forceinline__ KeyRange read_range(const DecodeArgs& a, int s, int n) {
+__device__ __forceinline__ KeyRange read_range(const ScoredArgs& a, int s, int n) {
   KeyRange all{n, n};
   if (!a.doc_starts) {                         // every query sees its own key
     if (n > 0) all.lo = a.window > 0 ? max(0, max(n - a.q_len, 0) - a.window + 1) : 0;

@@ -142,11 +142,10 @@ __device__ __forceinline__ long long owner_of(long long b, long long T, long lon
   return ((b + 1) * P - 1) / T;
 }
 
-// a * b / c, in 32 bits where that is enough (a 64-bit division takes some 100
+// n / c of counts, in 32 bits where that is enough (a 64-bit division takes some 100
 // instructions, and a short call's prologue is a chain of them).
-__device__ __forceinline__ long long muldiv(long long a, long long b, long long c) {
-  const unsigned long long n = (unsigned long long)a * b;
-  if ((n | (unsigned long long)c) >> 32) return (long long)(n / c);
+__device__ __forceinline__ long long divide(unsigned long long n, unsigned long long c) {
+  if ((n | c) >> 32) return (long long)(n / c);
   return (unsigned)n / (unsigned)c;
 }
 
@@ -1079,8 +1078,8 @@ __device__ __forceinline__ void find_run_of_few(const Args<kMode>& a, SmemHeader
   const long long total = __shfl_sync(0xffffffffu, upto, 31);
   const long long P = min(total, (long long)gridDim.x);
   const bool takes_part = blockIdx.x < P;
-  const long long gb0 = takes_part ? muldiv(blockIdx.x, total, P) : 0;
-  const long long gb1 = takes_part ? muldiv(blockIdx.x + 1, total, P) : 0;
+  const long long gb0 = takes_part ? divide(blockIdx.x * total, P) : 0;
+  const long long gb1 = takes_part ? divide((blockIdx.x + 1) * total, P) : 0;
   if (lane == 0) {
     hdr->total = total;
     hdr->gb0 = gb0;
@@ -1433,11 +1432,8 @@ __global__ void __launch_bounds__(32 * (kMaxHG + 1), 1)
           const long long unit_first_gb = cur.gb - cur.j;
           const long long parts = hdr->total < (long long)gridDim.x ? hdr->total : (long long)gridDim.x;
           const long long last = unit_first_gb + cur.nb - 1;
-          const long long c_last = is_scored(kMode)
-                                       ? ((last + 1) * parts >> 32 ? owner_of(last, hdr->total, parts)
-                                                                   : (unsigned)((last + 1) * parts - 1) /
-                                                                         (unsigned)hdr->total)
-                                       : owner_of(last, hdr->total, parts);
+          const long long c_last = is_scored(kMode) ? divide((last + 1) * parts - 1, hdr->total)
+                                                    : owner_of(last, hdr->total, parts);
           a.unit_info[u] = make_int2((int)slot, (int)(c_last - blockIdx.x + 1));
         }
       } else {

@@ -58,8 +58,10 @@ __device__ __forceinline__ KeyRange read_range(const ScoredArgs& a, int s, int n
   return {all.lo / a.BS * a.BS, all.hi};
 }
 
-// tanh within 2^-22 of itself: below 0.6 an odd polynomial (fitted by weighted least
-// squares to the smallest largest relative error, 2^-28), above it 1 - 2 / (e^2x + 1).
+// tanh: below 0.6 an odd polynomial (fitted by weighted least squares to the smallest largest
+// relative error, 2^-27.6), above it 1 - 2 / (e^2x + 1), whose difference cancels the more the
+// smaller x is.  Over every fp32 within 2^-23.7 and 2^-22.2 of itself on either side of the
+// break, times cap_out within 2^-22.9 and 2^-22.
 __device__ __forceinline__ float tanh_score(float x) {
   const float z = x * x;
   const float e = ex2_ftz(x * (2.f * kLog2e));
@@ -97,8 +99,9 @@ __device__ __forceinline__ void odd_polynomial(float* x, float cap_out, const fl
 // the choice, or what lies in its slot would decide the bits of the others.)
 
 // In a chunk, whose softmax is bound by these instructions and rounds its weights to 2^-16
-// or less ahead of the values: within 2^-20.5, by the shortest polynomial (4 to 7
-// instructions for two scores) that the warp's largest score `top` allows.
+// or less ahead of the values: within 2^-20.5, 2^-20.2 with the rounding of its steps, by the
+// shortest polynomial (4 to 7 instructions for two scores) that the warp's largest score
+// `top` allows.
 __device__ __forceinline__ int cap_tier(float top) {
   // (magnitudes are in the order of their bits, NaN above all)
   const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
@@ -126,7 +129,8 @@ __device__ __forceinline__ void cap_scores(float* x, float cap_out) {
                         -0x1.99ce86p-9f};
     odd_polynomial<N>(x, cap_out, c);
   } else {
-    // 1 - 2 / (e^2x + 1), within 2^-22 of 1
+    // 1 - 2 / (e^2x + 1): scores are off by cap_out 2^-23.4 at most, the small ones too (a
+    // cap of 50: the weights by 2^-17.7 of themselves)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float e = ex2_ftz(x[i] * (2.f * kLog2e));
@@ -135,8 +139,8 @@ __device__ __forceinline__ void cap_scores(float* x, float cap_out) {
   }
 }
 
-// In a decode, whose weights may be recorded in fp32: 2^-24 before rounding, 2^-22.5 with
-// it.  x[i] = cap_out tanh(x[i]).  `all_seen`: of the warp; other scores get no polynomial.
+// In a decode, whose weights may be recorded in fp32: within 2^-23.5, 2^-22.3 with rounding.
+// x[i] = cap_out tanh(x[i]).  `all_seen`: of the warp; other scores get no polynomial.
 template <int N>
 __device__ __forceinline__ void cap_scores_fine(float* x, float cap_out, bool all_seen) {
   float top = 0.f;

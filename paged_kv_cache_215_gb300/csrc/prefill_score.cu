@@ -18,13 +18,13 @@
 // (Q, the last P V), and a bit a ring stage for tiles whose V rows were zeroed.  A role that
 // waits for a ring stage follows every tile of it.
 //
-// Measured, a call (with a CTA for each item): 2 x 2048 bf16 tokens over 8192 in documents,
-// capped, 141 us (181); 4 x 2048 tokens over 16384 E4M3 ones in a window of 4096, 559 us
-// (569); 3 prompts of 1001 f16 tokens, 64 heads on 8, that see a prefix, 80 us (110).  Of the
-// cycles between two items' key tiles some 4000 are the wait for Q, 3500 the output's stores.
-// A key tile takes 1700 cycles (f16) and 2100 (E4M3: the converters share the issue slots);
-// its matrix products alone would take 1100 (1650 with P's low half on bf16 pools), and the
-// softmax warps are behind them.
+// Measured, a call: 2 x 2048 bf16 tokens over 8192 in documents, capped, 148 us; 4 x 2048
+// tokens over 16384 E4M3 ones in a window of 4096, 553 us; 3 prompts of 1001 f16 tokens, 64
+// heads on 8, that see a prefix, 82 us (a CTA for each item took 181, 569 and 110 us where
+// these took 172, 560 and 81).  Of the cycles between two items' key tiles some 4000 are the
+// wait for Q, 3500 the output's stores.  A key tile takes 1700 cycles (f16) and 2100 (E4M3: the
+// converters share the issue slots); its matrix products alone would take 1100 (1650 with P's
+// low half on bf16 pools), and the softmax warps are behind them.
 #include <algorithm>
 
 #include "prefill_tc.cuh"
@@ -51,9 +51,9 @@ constexpr float kTiny = 0x1p-126f;           // in the place of a scale of 0: -i
 // A softmax thread has a row of 64 scores, or with a cap, whose instructions then bound the
 // call, half of one: the other half's thread is in a warp of the same quarter of tensor
 // memory's lanes, and the two warps vote on every tile whether a score passes the row's
-// reference.  One and two threads a row, us: capped documents bf16 159 and 141, f16 143 and
-// 140, E4M3 199 and 166; without a cap windows bf16 602 and 611, E4M3 558 and 614, an f16
-// prompt 81 and 84, distances bf16 180 and 203.  The softmax warps take registers that the
+// reference.  One and two threads a row, us: capped documents bf16 169 and 148, f16 153 and
+// 148, E4M3 208 and 178; without a cap windows bf16 625 and 646, E4M3 553 and 625, an f16
+// prompt 82 and 88, distances bf16 169 and 180.  The softmax warps take registers that the
 // others do not need (setmaxnreg, by warpgroups).
 template <int KVT, int kRules>
 struct Roles {
@@ -390,16 +390,20 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
   using Ro = Roles<KVT, kRules>;
   constexpr int kHalves = Ro::kHalves, kCols = Ro::kCols, kSoftmaxWarps = Ro::kSoftmaxWarps;
   constexpr int kWarpS = Ro::kWarpS, kWarpPV = Ro::kWarpPV, kWarpTMA = Ro::kWarpTMA;
-  constexpr bool kSplitP = kBf16;            // f16 P (11 bits) needs no low term
+  // P is one f16 term (11 bits) on f16 and E4M3 pools, as in the plain chunk: a low term would
+  // cost another P V product for the difference between a root mean square error of 2.3e-4
+  // (f16 prompt) and the 2.0e-4 of the output's own rounding
+  constexpr bool kSplitP = kBf16;
   // where a cap's polynomial goes by the scores, keys that no row sees are zeroed with V's rows
-  constexpr bool kZeroK = kRules >= kCap;
+  const bool zero_k = kRules == kCap || (kRules == kDistance && a.cap_in != 0.f);
   // P = 2^(s - ref + kPOff), ref at most kSlack below the row's largest score so far: in
   // two bf16 terms 2^8 at most, as in the plain chunk (values above 2^120 / keys overflow),
   // and 2^-24 or more for the largest, so that O is hardly ever rescaled (capped documents
   // with a slack of 8, 16, 24, 32, 60: 165, 159, 150, 146, 145 us; keys of four times the
-  // usual size have a warp do it every fourth tile at 8); in f16 2^15 at most, and weights
-  // down to 2^-21 of the largest keep every bit (a slack of 12 with 2^-17 saved 1% and added
-  // a quarter to an f16 output's error).
+  // usual size have a warp do it every fourth tile at 8; with distances, whose scores climb
+  // from tile to tile, documents take 169 us, with a slack of 60 164); in f16 2^15 at most,
+  // and weights down to 2^-21 of the largest keep every bit (a slack of 12 with 2^-17 saved
+  // 1% and added a quarter to an f16 output's error).
   constexpr float kSlack = kSplitP ? 32.f : 8.f, kPOff = kSplitP ? 8.f - kSlack : 7.f;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -555,7 +559,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
               const uint32_t at = kFp8 ? sw128(r, c16)
                                        : ((r >> 3) * 2 + (c16 >> 3)) * 1024 + sw128(r & 7, c16 & 7);
               *reinterpret_cast<uint4*>(vbuf + at) = make_uint4(0, 0, 0, 0);
-              if (kZeroK) *reinterpret_cast<uint4*>(kbuf + at) = make_uint4(0, 0, 0, 0);
+              if (zero_k) *reinterpret_cast<uint4*>(kbuf + at) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -591,7 +595,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
               if (r >= r0 && r < r1) continue;
               const uint32_t at = ((r >> 3) * 2 + (c16 >> 3)) * 1024 + sw128(r & 7, c16 & 7);
               *reinterpret_cast<uint4*>(vbuf + at) = make_uint4(0, 0, 0, 0);
-              if (kZeroK) *reinterpret_cast<uint4*>(kbuf + at) = make_uint4(0, 0, 0, 0);
+              if (zero_k) *reinterpret_cast<uint4*>(kbuf + at) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -659,7 +663,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
                   }
                 }
                 // keys that no row sees: zero V, so that P = 0 never meets NaN
-                if ((kv || kZeroK) && zeros && (r >= valid || r < skip)) {
+                if ((kv || zero_k) && zeros && (r >= valid || r < skip)) {
 #pragma unroll
                   for (int e = 0; e < 8; ++e) o[e] = 0u;
                 }
@@ -701,7 +705,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
           ok = wait(&bars->kv_full[st], (g / kStages) & 1);
           const bool mine = j < it.tiles_of(t);
           // (issuers that go by zeroing follow every one, so that they count alike)
-          if (!kFp8 && (kZeroK || !scores) && ok && needs_zeros(it, j)) {
+          if (!kFp8 && (zero_k || !scores) && ok && needs_zeros(it, j)) {
             ok = wait(&bars->v_fixed[st], (fixes >> st) & 1);
             fixes ^= 1u << st;
           }

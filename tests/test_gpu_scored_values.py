@@ -3,7 +3,7 @@ that climb tile after tile."""
 import pytest
 import torch
 
-from tests.scored_reference import Case
+from tests.scored_reference import Case, slopes
 from tests.test_gpu_scored import run
 
 pytestmark = pytest.mark.gpu
@@ -21,11 +21,11 @@ def climbing(case, step):
 
 @pytest.mark.parametrize("power", [-70, 90, 105])
 @pytest.mark.parametrize("step", [0.0, 3.0, 9.0, 20.0])
-@pytest.mark.parametrize("cap", [0.0, 200.0])
-def test_values_of_every_size(cap, step, power):
+@pytest.mark.parametrize("rules", ["none", "cap", "slopes"])
+def test_values_of_every_size(rules, step, power):
     case = Case([640, 200, 70], 8, 2, 128, "bf16", 16, 40, seed=41, q_gain=1.0)
     if step:
         climbing(case, step)
     case.pool[:, 1] = (case.pool[:, 1].float() * 2.0 ** power).to(torch.bfloat16)
-    r = dict(cap=cap) if cap else {}
+    r = {"none": {}, "cap": dict(cap=200.0), "slopes": dict(slopes=slopes(8))}[rules]
     case.check(run(case, torch.float32, **r), case.reference(**r))

@@ -3,8 +3,9 @@
 // query rows per KV head, a consumer warp for every 8 of them; and for one query token
 // without slopes the plain decode's loop, with or without a cap and a record.
 //
-// 128K tokens of 8 heads, capped: 57 us (0.70 of the copy rate; the instructions that
-// convert, cap and weigh a byte's score take as long as its load).
+// 128K tokens of 8 heads, capped: 57 us (0.69 of the copy rate; ten warps an SM issue in 48%
+// of the cycles and read at 60% of DRAM's nominal rate: neither is full, the chain of a
+// block's products, conversion, cap and weights is).  16 x 4 drafts in windows of 2048: 41 us.
 #include "decode_mma.cuh"
 
 namespace pkv {

@@ -436,7 +436,7 @@ __device__ __forceinline__ void merge_row128(const ScoredArgs& a, const RowParti
 // kWarpRows a warp each), the others (with a record) take its tokens.
 //
 // Bound by latency: partials of 32 requests 5.4 us alone, of one request of 128K tokens
-// (some 152 partials a row) 8.9; with the record of 32 ragged requests of up to 8192 tokens
+// (some 152 partials a row) 8.4; with the record of 32 ragged requests of up to 8192 tokens
 // (35 MB, most of it in L2) 17 us.
 template <bool kWarpRows, bool kRecord>
 __global__ void __launch_bounds__(kThreads, 2)

@@ -26,7 +26,7 @@ __device__ __forceinline__ int scored_len(const ScoredArgs& a, int s) {
 }
 
 struct KeyRange {
-  int lo, hi;                // keys [lo, hi); hi <= lo: none
+  int lo, hi;                // keys [lo, hi); lo = hi: none
 };
 
 __device__ __forceinline__ KeyRange key_range(const ScoredArgs& a, int s, int n, int i) {
@@ -36,7 +36,7 @@ __device__ __forceinline__ KeyRange key_range(const ScoredArgs& a, int s, int n,
   if (a.doc_starts) lo = max(lo, a.doc_starts[(size_t)s * a.q_len + i]);
   int hi = p + 1;
   if (a.prefix_lens) hi = max(hi, min(a.prefix_lens[s], n));
-  return {lo, hi};
+  return {min(lo, hi), hi};                  // (a document may start at any number)
 }
 
 // The tokens [lo, hi) the scored decode reads of a sequence: from the block of the first key

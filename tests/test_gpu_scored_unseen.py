@@ -45,17 +45,19 @@ def hide_unseen(case, **rules):
         prefix = rules["prefix"][b] if rules.get("prefix") else 0
         for lo, hi in case.ranges(b, rules.get("window", 0), prefix, rules.get("docs")):
             seen.update(range(max(lo, 0), hi))
-        for j in range(n):
-            if j not in seen:
-                case.hide(b, j, j + 1)
+        table = case.tables[b].tolist()
+        at = [(table[j // case.bs], j % case.bs) for j in range(n) if j not in seen]
+        if at:
+            at = torch.tensor(at, device="cuda")
+            case.pool[at[:, 0], :, case.layer, :, at[:, 1]] = case.nan
         blocks = {j // case.bs for j in seen}
-        for j in range(-(-n // case.bs)):
-            if j not in blocks:
-                block = int(case.tables[b, j])
-                if case.block_scales is not None:
-                    case.block_scales[block, 0] = float("nan")
-                    case.block_scales[block, 1] = 1e30
-                case.tables[b, j] = -1
+        stale = [j for j in range(-(-n // case.bs)) if j not in blocks]
+        if stale:
+            if case.block_scales is not None:
+                unseen = torch.tensor([table[j] for j in stale], device="cuda")
+                case.block_scales[unseen, 0] = float("nan")
+                case.block_scales[unseen, 1] = 1e30
+            case.tables[b, torch.tensor(stale, device="cuda")] = -1
 
 
 RULES = {"docs": {}, "cap": dict(cap=9.0), "slopes": dict(cap=12.0, slopes=True),
@@ -104,3 +106,21 @@ def test_drafts(kv, hq, hkv, bs, q_len, rules, kind):
     for b, n in enumerate(lens):                           # columns behind the sequence
         assert (w[b, :, n:] == -5.0).all()
     case.check(run(case, torch.float32, **r), want)
+
+
+@pytest.mark.parametrize("kv,hq,rules,kind", [
+    ("bf16", 16, "cap", "between"), ("bf16", 16, "prefix", "any"), ("f16", 16, "docs", "any"),
+    ("e4m3", 16, "docs", "between"), ("e4m3", 16, "cap", "any"), ("scaled", 16, "docs", "any")])
+def test_many_items(kv, hq, rules, kind):
+    # more pairs of query tiles than multiprocessors: gaps of one item beside the next one's
+    lens = [0, 70, 1, 200, 69, 333, 64, 71, 128, 30, 0, 500, 70, 3, 65, 448, 99, 0, 150, 321, 7, 70,
+            641, 12, 192, 90, 35, 256, 77, 400, 129, 100, 110, 300, 44, 59]
+    case = Case(lens, hq, 4, 128, "e4m3" if kv == "scaled" else kv, 16, 70, seed=33,
+                block_scales=kv == "scaled")
+    r = rules_of(case, kind, rules, seed=hq)
+    want = case.reference(**r)
+    hide_unseen(case, **r)
+    got = run(case, torch.float32, **r)
+    case.check(got, want)
+    for _ in range(5):                                     # the same bits, whoever is late
+        assert torch.equal(run(case, torch.float32, **r), got)

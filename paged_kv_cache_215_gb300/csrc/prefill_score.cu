@@ -20,7 +20,7 @@
 //
 // Measured, a call: 2 x 2048 bf16 tokens over 8192 in documents, capped, 148 us; 4 x 2048
 // tokens over 16384 E4M3 ones in a window of 4096, 553 us; 3 prompts of 1001 f16 tokens, 64
-// heads on 8, that see a prefix, 82 us (a CTA for each item took 181, 569 and 110 us where
+// heads on 8, that see a prefix, 83 us (a CTA for each item took 181, 569 and 110 us where
 // these took 172, 560 and 81).  Of the cycles between two items' key tiles some 4000 are the
 // wait for Q, 3500 the output's stores.  A key tile takes 1700 cycles (f16) and 2100 (E4M3: the
 // converters share the issue slots); its matrix products alone would take 1100 (1650 with P's
@@ -53,7 +53,7 @@ constexpr float kTiny = 0x1p-126f;           // in the place of a scale of 0: -i
 // memory's lanes, and the two warps vote on every tile whether a score passes the row's
 // reference.  One and two threads a row, us: capped documents bf16 169 and 148, f16 153 and
 // 148, E4M3 208 and 178; without a cap windows bf16 625 and 646, E4M3 553 and 625, an f16
-// prompt 82 and 88, distances bf16 169 and 180.  The softmax warps take registers that the
+// prompt 83 and 88, distances bf16 167 and 180.  The softmax warps take registers that the
 // others do not need (setmaxnreg, by warpgroups).
 template <int KVT, int kRules>
 struct Roles {
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(Roles<KVT, kRules>::kThreads, 1)
   // and 2^-24 or more for the largest, so that O is hardly ever rescaled (capped documents
   // with a slack of 8, 16, 24, 32, 60: 165, 159, 150, 146, 145 us; keys of four times the
   // usual size have a warp do it every fourth tile at 8; with distances, whose scores climb
-  // from tile to tile, documents take 169 us, with a slack of 60 164); in f16 2^15 at most,
+  // from tile to tile, documents take 167 us, with a slack of 60 some 5 less); in f16 2^15 at most,
   // and weights down to 2^-21 of the largest keep every bit (a slack of 12 with 2^-17 saved
   // 1% and added a quarter to an f16 output's error).
   constexpr float kSlack = kSplitP ? 32.f : 8.f, kPOff = kSplitP ? 8.f - kSlack : 7.f;

@@ -26,17 +26,18 @@ __device__ __forceinline__ int scored_len(const ScoredArgs& a, int s) {
 }
 
 struct KeyRange {
-  int lo, hi;                // keys [lo, hi); lo = hi: none
+  int lo, hi;                // keys [lo, hi), both in [0, n]; hi <= lo: none
 };
 
 __device__ __forceinline__ KeyRange key_range(const ScoredArgs& a, int s, int n, int i) {
   const int p = n - a.q_len + i;
   if (p < 0) return {0, 0};
   int lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
-  if (a.doc_starts) lo = max(lo, a.doc_starts[(size_t)s * a.q_len + i]);
+  // (a document may start at any number)
+  if (a.doc_starts) lo = max(lo, min(a.doc_starts[(size_t)s * a.q_len + i], n));
   int hi = p + 1;
   if (a.prefix_lens) hi = max(hi, min(a.prefix_lens[s], n));
-  return {min(lo, hi), hi};                  // (a document may start at any number)
+  return {lo, hi};
 }
 
 // The tokens [lo, hi) the scored decode reads of a sequence: from the block of the first key
